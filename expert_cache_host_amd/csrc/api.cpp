@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "../../include/moe_cache.h"
+#include "errors.hpp"
 #include "host_expert.hpp"
 #include "host_routing.hpp"
 #include "kernels.hpp"
@@ -918,6 +919,21 @@ moe_status guarded(moe_cache *c, F &&f) {
 }
 
 }  // namespace
+
+namespace moe {
+
+void clear_error() { g_err.clear(); }
+
+moe_status set_error(moe_status st, const char *msg) {
+  try {
+    g_err = msg;
+  } catch (...) {
+    g_err.clear();
+  }
+  return st;
+}
+
+}  // namespace moe
 
 extern "C" {
 

@@ -1,0 +1,360 @@
+"""ctypes binding of the decoder-layer operators (argument marshalling only).
+
+block_norm, q4_matvec over a Q4Matrix, and KVCache.append / attend / read: what a
+decoder layer needs around the routed MoE layer.  The formulas and layouts are
+set out in include/moe_cache.h.  Tensors are torch tensors on one GPU; calls go
+to the given stream, or to the current stream of that GPU.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import numpy as np
+import torch
+
+from .binding import _check, load_library
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + \
+               [(n, ctypes.c_int32) for n in ("n_pages", "page_tokens", "kv_heads", "head_dim")]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pages", "start", "past")] + \
+               [(n, ctypes.c_int32) for n in ("n_seqs", "max_pages", "n_rows")]
+
+
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = load_library()
+        P, I32, I64, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        C, B = ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
+        sig = {
+            "moe_block_norm": (I32, [P, I32, I64, P, I32, I64, P, P, I32, I64, P, I32, I32, F, F, F,
+                                     P, I64, P, I32, I64, P]),
+            "moe_q4_matvec": (I32, [P, P, I32, I32, I32, P, I32, I64, I32, P, I64, P]),
+            "moe_kv_append": (I32, [C, B, I32, P, I64, P, I64, P, I32, I32, P, I64, I32, P, I64, P]),
+            "moe_kv_read": (I32, [C, B, P, P, P]),
+            "moe_kv_attend_workspace": (I64, [C, B, I32, I32, I32]),
+            "moe_kv_attend": (I32, [C, B, I32, P, I64, I32, F, I32, P, I64, P, I64, P]),
+        }
+        for name, (res, args) in sig.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+class _on:
+    """Makes `device` and the call's stream current (so that what the call allocates
+    belongs to that stream) and yields the raw stream."""
+
+    def __init__(self, device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
+
+
+def _rows(t, name, device, d=None, dtype=None):
+    """Checks a [rows, d] tensor with contiguous rows; returns its row stride."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2 or (d is not None and t.shape[1] != d):
+        raise ValueError(f"{name} must be [rows, {'d' if d is None else d}]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    if dtype is None:
+        if t.dtype not in _TYPES:
+            raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    return t.stride(0)
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return t.device
+
+
+def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: float = 1.0,
+               block_scale: float = 1.0, eps: float = 1e-6, h_out=None, x_out=None,
+               x_dtype: Optional[torch.dtype] = None, stream=None):
+    """(h', x): a block's residual update and the norm before the next block.
+
+        n  = y / sqrt(mean(y^2) + eps) * post_w        (post_w None: n = y)
+        h' = res_scale * h + block_scale * gate * n    (y None: res_scale * h)
+        x  = h' / sqrt(mean(h'^2) + eps) * pre_w       (pre_w None: x is None)
+
+    h [T, d], y [T, d], gate [d] or [T, d], post_w and pre_w float32 [d].  h' has h's
+    type, x `x_dtype` (default: y's type, else h's).  h_out may be h, x_out may be y.
+    With y None and res_scale 1, h' is h itself, returned without a copy unless
+    h_out is given.
+    """
+    dev = _cuda(h, "h")
+    ldh = _rows(h, "h", dev)
+    T, d = h.shape
+    if y is None and (post_w is not None or gate is not None):
+        raise ValueError("post_w and gate need y")
+    ldy = yt = ldg = gt = 0
+    if y is not None:
+        ldy = _rows(y, "y", dev, d)
+        yt = _TYPES[y.dtype]
+        if y.shape[0] != T:
+            raise ValueError("y must have h's rows")
+    if gate is not None:
+        if gate.dim() == 1:
+            ldg = _rows(gate.unsqueeze(0), "gate", dev, d) * 0
+        else:
+            ldg = _rows(gate, "gate", dev, d)
+            if gate.shape[0] != T:
+                raise ValueError("gate must be [d] or have h's rows")
+        gt = _TYPES[gate.dtype]
+    for w, name in ((post_w, "post_w"), (pre_w, "pre_w")):
+        if w is not None and (w.device != dev or w.dtype != torch.float32 or w.dim() != 1 or
+                              w.shape[0] != d or not w.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous float32 [d] on {dev}")
+    if x_out is not None and pre_w is None:
+        raise ValueError("x_out needs pre_w")
+    keep = y is None and res_scale == 1.0 and h_out is None
+    if keep and pre_w is None:
+        raise ValueError("nothing to compute: y and pre_w are None")
+    with _on(dev, stream) as s:
+        if h_out is None:
+            if not keep:
+                h_out = torch.empty((T, d), dtype=h.dtype, device=dev)
+        elif h_out.shape[0] != T:
+            raise ValueError("h_out must have h's shape")
+        x = x_out
+        if pre_w is not None and x is None:
+            x = torch.empty((T, d), device=dev, dtype=x_dtype or (h if y is None else y).dtype)
+        ldx = xt = ldho = 0
+        if x is not None:
+            ldx = _rows(x, "x_out", dev, d, x_dtype)
+            xt = _TYPES[x.dtype]
+            if x.shape[0] != T:
+                raise ValueError("x_out must have h's shape")
+        if h_out is not None:
+            ldho = _rows(h_out, "h_out", dev, d, h.dtype)
+        _check(_library().moe_block_norm(
+            h.data_ptr(), _TYPES[h.dtype], ldh, None if y is None else y.data_ptr(), yt, ldy,
+            None if post_w is None else post_w.data_ptr(), None if gate is None else gate.data_ptr(),
+            gt, ldg, None if pre_w is None else pre_w.data_ptr(), T, d, res_scale, block_scale, eps,
+            None if h_out is None else h_out.data_ptr(), ldho, None if x is None else x.data_ptr(), xt,
+            ldx, s))
+    return (h if keep else h_out), x
+
+
+class Q4Matrix:
+    """A matrix [rows, cols] in 4 bits on the GPU: codes uint8 [rows, cols / 32, 16] and
+    scales float16 [rows, cols / group] (both contiguous, kept, not copied)."""
+
+    def __init__(self, codes, scales):
+        dev = _cuda(codes, "codes")
+        if codes.dtype != torch.uint8 or codes.dim() != 3 or codes.shape[2] != 16 or \
+                not codes.is_contiguous():
+            raise ValueError("codes must be contiguous uint8 [rows, cols / 32, 16]")
+        self.rows, self.cols = codes.shape[0], codes.shape[1] * 32
+        if scales.device != dev or scales.dtype != torch.float16 or scales.dim() != 2 or \
+                scales.shape[0] != self.rows or not scales.is_contiguous():
+            raise ValueError("scales must be contiguous float16 [rows, cols / group] beside the codes")
+        if self.rows < 1 or scales.shape[1] < 1 or \
+                scales.shape[1] * (g := self.cols // scales.shape[1]) != self.cols or g not in (32, 64, 128):
+            raise ValueError("scales must hold one scale per 32, 64 or 128 weights")
+        self.group = g
+        self.codes, self.scales, self.device = codes, scales, dev
+        self._head = (codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, g)
+
+    @classmethod
+    def from_blocks(cls, blocks, rows: int, cols: int, group: int = 32, device="cuda"):
+        """From host bytes in the interchange layout: per group of a row a binary16 scale,
+        then the nibble bytes of its blocks of 32 (group 32 is Q4_0)."""
+        if group not in (32, 64, 128) or rows < 1 or cols < group or cols % group:
+            raise ValueError("cols must be a multiple of group (32, 64 or 128)")
+        b = np.ascontiguousarray(blocks, dtype=np.uint8).reshape(-1)
+        n = 2 + group // 2
+        if b.size != rows * (cols // group) * n:
+            raise ValueError(f"blocks holds {b.size} bytes, {rows * (cols // group) * n} needed")
+        b = b.reshape(rows, cols // group, n)
+        scales = np.ascontiguousarray(b[:, :, :2]).view(np.float16).reshape(rows, cols // group)
+        codes = np.ascontiguousarray(b[:, :, 2:]).reshape(rows, cols // 32, 16)
+        return cls(torch.from_numpy(codes).to(device), torch.from_numpy(scales.copy()).to(device))
+
+
+def q4_matvec(x, w: Q4Matrix, out=None, stream=None):
+    """out [T, rows] = x [T, cols] times w transposed, in x's type (float32 sums)."""
+    dev = w.device
+    ldx = _rows(x, "x", dev, w.cols)
+    T = x.shape[0]
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty((T, w.rows), dtype=x.dtype, device=dev)
+            ldo = w.rows
+        else:
+            ldo = _rows(out, "out", dev, w.rows, x.dtype)
+            if out.shape[0] != T:
+                raise ValueError("out must have x's rows")
+        _check(_library().moe_q4_matvec(*w._head, x.data_ptr(), _TYPES[x.dtype], ldx, T, out.data_ptr(),
+                                        ldo, s))
+    return out
+
+
+class KVCache:
+    """A paged cache of keys and values in 4 bits over the caller's four tensors:
+
+        k_codes  uint8   [n_pages, kv_heads, page_tokens, head_dim / 32, 16]
+        k_scales float16 [n_pages, kv_heads, page_tokens, head_dim / 32]
+        v_codes  uint8   [n_pages, kv_heads, page_tokens, 16, head_dim / 32]
+        v_scales float16 [n_pages, kv_heads, page_tokens, head_dim / 32]
+
+    A batch is given by pages int32 [n_seqs, max_pages], start int32 [n_seqs + 1] and
+    past int32 [n_seqs]: rows start[s] .. start[s+1]-1 of the tensors are sequence s's
+    new tokens, at positions past[s], past[s] + 1, ...
+    """
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales):
+        dev = _cuda(k_codes, "k_codes")
+        if k_codes.dim() != 5 or k_codes.shape[4] != 16:
+            raise ValueError("k_codes must be [n_pages, kv_heads, page_tokens, head_dim / 32, 16]")
+        n, h, p, nb = (int(v) for v in k_codes.shape[:4])
+        want = {"k_codes": (k_codes, torch.uint8, (n, h, p, nb, 16)),
+                "k_scales": (k_scales, torch.float16, (n, h, p, nb)),
+                "v_codes": (v_codes, torch.uint8, (n, h, p, 16, nb)),
+                "v_scales": (v_scales, torch.float16, (n, h, p, nb))}
+        for name, (t, dtype, shape) in want.items():
+            if t.device != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+        if n < 1 or h < 1 or h > 1024 or p < 16 or p % 16 or p > 65536 or nb not in (2, 4, 8):
+            raise ValueError("head_dim must be 64, 128 or 256, page_tokens a multiple of 16 up to 65536, "
+                             "kv_heads at most 1024")
+        self.device, self.tensors = dev, (k_codes, k_scales, v_codes, v_scales)
+        self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = n, h, p, nb * 32
+        self._c = _KvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                           v_scales.data_ptr(), n, p, h, nb * 32)
+        self._cp = ctypes.pointer(self._c)
+
+    @classmethod
+    def create(cls, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+        """A cache over new tensors (zeroed)."""
+        shape, nb = (n_pages, kv_heads, page_tokens), head_dim // 32
+        if head_dim not in (64, 128, 256):
+            raise ValueError("head_dim must be 64, 128 or 256")
+        z = lambda s, t: torch.zeros(shape + s, dtype=t, device=device)  # noqa: E731
+        return cls(z((nb, 16), torch.uint8), z((nb,), torch.float16), z((16, nb), torch.uint8),
+                   z((nb,), torch.float16))
+
+    def _batch(self, pages, start, past, rows):
+        dev = self.device
+        for t, name in ((pages, "pages"), (start, "start"), (past, "past")):
+            if t.device != dev or t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 on {dev}")
+        if pages.dim() != 2 or start.dim() != 1 or past.dim() != 1:
+            raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1], past [n_seqs]")
+        n, m = pages.shape
+        if n < 1 or m < 1 or start.shape[0] != n + 1 or past.shape[0] != n:
+            raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1], past [n_seqs]")
+        return _KvBatch(pages.data_ptr(), start.data_ptr(), past.data_ptr(), n, m, rows)
+
+    def append(self, k, v, pages, start, past, q=None, inv_freq=None, interleaved: bool = False,
+               q_out=None, stream=None):
+        """Writes k, v [T, kv_heads * head_dim] into the cache, the keys rotated by their
+        positions (inv_freq float32 [rot_dim / 2] or None); returns q [T, q_heads * head_dim]
+        rotated likewise, or None."""
+        dev, D = self.device, self.head_dim
+        ldk = _rows(k, "k", dev, self.kv_heads * D)
+        T, dt = k.shape[0], k.dtype
+        ldv = _rows(v, "v", dev, self.kv_heads * D, dt)
+        if v.shape[0] != T:
+            raise ValueError("v must have k's rows")
+        rot = 0
+        if inv_freq is not None:
+            rot = 2 * inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+            if rot < 0 or rot > D or inv_freq.dtype != torch.float32 or inv_freq.device != dev or \
+                    not inv_freq.is_contiguous():
+                raise ValueError(f"inv_freq must be contiguous float32 [rot_dim / 2] on {dev}, rot_dim <= head_dim")
+        b = self._batch(pages, start, past, T)
+        ldq = ldqo = heads = 0
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out needs q")
+        else:
+            ldq = _rows(q, "q", dev, None, dt)
+            heads = self._heads(q, T)
+        with _on(dev, stream) as s:
+            if q is not None:
+                if q_out is None:
+                    q_out = torch.empty((T, heads * D), dtype=dt, device=dev)
+                ldqo = _rows(q_out, "q_out", dev, heads * D, dt)
+                if q_out.shape[0] != T:
+                    raise ValueError("q_out must have q's rows")
+            _check(_library().moe_kv_append(
+                self._cp, b, _TYPES[dt], k.data_ptr(), ldk, v.data_ptr(), ldv,
+                inv_freq.data_ptr() if rot else None, rot, 1 if interleaved else 0,
+                None if q is None else q.data_ptr(), ldq, heads,
+                None if q is None else q_out.data_ptr(), ldqo, s))
+        return q_out
+
+    def _heads(self, q, T) -> int:
+        n, D = q.shape[1], self.head_dim
+        if q.shape[0] != T or n < 1 or n % (self.kv_heads * D):
+            raise ValueError("q must be [T, q_heads * head_dim], q_heads a multiple of kv_heads")
+        return n // D
+
+    def read(self, pages, start, past, rows: int, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """(k, v) float32 [rows, kv_heads, head_dim]: the values the cache holds for the
+        batch's rows (0 in a hole; undefined for rows of no sequence)."""
+        b = self._batch(pages, start, past, rows)
+        if rows < 0:
+            raise ValueError("rows must be >= 0")
+        with _on(self.device, stream) as s:
+            k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
+            v = torch.empty_like(k)
+            _check(_library().moe_kv_read(self._cp, b, k.data_ptr(), v.data_ptr(), s))
+        return k, v
+
+    def attend(self, q, pages, start, past, scale: float, window: int = 0, out=None, stream=None):
+        """out [T, q_heads * head_dim] = softmax(scale * q K^T) V over the keys each row
+        sees: positions up to its own, within `window` when window > 0.  Rows of no sequence
+        are left as they are in `out` (undefined in a new one)."""
+        dev, D = self.device, self.head_dim
+        ldq = _rows(q, "q", dev)
+        T = q.shape[0]
+        heads = self._heads(q, T)
+        b = self._batch(pages, start, past, T)
+        lib, ty = _library(), _TYPES[q.dtype]
+        with _on(dev, stream) as s:
+            if out is None:
+                out = torch.empty((T, heads * D), dtype=q.dtype, device=dev)
+            ldo = _rows(out, "out", dev, heads * D, q.dtype)
+            if out.shape[0] != T:
+                raise ValueError("out must have q's rows")
+            n = lib.moe_kv_attend_workspace(self._cp, b, ty, heads, window)
+            if n < 0:
+                _check(n)
+            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+            _check(lib.moe_kv_attend(self._cp, b, ty, q.data_ptr(), ldq, heads, scale, window,
+                                     out.data_ptr(), ldo, None if ws is None else ws.data_ptr(), n, s))
+        return out

@@ -426,6 +426,145 @@ moe_status moe_host_topk(const float *z, int32_t n_tokens, int32_t n_experts, in
 moe_status moe_host_expert_forward(const void *expert_q4, int32_t d_model, int32_t d_ff,
                                    const float *x, int32_t n_tokens, float *y, int32_t threads);
 
+/* ---- operators of the decoder layer around the MoE layer ----
+ *
+ * What a decoder layer needs next to its routed MoE block: the norms before and
+ * after a block, the projections, and attention with its cache, over the same
+ * 4-bit blocks the experts are held in.  These calls hold no state: they work on
+ * the caller's device memory, enqueue their kernels on `stream` and return
+ * without waiting; they allocate nothing, may be captured into a HIP graph and
+ * may be called from several threads and streams at once.  The current HIP
+ * device must be the one that owns the memory.  Strides count elements; within
+ * a row elements are contiguous.  Output memory must not overlap an input,
+ * except where stated.  A call with no tokens writes nothing and succeeds. */
+
+/* Element types. */
+#define MOE_F32 0
+#define MOE_BF16 1
+#define MOE_F16 2
+
+#define MOE_NORM_MAX_D 32768
+#define MOE_Q4_MAX_TOKENS 65536
+#define MOE_KV_MAX_PAGE_TOKENS 65536
+#define MOE_KV_MAX_HEADS 1024
+
+/* moe_block_norm -- a block's residual update and the norm before the next one:
+ *
+ *     n  = y / sqrt(mean(y^2) + eps) * post_w       (post_w NULL: n = y)
+ *     h' = res_scale * h + block_scale * gate * n   (gate NULL: 1)
+ *     x  = h' / sqrt(mean(h'^2) + eps) * pre_w
+ *
+ *   h           [n_tokens][d] of h_type: the residual stream
+ *   y           [n_tokens][d] of y_type: the block's output; NULL: h' = res_scale * h
+ *               (post_w and gate must then be NULL)
+ *   gate        of gate_type: one row for every token (gate_stride = 0) or a row
+ *               per token; NULL: no gate
+ *   post_w, pre_w  float32 [d] or NULL
+ *   h_out       [n_tokens][d] of h_type, or NULL when h' is not wanted; may be h
+ *               (same stride)
+ *   x           [n_tokens][d] of x_type, given exactly when pre_w is; may be y
+ *               (same type and stride), e.g. the x that moe_layer_forward takes
+ *
+ * Sums and products are float32; x is formed from h' before h' is rounded to
+ * its type.  1 <= d <= MOE_NORM_MAX_D. */
+moe_status moe_block_norm(const void *h, int32_t h_type, int64_t h_stride, const void *y,
+                          int32_t y_type, int64_t y_stride, const float *post_w, const void *gate,
+                          int32_t gate_type, int64_t gate_stride, const float *pre_w,
+                          int32_t n_tokens, int32_t d, float res_scale, float block_scale,
+                          float eps, void *h_out, int64_t h_out_stride, void *x, int32_t x_type,
+                          int64_t x_stride, moe_stream_t stream);
+
+/* moe_q4_matvec -- out[t][r] = sum_c w[r][c] x[t][c] for a matrix held in 4 bits,
+ * w = scale * (code - 8), one binary16 scale per `group` weights of a row.
+ *
+ *   codes   [rows][cols / 32][16] bytes, 16-byte aligned: byte j of a block of 32
+ *           holds element j in the low nibble and j + 16 in the high one (the
+ *           nibbles of the interchange layout without the scales between them)
+ *   scales  binary16 [rows][cols / group]; group 32 (Q4_0), 64 or 128
+ *   x, out  [n_tokens][cols] and [n_tokens][rows] of `type`
+ *
+ * Meant for the few tokens of decode (weights are read once for up to 8 float32
+ * or 16 half-width tokens); n_tokens <= MOE_Q4_MAX_TOKENS.  Sums are float32.
+ * cols must be a multiple of group. */
+moe_status moe_q4_matvec(const void *codes, const void *scales, int32_t rows, int32_t cols,
+                         int32_t group, const void *x, int32_t type, int64_t x_stride,
+                         int32_t n_tokens, void *out, int64_t out_stride, moe_stream_t stream);
+
+/* A paged cache of keys and values in 4 bits, in the caller's device memory
+ * (each pointer 16-byte aligned).  nb = head_dim / 32:
+ *   k_codes  bytes [n_pages][kv_heads][page_tokens][nb][16]
+ *   v_codes  bytes [n_pages][kv_heads][page_tokens][16][nb]
+ *   k_scales, v_scales  binary16 [n_pages][kv_heads][page_tokens][nb]
+ * Byte j of a block of 32 elements holds element j in the low nibble and j + 16
+ * in the high one; an element is scale * (code - 8).  head_dim is 64, 128 or
+ * 256; page_tokens a multiple of 16. */
+typedef struct moe_kv_cache {
+  void *k_codes, *k_scales, *v_codes, *v_scales;
+  int32_t n_pages, page_tokens, kv_heads, head_dim;
+} moe_kv_cache;
+
+/* A packed batch (device pointers): rows start[s] .. start[s + 1] - 1 are
+ * sequence s's new tokens, at positions past[s], past[s] + 1, ...; position p lies
+ * on page pages[s][p / page_tokens].  start holds n_seqs + 1 ascending entries;
+ * rows outside [start[0], start[n_seqs]) belong to no sequence: they are neither
+ * read nor written.  A page outside [0, n_pages), a position past the table and a
+ * negative past are holes: nothing is written there and no key is seen there. */
+typedef struct moe_kv_batch {
+  const int32_t *pages; /* [n_seqs][max_pages] */
+  const int32_t *start; /* [n_seqs + 1] */
+  const int32_t *past;  /* [n_seqs] */
+  int32_t n_seqs, max_pages;
+  int32_t n_rows; /* rows of the tensors given with the batch */
+} moe_kv_batch;
+
+/* moe_kv_append -- writes the new tokens' keys and values into the cache, keys
+ * (and queries, when given) rotated by their positions.
+ *
+ *   k, v       [n_rows][kv_heads][head_dim] of `type`, row strides k_stride, v_stride
+ *   inv_freq   float32 [rot_dim / 2]; pair j of a head is turned by position *
+ *              inv_freq[j].  rot_dim 0: no rotation; below head_dim: the rest of the
+ *              head is left as it is
+ *   interleaved  0: pair j is elements (j, j + rot_dim / 2); 1: (2j, 2j + 1)
+ *   q, q_out   [n_rows][q_heads][head_dim] of `type`, or both NULL
+ *
+ * Angles, sines, cosines and the rotation are computed in binary64 and the result
+ * rounded to float32 before it is coded.  Per block of 32: m = the first element
+ * of largest magnitude, scale = binary16(m / -8) (saturating at +-65504), code =
+ * clamp(floor(x / scale + 8.5), 0, 15), decided exactly; a zero scale gives code 8.
+ * A NaN is stored as 0 and an infinity as the largest value of its sign, so that
+ * the cache holds finite numbers only.
+ * A place must not be written by two sequences of one call (a page that stands
+ * twice in the tables under new tokens): what it then holds is some mixture. */
+moe_status moe_kv_append(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
+                         const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                         const float *inv_freq, int32_t rot_dim, int32_t interleaved,
+                         const void *q, int64_t q_stride, int32_t q_heads, void *q_out,
+                         int64_t q_out_stride, moe_stream_t stream);
+
+/* moe_kv_read -- the values the cache holds for the batch's rows (positions
+ * past[s] + i), float32 [n_rows][kv_heads][head_dim] each; 0 for a hole.  For
+ * moving a sequence out of the cache and for inspection. */
+moe_status moe_kv_read(const moe_kv_cache *cache, const moe_kv_batch *batch, float *k, float *v,
+                       moe_stream_t stream);
+
+/* moe_kv_attend -- out = softmax(scale * q K^T) V for the batch's rows over the
+ * cache: a row at position p sees the keys at positions <= p (> p - window when
+ * window > 0) that do not lie in a hole; a row that sees none gets 0.  The
+ * new tokens' own keys are read from the cache: append them first.
+ *
+ *   q, out   [n_rows][q_heads][head_dim] of `type`; query head i reads KV head
+ *            i / (q_heads / kv_heads)
+ *   workspace  device memory of moe_kv_attend_workspace bytes (same arguments),
+ *            16-byte aligned, for this call alone until its work is done
+ *
+ * Scores, softmax statistics and sums are float32. */
+int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
+                                int32_t q_heads, int32_t window);
+moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
+                         const void *q, int64_t q_stride, int32_t q_heads, float scale,
+                         int32_t window, void *out, int64_t out_stride, void *workspace,
+                         int64_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
