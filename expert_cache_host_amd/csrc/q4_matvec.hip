@@ -2,45 +2,290 @@
 //
 //   out[t][r] = sum_g s[r][g] * sum_{c in group g} (q[r][c] - 8) * x[t][c]
 //
-// One wave per output row and token; a lane takes every 64th block of 32
-// weights.  Codes are exact small integers, products and sums in float32.
+// Bound by reading the weights (0.56 bytes each at group 32).  On the vector
+// units a weight would cost one fused multiply-add per token beside its
+// decoding, more than the memory rate leaves room for; so the products go to
+// the matrix cores: B = 16 rows' codes of a block (exact binary16 integers), A =
+// the tokens as binary16 rows.  A float32 token takes two rows (hi and lo part,
+// 22 bits), a half-width one takes one; the power of two that brings a token's
+// largest element of a wave's K slice to [2^13, 2^14) keeps the precision
+// independent of the input's magnitude.  Each group's sum is exact to float32
+// and its scale is applied in float32.
+//
+// A workgroup owns all of K: wave w holds the tokens' slice of KT chunks of 128
+// columns in registers for the whole launch and streams its slice of 16 rows
+// after 16 rows, the next tile's loads in flight while the present one is
+// multiplied; the waves' sums meet in LDS, a barrier per tile.
 #include "device_types.hpp"
+#include "q4_tile.hpp"
 
 namespace moe {
 
 namespace {
 
-__global__ __launch_bounds__(256) void q4_matvec_kernel(Q4MatvecArgs a) {
-  const int lane = threadIdx.x & 63;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const long long t = blockIdx.y;
-  if (row >= a.rows) return;
-  const int nb = a.cols / 32, per = a.group / 32;
-  float acc = 0.f;
-  for (int b = lane; b < nb; b += 64) {
-    const uint4 w = *(const uint4 *)(a.q + (row * nb + b) * 16);
-    const float s = f16_to_f32(a.scales[row * (nb / per) + b / per]);
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint32_t byte = ws[j / 4] >> (8 * (j % 4));
-      sum = fmaf((float)(int)(byte & 15u) - 8.f, load1(a.x, a.type, t * a.ldx + b * 32 + j), sum);
-      sum = fmaf((float)(int)((byte >> 4) & 15u) - 8.f,
-                 load1(a.x, a.type, t * a.ldx + b * 32 + 16 + j), sum);
+constexpr int kMaxWaves = 16;
+
+// Row of A that token part u = t * PL + p takes: parts 0..3 in the first C
+// register of the four lane rows, 4..7 in the second, and so on, so that few
+// tokens need few scaled adds.
+__device__ __forceinline__ int part_of_row(int m) { return 4 * (m & 3) + (m >> 2); }
+
+// PL: binary16 parts per token; KT: chunks of 4 blocks per wave and pass; FI: C
+// registers in use (4 FI parts).
+template <int PL, int KT, int FI>
+struct Matvec {
+  const Q4MatvecArgs &a;
+  const int lane, n, g, wave, waves, nb, t0, parts;
+  const bool aligned;  // x's rows allow loads of four elements
+  half8_t X[KT * 4];  // the lane's part, 8 K slots of every block
+  float xs[FI];       // 2^e of the parts in this lane's C registers
+
+  __device__ Matvec(const Q4MatvecArgs &args, int first_token, bool al)
+      : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), wave(threadIdx.x >> 6),
+        waves(blockDim.x >> 6), nb(args.cols / 32), t0(first_token),
+        parts(min(args.T - first_token, 4 * FI / PL) * PL), aligned(al) {}
+
+  // Word gg of a block of token t, in the codes' order.
+  __device__ __forceinline__ void load_unit(int t, int block, int gg, float (&v)[8]) const {
+    const long long i = (long long)t * a.ldx + block * 32 + 4 * gg;
+    float4 p, q;
+    if (aligned) {
+      p = load4(a.x, a.type, i);
+      q = load4(a.x, a.type, i + 16);
+    } else {
+      p = make_float4(load1(a.x, a.type, i), load1(a.x, a.type, i + 1), load1(a.x, a.type, i + 2),
+                      load1(a.x, a.type, i + 3));
+      q = make_float4(load1(a.x, a.type, i + 16), load1(a.x, a.type, i + 17),
+                      load1(a.x, a.type, i + 18), load1(a.x, a.type, i + 19));
     }
-    acc = fmaf(s, sum, acc);
+    unit_order(p, q, v);
   }
+
+  // The wave's K slice of every token into X and xs; `first` is its first block.
+  // Many parts: every lane converts the units of its own row of A.  The slice is
+  // read twice (its largest element, then the parts), which holds no more
+  // registers than X.
+  __device__ __forceinline__ void stage_many(int first) {
+    const int u = part_of_row(n), t = t0 + u / PL, p = u % PL;
+    const bool mine = u < parts;
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int b = 0; b < KT * 4; ++b) {
+      float v[8] = {};
+      if (mine && first + b < nb) load_unit(t, first + b, g, v);
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) acc += __shfl_xor(acc, m);
-  if (lane == 0) store1(a.out, a.type, t * a.ldo + row, acc);
+      for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+    }
+    const int e = scale_exp(rows_max_u32(top));
+    const float f = exp2_int(-e);
+#pragma unroll
+    for (int b = 0; b < KT * 4; ++b) {
+      float v[8] = {};
+      if (mine && first + b < nb) load_unit(t, first + b, g, v);
+      _Float16 hi[8], lo[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) split_half(v[j] * f, hi[j], lo[j]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) X[b][j] = PL == 2 && p == 1 ? lo[j] : hi[j];
+    }
+    // part 4 i + g stands in row 4 g + i of A, so lane n = 4 g + i knows its exponent
+#pragma unroll
+    for (int i = 0; i < FI; ++i) xs[i] = exp2_int(__shfl(e, 4 * g + i));
+  }
+
+  // Up to four parts: a lane converts one unit (word g' of block b') of each
+  // token, and the wave shares them through its own LDS, where a lane then reads
+  // the units of its row of A.
+  __device__ __forceinline__ void stage_few(int first, uint4 (*buf)[KT * 16 + 4]) {
+    const int b = lane >> 2, u = part_of_row(n);
+    xs[0] = 1.f;
+#pragma unroll
+    for (int t = 0; t < 4 / PL; ++t) {
+      if (t * PL >= parts) break;
+      float v[8] = {};
+      if (b < KT * 4 && first + b < nb) load_unit(t0 + t, first + b, lane & 3, v);
+      uint32_t top = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
+      const int e = scale_exp(wave_max_u32(top));
+      const float f = exp2_int(-e);
+      half8_t hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        _Float16 x, y;
+        split_half(v[j] * f, x, y);
+        hi[j] = x, lo[j] = y;
+      }
+      if (b < KT * 4) {
+        buf[t * PL][lane] = __builtin_bit_cast(uint4, hi);
+        if constexpr (PL == 2) buf[t * PL + 1][lane] = __builtin_bit_cast(uint4, lo);
+      }
+      if (g / PL == t) xs[0] = exp2_int(e);  // C's one register in row g: part g
+    }
+    // the units are read by the wave that wrote them: order the LDS accesses
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int k = 0; k < KT * 4; ++k) {
+      uint4 r = make_uint4(0, 0, 0, 0);
+      if (u < parts) r = buf[u][4 * k + g];
+      X[k] = __builtin_bit_cast(half8_t, r);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+};
+
+// GB: blocks per scale; RB: row tiles per visit, above 1 when K takes passes.
+template <int PL, int KT, int FI, int GB, int RB>
+__global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4MatvecArgs a, int passes,
+                                                                         int aligned) {
+  __shared__ float red[2][kMaxWaves][FI * 64];
+  // FI == 1: the waves' units of x on their way to X
+  __shared__ uint4 units[FI == 1 ? (KT == 4 ? 12 : kMaxWaves) : 1][4][KT * 16 + 4];
+  Matvec<PL, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL), aligned);
+  auto stage = [&](int first) {
+    if constexpr (FI == 1)
+      m.stage_few(first, units[m.wave]);
+    else
+      m.stage_many(first);
+  };
+  const int tiles = (a.rows + 15) / 16, nb = m.nb, per_pass = m.waves * KT * 4;
+  uint4 w[RB > 1 ? 1 : 2][KT];
+  uint32_t s[RB > 1 ? 1 : 2][KT];
+  // the wave's KT chunks of tile `tile`; blocks and rows past the end re-read a
+  // valid place (their scale, or their row's output, is dropped)
+  auto load = [&](int tile, int first, uint4 (&ww)[KT], uint32_t (&ss)[KT]) {
+    const long long row = min(tile * 16 + m.n, a.rows - 1);
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const int b = first + 4 * k + m.g, bb = min(b, nb - 1);
+      ww[k] = *(const uint4 *)(a.q + (row * nb + bb) * 16);
+      const uint32_t sc = a.scales[row * (nb / GB) + bb / GB];
+      ss[k] = b < nb ? sc : 0u;
+    }
+  };
+  auto multiply = [&](const uint4 (&ww)[KT], const uint32_t (&ss)[KT], float (&acc)[FI]) {
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const uint4 t = transpose_rows(ww[k]);
+      const uint4 sg = gather_rows(ss[k]);
+      const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, sw[4] = {sg.x, sg.y, sg.z, sg.w};
+#pragma unroll
+      for (int b = 0; b < 4; b += GB) {
+        floatx4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < GB; ++j)
+          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(m.X[4 * k + b + j], decode_word(tw[b + j]), c,
+                                                     0, 0, 0);
+        const float d = f16_to_f32((uint16_t)sw[b]);
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[i] = fmaf(d, c[i], acc[i]);
+      }
+    }
+  };
+  // the waves' sums of a tile to out
+  auto finish = [&](int tile, int buf, const float (&acc)[FI]) {
+#pragma unroll
+    for (int i = 0; i < FI; ++i) red[buf][m.wave][i * 64 + m.lane] = acc[i];
+    __syncthreads();
+    const int tokens = m.parts / PL;
+    for (int j = threadIdx.x; j < 16 * tokens; j += blockDim.x) {
+      const int t = j >> 4, row = tile * 16 + (j & 15);
+      float v = 0.f;
+      for (int x = 0; x < m.waves; ++x)
+#pragma unroll
+        for (int p = 0; p < PL; ++p) {
+          const int u = t * PL + p;
+          v += red[buf][x][(u >> 2) * 64 + (u & 3) * 16 + (j & 15)];
+        }
+      if (row < a.rows) store1(a.out, a.type, (long long)(m.t0 + t) * a.ldo + row, v);
+    }
+  };
+  if constexpr (RB == 1) {
+    const int first = m.wave * KT * 4;
+    int tile = blockIdx.x, it = 0;
+    load(tile, first, w[0], s[0]);
+    stage(first);
+    for (; tile < tiles; tile += gridDim.x, ++it) {
+      load(min(tile + (int)gridDim.x, tiles - 1), first, w[1], s[1]);
+      float acc[FI] = {};
+      multiply(w[0], s[0], acc);
+#pragma unroll
+      for (int i = 0; i < FI; ++i) acc[i] *= m.xs[i];
+      finish(tile, it & 1, acc);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) w[0][k] = w[1][k], s[0][k] = s[1][k];
+    }
+  } else {
+    // more columns than one pass holds: the tokens' slices are staged again for
+    // every pass and RB tiles
+    int it = 0;
+    for (int tile = blockIdx.x * RB; tile < tiles; tile += gridDim.x * RB) {
+      float acc[RB][FI] = {};
+      for (int p = 0; p < passes; ++p) {
+        const int first = p * per_pass + m.wave * KT * 4;
+        stage(first);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          load(min(tile + r, tiles - 1), first, w[0], s[0]);
+          float part[FI] = {};
+          multiply(w[0], s[0], part);
+#pragma unroll
+          for (int i = 0; i < FI; ++i) acc[r][i] = fmaf(part[i], m.xs[i], acc[r][i]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < RB; ++r)
+        if (tile + r < tiles) finish(tile + r, it++ & 1, acc[r]);
+    }
+  }
+}
+
+template <int PL, int KT, int FI, int GB>
+hipError_t launch_one(const Q4MatvecArgs &a, int waves, int passes, bool aligned, hipStream_t s) {
+  const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / PL;
+  const unsigned gy = (unsigned)((a.T + tokens - 1) / tokens);
+  if (KT < 4 || passes == 1) {
+    const dim3 grid((unsigned)min(tiles, 512), gy);
+    q4_matvec_kernel<PL, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1, aligned);
+  } else if constexpr (KT == 4) {
+    const dim3 grid((unsigned)min((tiles + 3) / 4, 512), gy);
+    q4_matvec_kernel<PL, KT, FI, GB, 4><<<grid, waves * 64, 0, s>>>(a, passes, aligned);
+  }
+  return hipGetLastError();
+}
+
+template <int PL, int KT, int FI>
+hipError_t launch_group(const Q4MatvecArgs &a, int waves, int passes, bool al, hipStream_t s) {
+  if (a.group == 32) return launch_one<PL, KT, FI, 1>(a, waves, passes, al, s);
+  if (a.group == 64) return launch_one<PL, KT, FI, 2>(a, waves, passes, al, s);
+  return launch_one<PL, KT, FI, 4>(a, waves, passes, al, s);
+}
+
+template <int PL, int KT>
+hipError_t launch_parts(const Q4MatvecArgs &a, int waves, int passes, bool al, hipStream_t s) {
+  const int parts = a.T * PL;
+  if (parts <= 4) return launch_group<PL, KT, 1>(a, waves, passes, al, s);
+  if (parts <= 8) return launch_group<PL, KT, 2>(a, waves, passes, al, s);
+  return launch_group<PL, KT, 4>(a, waves, passes, al, s);
+}
+
+template <int PL>
+hipError_t launch_cols(const Q4MatvecArgs &a, bool al, hipStream_t s) {
+  const int chunks = (a.cols / 32 + 3) / 4;
+  if (chunks <= 16) return launch_parts<PL, 1>(a, chunks, 1, al, s);
+  if (chunks <= 32) return launch_parts<PL, 2>(a, (chunks + 1) / 2, 1, al, s);
+  if (chunks <= 48) return launch_parts<PL, 4>(a, (chunks + 3) / 4, 1, al, s);
+  const int passes = (chunks + 47) / 48;
+  return launch_parts<PL, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, al, s);
 }
 
 }  // namespace
 
 hipError_t launch_q4_matvec(const Q4MatvecArgs &a, hipStream_t s) {
-  q4_matvec_kernel<<<dim3((unsigned)((a.rows + 3) / 4), (unsigned)a.T), 256, 0, s>>>(a);
-  return hipGetLastError();
+  const bool al = (uintptr_t)a.x % (4 * type_bytes(a.type)) == 0 && a.ldx % 4 == 0;
+  return a.type == kF32 ? launch_cols<2>(a, al, s) : launch_cols<1>(a, al, s);
 }
 
 }  // namespace moe
