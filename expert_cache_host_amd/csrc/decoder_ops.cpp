@@ -189,6 +189,8 @@ int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *b
   if (!f && bad_type(type)) f = "element type must be MOE_F32, MOE_BF16 or MOE_F16";
   if (!f) f = heads_fault(cache, q_heads);
   if (!f && window < 0) f = "window must be >= 0";
+  if (!f && (int64_t)batch->n_rows * q_heads > INT32_MAX - batch->n_seqs)
+    f = "n_rows * q_heads must stay below 2^31";
   if (f) return einval(f);
   return (int64_t)moe::kv_attend_ws_bytes(to_cache(cache), to_batch(batch), type, q_heads, window);
 }
@@ -207,6 +209,8 @@ moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, i
   if (q_stride < 0) return einval("input strides must be >= 0");
   if (batch->n_rows > 1 && out_stride < (int64_t)q_heads * cache->head_dim)
     return einval("out_stride must be >= q_heads * head_dim");
+  if ((int64_t)batch->n_rows * q_heads > INT32_MAX - batch->n_seqs)
+    return einval("n_rows * q_heads must stay below 2^31");
   if (batch->n_rows == 0) return MOE_OK;
   if (!q || !out) return einval("q or out is NULL");
   if (misaligned(q, type) || misaligned(out, type))

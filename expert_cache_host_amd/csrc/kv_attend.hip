@@ -4,97 +4,564 @@
 //   its own, within `window` positions when window > 0, on valid pages; a row
 //   that sees no key gets 0.
 //
-// One wave per row and query head: 64 keys a step, a key per lane for the
-// scores, a few elements of the head per lane for the weighted sum, with the
-// running maximum and sum of the softmax in float32.
+// One pass over the cached codes with the running maximum and sum of the
+// softmax.  The rows of a tile are (new token, query head) pairs of one
+// sequence and one KV head, so that a group's heads share one reading of the
+// cache.  At decode the kernel is bound by reading the codes; decoding them and
+// two multiply-adds per element on the vector units would take longer than the
+// reading, so both products run on the matrix cores with the codes as exact
+// binary16 integers:
+//
+//  - S^T = K q^T, 16 keys by 16 columns a block of 32 elements; a key's block
+//    scale is applied to the block's sum in float32.
+//  - S^T leaves a lane one column and the keys 4 g + i of a tile, which is the
+//    layout the second product wants its probabilities in when its K slots are
+//    those keys of two tiles: nothing is moved between lanes.
+//  - O^T = V^T P^T: a value's block scale belongs to the summed index, so it is
+//    multiplied into the probability (a product per key and block) before that
+//    is rounded to binary16.
+//
+// A float32 row takes two columns of 16 (hi and lo binary16 parts of q and of
+// the scaled probabilities, 22 bits), a half-width row one.  The columns' power
+// of two for q, and for the probabilities the largest value scale met so far,
+// keep binary16 in range whatever the magnitudes are; the running maximum is
+// raised only when a score passes it by 2^4 (the sums' common factor cancels).
+//
+// Keys are split over the waves of a workgroup and over workgroups; the parts
+// are joined in LDS, and by a second kernel when there is more than one
+// workgroup to a tile.
 #include "device_types.hpp"
+#include "q4_tile.hpp"
 
 namespace moe {
 
 namespace {
 
-__global__ __launch_bounds__(64) void kv_attend_kernel(KvAttendArgs a) {
-  __shared__ float qs[256], ps[64];
-  __shared__ long long rows[64];
-  const int t = blockIdx.x, qh = blockIdx.y, lane = threadIdx.x;
-  const int s = seq_of_row(a.b, t);
-  if (s < 0) return;
-  const long long i = (long long)t - a.b.start[s], past = a.b.past[s];
-  if (i < 0) return;
-  const int D = a.c.head_dim, nb = D / 32, head = qh / (a.q_heads / a.c.kv_heads);
-  const long long pos = past + i;
-  const long long hi = past < 0 ? 0 : min(pos + 1, (long long)a.b.max_pages * a.c.page_tokens);
-  const long long lo = a.window > 0 ? max(0ll, pos + 1 - a.window) : 0;
-  for (int e = lane; e < D; e += 64) qs[e] = load1(a.q, a.type, t * a.ldq + qh * D + e) * a.scale;
+constexpr int kWaves = 4;
+constexpr int kMaxPos = 0x7fffff00;  // positions from here on are out of the cache
+constexpr float kLog2e = 1.4426950408889634f;
+// Probabilities stand at 2^kHead over the running maximum's, and may rise by
+// 2^kSlack before the maximum is raised: with scales below 2 a product stays
+// under 2^15.
+constexpr int kHead = 10;
+constexpr float kSlack = 4.f;
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int PL>
+constexpr int rows_of() {
+  return 16 / PL;
+}
+
+// First tile of sequence s when tiles of RT rows never span sequences: an upper
+// bound of the tiles before it that needs no running count.
+__device__ __forceinline__ long long tile_base(const KvBatch &b, int s, int G, int RT) {
+  return ((long long)b.start[s] - b.start[0]) * G / RT + s;
+}
+
+struct Tile {
+  int s, first, rows;  // sequence, first row of the tile in it, rows of the sequence
+  int t0;              // packed row of the sequence's first token
+  long long past;
+};
+
+__device__ __forceinline__ bool find_tile(const KvBatch &b, int G, int RT, long long tile, Tile &o) {
+  int lo = 0, hi = b.n_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tile_base(b, mid, G, RT) <= tile)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  o.s = uniform(lo);
+  o.t0 = uniform(b.start[o.s]);
+  o.rows = uniform((b.start[o.s + 1] - o.t0)) * G;
+  const long long first = (tile - tile_base(b, o.s, G, RT)) * RT;
+  o.past = b.past[o.s];
+  if (first < 0 || first >= o.rows) return false;
+  o.first = (int)first;
+  return true;
+}
+
+__device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
+__device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+// The largest and the sum of v over the four 16-lane rows, per lane n.  (The
+// swaps' results are taken as integers first: a bit cast straight from an
+// element of the returned pair yields element 0.)
+__device__ __forceinline__ float rows_max(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(as_bits(v), as_bits(v), false, false);
+  v = fmaxf(as_float(a[0]), as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(as_bits(v), as_bits(v), false, false);
+  return fmaxf(as_float(b[0]), as_float(b[1]));
+}
+
+__device__ __forceinline__ float rows_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(as_bits(v), as_bits(v), false, false);
+  v = as_float(a[0]) + as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(as_bits(v), as_bits(v), false, false);
+  return as_float(b[0]) + as_float(b[1]);
+}
+
+// v of the lane 8 columns away (within 16 lanes).
+__device__ __forceinline__ float other_half(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
+}
+
+template <int NB>
+struct Scales {  // 4 keys' block scales, as they lie in memory
+  uint32_t w[2 * NB];
+  __device__ __forceinline__ void load(const uint16_t *p) {
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) {
+      const uint4 v = *(const uint4 *)(p + 8 * i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ float at(int key, int b) const {
+    const half2_t h = __builtin_bit_cast(half2_t, w[(key * NB + b) / 2]);
+    return (float)h[(key * NB + b) & 1];
+  }
+  __device__ __forceinline__ void drop(int key) {
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) w[key * NB / 2 + i] = 0;
+  }
+};
+
+template <int D, int PL>
+struct Attend {
+  static constexpr int NB = D / 32, RT = rows_of<PL>();
+  static constexpr int KW = NB >= 4 ? NB / 2 : 1;  // 16-byte loads of 32 keys' codes per lane
+  const KvAttendArgs &a;
+  const int lane, n, g, kvh, tiles_per_page;
+  const int32_t *table;  // the sequence's pages
+  // the next step's two 16-key tiles: page index and tile in the page
+  uint4 kc[KW];
+  Scales<NB> ks[2], vs[2];
+  uint32_t vc[8][NB == 8 ? 2 : 1];
+  uint32_t vtop[NB == 8 ? 2 : 1];  // one share of the step's value scales
+
+  __device__ Attend(const KvAttendArgs &args, int kv_head, int s)
+      : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), kvh(kv_head),
+        tiles_per_page(args.c.page_tokens / 16), table(args.b.pages + (long long)s * args.b.max_pages) {}
+
+  // First cache row of 16-key tile number `kt` (clamped to a valid place), and
+  // whether the sequence has a page there.
+  __device__ __forceinline__ bool tile_row(int kt, long long &row) const {
+    const int pi = kt / tiles_per_page, off = kt - pi * tiles_per_page;
+    const int page = pi < a.b.max_pages ? uniform(table[pi]) : -1;
+    const bool ok = page >= 0 && page < a.c.n_pages;
+    row = ((long long)(ok ? page : 0) * a.c.kv_heads + kvh) * a.c.page_tokens + off * 16;
+    return ok;
+  }
+
+  __device__ __forceinline__ void load_k(long long ra, long long rb) {
+    if constexpr (NB == 2) {
+      const long long r = g < 2 ? ra : rb;
+      kc[0] = *(const uint4 *)(a.c.k_q + (r + n) * 32 + (g & 1) * 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < KW / 2; ++j) {
+        kc[j] = *(const uint4 *)(a.c.k_q + (ra + n) * (D / 2) + j * 64 + g * 16);
+        kc[KW / 2 + j] = *(const uint4 *)(a.c.k_q + (rb + n) * (D / 2) + j * 64 + g * 16);
+      }
+    }
+    ks[0].load(a.c.k_s + (ra + 4 * g) * NB);
+    ks[1].load(a.c.k_s + (rb + 4 * g) * NB);
+  }
+
+  __device__ __forceinline__ void load_v(long long ra, long long rb) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint8_t *p = a.c.v_q + ((j < 4 ? ra : rb) + 4 * g + (j & 3)) * (D / 2) + n * NB;
+      if constexpr (NB == 2) {
+        vc[j][0] = *(const uint16_t *)p;
+      } else if constexpr (NB == 4) {
+        vc[j][0] = *(const uint32_t *)p;
+      } else {
+        const uint2 v = *(const uint2 *)p;
+        vc[j][0] = v.x, vc[j][1] = v.y;
+      }
+    }
+    vs[0].load(a.c.v_s + (ra + 4 * g) * NB);
+    vs[1].load(a.c.v_s + (rb + 4 * g) * NB);
+    const uint16_t *p = a.c.v_s + (lane < 32 ? ra : rb) * NB + (lane & 31) * (NB / 2);
+    if constexpr (NB == 2) {
+      vtop[0] = *p;
+    } else if constexpr (NB == 4) {
+      vtop[0] = *(const uint32_t *)p;
+    } else {
+      const uint2 v = *(const uint2 *)p;
+      vtop[0] = v.x, vtop[1] = v.y;
+    }
+  }
+
+  // Scores of the step's keys, as the matrix cores leave them: s[x][i] is key
+  // 4 g + i of tile x against the lane's column.
+  __device__ __forceinline__ void scores(const half8_t (&Q)[NB], float (&s)[2][4]) const {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
+    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < KW; ++j) {
+      const uint4 t = transpose_rows(kc[j]);
+      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // item k: NB 2: (tile k / 2, block k % 2); else block 4 (j % (KW / 2)) + k of tile j / (KW / 2)
+        const int x = NB == 2 ? k >> 1 : j / (KW > 1 ? KW / 2 : 1);
+        const int b = NB == 2 ? k & 1 : (j % (KW > 1 ? KW / 2 : 1)) * 4 + k;
+        const floatx4 c =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_word(w[k]), Q[b], z, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
+      }
+    }
+    if constexpr (PL == 2) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[x][i] += other_half(s[x][i]);
+    }
+  }
+
+  // O += V^T P^T for the step's probabilities p (key j of K slot j).
+  __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB]) const {
+    const uint32_t lo_part = PL == 2 && n >= 8 ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      half2_t P[4];
+      half2_t A[2][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const Scales<NB> &sc = vs[j >> 1];
+        const int k = 2 * (j & 1);
+        const float s0 = sc.at(k, b), s1 = sc.at(k + 1, b);
+        half2_t h = {(_Float16)(p[2 * j] * s0), (_Float16)(p[2 * j + 1] * s1)};
+        if constexpr (PL == 2) {
+          // the second part's columns hold what the first part's rounding left.
+          // The compiler may round the product in two ways for two uses (once
+          // or twice), which would lose a whole step: the register is fixed first.
+          uint32_t bits = __builtin_bit_cast(uint32_t, h);
+          asm("" : "+v"(bits));
+          h = __builtin_bit_cast(half2_t, bits);
+          const half2_t l = {(_Float16)fmaf(p[2 * j], s0, -(float)h[0]),
+                             (_Float16)fmaf(p[2 * j + 1], s1, -(float)h[1])};
+          h = __builtin_bit_cast(half2_t, (__builtin_bit_cast(uint32_t, l) & lo_part) |
+                                              (__builtin_bit_cast(uint32_t, h) & ~lo_part));
+        }
+        P[j] = h;
+        // keys 2 j and 2 j + 1: the half of their words that holds block b
+        const uint32_t w0 = vc[2 * j][b / 4], w1 = vc[2 * j + 1][b / 4];
+        const uint32_t w = __builtin_amdgcn_perm(w1, w0, (b & 2) ? 0x07060302u : 0x05040100u);
+        A[0][j] = codes_lo(b & 1 ? w >> 8 : w);
+        A[1][j] = codes_hi(b & 1 ? w >> 8 : w);
+      }
+      const half8_t B = join8(P[0], P[1], P[2], P[3]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        O[2 * b + h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            join8(A[h][0], A[h][1], A[h][2], A[h][3]), B, O[2 * b + h], 0, 0, 0);
+    }
+  }
+};
+
+// Partial results of one workgroup in the workspace: per slot RT rows of D sums,
+// then the slots' references and sums of probabilities.
+struct Parts {
+  float *o, *ref, *sum;
+};
+template <int D, int PL>
+__device__ __host__ inline size_t part_floats() {
+  return (size_t)rows_of<PL>() * (D + 2);
+}
+
+template <int D, int PL>
+__global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, int splits,
+                                                                int aligned) {
+  constexpr int NB = D / 32, RT = rows_of<PL>();
+  __shared__ float lo[kWaves][RT][D + 4];
+  __shared__ float lref[kWaves][RT], lsum[kWaves][RT];
+  const int G = a.q_heads / a.c.kv_heads;
+  const int kvh = blockIdx.y / splits, split = blockIdx.y % splits;
+  Tile tile;
+  if (!find_tile(a.b, G, RT, blockIdx.x, tile)) return;
+  Attend<D, PL> w(a, kvh, tile.s);
+  const int n = w.n, g = w.g, wave = uniform(threadIdx.x >> 6);
+
+  // the lane's column: row n % RT of the tile, part n / RT of it
+  const int row = tile.first + n % RT, tok = row / G, head = kvh * G + row % G;
+  const long long t = (long long)tile.t0 + tok;
+  const bool live = row < tile.rows && t >= 0 && t < a.b.T && tile.past >= 0;
+  const long long cap = min((long long)a.b.max_pages * a.c.page_tokens, (long long)kMaxPos);
+  const int hi = live ? (int)min(tile.past + tok + 1, cap) : 0;
+  const int lo_key =
+      a.window > 0 ? (int)min(max(tile.past + tok + 1 - a.window, 0ll), cap) : 0;
+  // the tile's range: every key some row sees, and the keys every row sees
+  const int tok0 = tile.first / G, tok1 = (min(tile.first + RT, tile.rows) - 1) / G;
+  const long long past = max(tile.past, 0ll);
+  const int hi_max = tile.past < 0 ? 0 : (int)min(past + tok1 + 1, cap);
+  const int hi_min = (int)min(past + tok0 + 1, cap);
+  const int lo_min = a.window > 0 ? (int)min(max(past + tok0 + 1 - a.window, 0ll), cap) : 0;
+  const int lo_max = a.window > 0 ? (int)min(max(past + tok1 + 1 - a.window, 0ll), cap) : 0;
+  const int step0 = lo_min / 32, steps = max(0, (hi_max + 31) / 32 - step0);
+  const int per = (steps + splits * kWaves - 1) / (splits * kWaves);
+  const int i0 = min((split * kWaves + wave) * per, steps), i1 = min(i0 + per, steps);
+
+  floatx4 O[2 * NB];
+#pragma unroll
+  for (int b = 0; b < 2 * NB; ++b) O[b] = floatx4{0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, sum = 0.f;  // running maximum (log2 units) and sum
+  int vexp = -14;                    // value scales met so far lie below 2^(vexp + 1)
+
+  if (i0 < i1) {
+    long long ra, rb;
+    bool oka = w.tile_row((step0 + i0) * 2, ra), okb = w.tile_row((step0 + i0) * 2 + 1, rb);
+    w.load_k(ra, rb);
+    w.load_v(ra, rb);
+
+    // q: the column's elements in the codes' order, at the row's power of two
+    half8_t Q[NB];
+    uint32_t big = 0;
+    float v[NB][8];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (live) {
+        const long long i = t * a.ldq + head * D + b * 32 + 4 * g;
+        if (aligned) {
+          x = load4(a.q, a.type, i), y = load4(a.q, a.type, i + 16);
+        } else {
+          x = make_float4(load1(a.q, a.type, i), load1(a.q, a.type, i + 1),
+                          load1(a.q, a.type, i + 2), load1(a.q, a.type, i + 3));
+          y = make_float4(load1(a.q, a.type, i + 16), load1(a.q, a.type, i + 17),
+                          load1(a.q, a.type, i + 18), load1(a.q, a.type, i + 19));
+        }
+      }
+      unit_order(x, y, v[b]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        big = max(big, __builtin_bit_cast(uint32_t, v[b][j]) & 0x7fffffffu);
+    }
+    const int e = scale_exp(rows_max_u32(big));
+    const float f = exp2_int(-e);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        _Float16 x, y;
+        split_half(v[b][j] * f, x, y);
+        Q[b][j] = PL == 2 && n >= 8 ? y : x;
+      }
+    const float unit = exp2_int(e), cq = a.scale * kLog2e;
+
+    for (int i = i0; i < i1; ++i) {
+      const int key0 = (step0 + i) * 32;
+      const bool whole = oka && okb && key0 >= lo_max && key0 + 32 <= hi_min;
+      const bool ok_now[2] = {oka, okb};
+      const int nx = min(i + 1, i1 - 1);
+      oka = w.tile_row((step0 + nx) * 2, ra);
+      okb = w.tile_row((step0 + nx) * 2 + 1, rb);
+
+      float s[2][4];
+      w.scores(Q, s);
+      w.load_k(ra, rb);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[x][j] = s[x][j] * unit * cq;
+      if (!whole) {
+        // keys the row does not see; and places that hold no key of the
+        // sequence, whose scales may be anything
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = key0 + 16 * x + 4 * g + j;
+            if (!(ok_now[x] && key >= lo_key && key < hi)) s[x][j] = -INFINITY;
+            if (!(ok_now[x] && key < hi_max)) w.vs[x].drop(j);
+          }
+        const int x = w.lane >> 5, key = key0 + 16 * x + ((w.lane & 31) >> 1);
+        if (!((x ? ok_now[1] : ok_now[0]) && key < hi_max)) {
+          w.vtop[0] = 0;
+          if constexpr (NB == 8) w.vtop[1] = 0;
+        }
+      }
+      float m = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                      fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+      if (__any(m > top + kSlack)) {
+        const float to = fmaxf(top, rows_max(m));
+        const float f = to == -INFINITY ? 1.f : exp2f(top - to);
+        top = to;
+        sum *= f;
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) O[b][j] *= f;
+      }
+      uint32_t sb = max(w.vtop[0] & 0x7fffu, (w.vtop[0] >> 16) & 0x7fffu);
+      if constexpr (NB == 8)
+        sb = max(sb, max(w.vtop[1] & 0x7fffu, (w.vtop[1] >> 16) & 0x7fffu));
+      if (__any((int)(sb >> 10) - 15 > vexp)) {
+        const int to = max(vexp, (int)(wave_max_u32(sb) >> 10) - 15);
+        const float f = exp2_int(vexp - to);
+        vexp = uniform(to);
+        sum *= f;
+#pragma unroll
+        for (int b = 0; b < 2 * NB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) O[b][j] *= f;
+      }
+      const float off = (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
+      float p[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(s[j >> 2][j & 3] - off);
+        sum += p[j];
+      }
+      w.weigh(p, O);
+      w.load_v(ra, rb);
+    }
+  }
+
+  // join the waves: reference of the column's sums, -inf when it saw no key
+  sum = rows_sum(sum);
+  const float ref =
+      sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
+  if (g == 0 && n < RT) lref[wave][n] = ref, lsum[wave][n] = sum;
+#pragma unroll
+  for (int b = 0; b < 2 * NB; ++b) {
+    if constexpr (PL == 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) O[b][j] += other_half(O[b][j]);
+    }
+    if (n < RT) *(floatx4 *)&lo[wave][n][b * 16 + 4 * g] = O[b];
+  }
   __syncthreads();
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (long long k0 = lo; k0 < hi; k0 += 64) {
-    const long long key = k0 + lane;
-    long long row = -1;
-    if (key < hi) {
-      const int page = a.b.pages[(long long)s * a.b.max_pages + key / a.c.page_tokens];
-      if (page >= 0 && page < a.c.n_pages)
-        row = ((long long)page * a.c.kv_heads + head) * a.c.page_tokens + key % a.c.page_tokens;
+  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * splits + split;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * splits;
+  float *ws = (float *)a.ws;
+  for (int j = threadIdx.x; j < RT * D / 4; j += kWaves * 64) {
+    const int r = j / (D / 4), d = j % (D / 4) * 4;
+    float best = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) best = fmaxf(best, lref[x][r]);
+    float l = 0.f;
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      const float f = lref[x][r] == -INFINITY ? 0.f : exp2f(lref[x][r] - best);
+      l = fmaf(f, lsum[x][r], l);
+      const floatx4 v = *(const floatx4 *)&lo[x][r][d];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
     }
-    float z = -INFINITY;
-    if (row >= 0) {
-      z = 0.f;
-      for (int b = 0; b < nb; ++b) {
-        float sum = 0.f;
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t byte = a.c.k_q[row * (D / 2) + b * 16 + j];
-          sum = fmaf((float)(int)(byte & 15u) - 8.f, qs[b * 32 + j], sum);
-          sum = fmaf((float)(int)(byte >> 4) - 8.f, qs[b * 32 + 16 + j], sum);
-        }
-        z = fmaf(f16_to_f32(a.c.k_s[row * nb + b]), sum, z);
+    if (splits > 1) {
+      *(floatx4 *)(ws + (slot * RT + r) * D + d) = o;
+      if (d == 0) {
+        ws[slots * RT * D + slot * RT + r] = best;
+        ws[slots * RT * (D + 1) + slot * RT + r] = l;
+      }
+    } else {
+      const int rr = tile.first + r, tk = rr / G;
+      const long long tt = (long long)tile.t0 + tk;
+      if (rr < tile.rows && tt >= 0 && tt < a.b.T) {
+        const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) store1(a.out, a.type, at + k, l == 0.f ? 0.f : o[k] / l);
       }
     }
-    float top = z;
-    for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-    const float alpha = expf(m - ref), p = expf(z - ref);
-    m = mn;
-    float sum = p;
-    for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x);
-    l = l * alpha + sum;
-    ps[lane] = p;
-    rows[lane] = row;
-    __syncthreads();
+  }
+}
+
+// Joins the splits of a tile.
+template <int D, int PL>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int splits) {
+  constexpr int RT = rows_of<PL>();
+  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y;
+  Tile tile;
+  if (!find_tile(a.b, G, RT, blockIdx.x, tile)) return;
+  const size_t slot0 = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * splits;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * splits;
+  const float *ws = (const float *)a.ws;
+  const float *refs = ws + slots * RT * D, *sums = refs + slots * RT;
+  for (int j = threadIdx.x; j < RT * D / 4; j += 256) {
+    const int r = j / (D / 4), d = j % (D / 4) * 4;
+    const int rr = tile.first + r, tk = rr / G;
+    const long long tt = (long long)tile.t0 + tk;
+    if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    float best = -INFINITY;
+    for (int x = 0; x < splits; ++x) best = fmaxf(best, refs[(slot0 + x) * RT + r]);
+    float l = 0.f;
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < splits; ++x) {
+      const float ref = refs[(slot0 + x) * RT + r];
+      if (ref == -INFINITY) continue;
+      const float f = exp2f(ref - best);
+      l = fmaf(f, sums[(slot0 + x) * RT + r], l);
+      const floatx4 v = *(const floatx4 *)(ws + ((slot0 + x) * RT + r) * D + d);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] *= alpha;
-    for (int j = 0; j < 64; ++j) {
-      const long long r = rows[j];
-      if (r < 0) continue;
-      const float pj = ps[j];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = lane + 64 * e;
-        if (d < D) {
-          const uint32_t byte = a.c.v_q[r * (D / 2) + (d & 15) * nb + d / 32];
-          const int code = (d & 16) ? byte >> 4 : byte & 15;
-          o[e] = fmaf(pj, f16_to_f32(a.c.v_s[r * nb + d / 32]) * (float)(code - 8), o[e]);
-        }
-      }
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
     }
-    __syncthreads();
-  }
+    const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int d = lane + 64 * e;
-    if (d < D) store1(a.out, a.type, t * a.ldo + qh * D + d, l == 0.f ? 0.f : o[e] / l);
+    for (int k = 0; k < 4; ++k) store1(a.out, a.type, at + k, l == 0.f ? 0.f : o[k] / l);
   }
+}
+
+int rows_per_tile(int type) { return type == kF32 ? 8 : 16; }
+
+long long tiles_bound(const KvCache &c, const KvBatch &b, int type, int q_heads) {
+  return (long long)b.T * (q_heads / c.kv_heads) / rows_per_tile(type) + b.n_seqs;
+}
+
+template <int D, int PL>
+hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
+  const int splits = kv_attend_splits(a.c, a.b, a.type, a.q_heads, a.window);
+  const long long tiles = tiles_bound(a.c, a.b, a.type, a.q_heads);
+  const int al = (uintptr_t)a.q % (4 * type_bytes(a.type)) == 0 && a.ldq % 4 == 0;
+  kv_attend_kernel<D, PL><<<dim3((unsigned)tiles, (unsigned)(a.c.kv_heads * splits)), kWaves * 64,
+                            0, s>>>(a, splits, al);
+  if (splits > 1)
+    kv_join_kernel<D, PL><<<dim3((unsigned)tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, splits);
+  return hipGetLastError();
+}
+
+template <int PL>
+hipError_t launch_dim(const KvAttendArgs &a, hipStream_t s) {
+  if (a.c.head_dim == 64) return launch_one<64, PL>(a, s);
+  if (a.c.head_dim == 128) return launch_one<128, PL>(a, s);
+  return launch_one<256, PL>(a, s);
 }
 
 }  // namespace
 
-int kv_attend_splits(const KvCache &, const KvBatch &, int, int, int) { return 1; }
+int kv_attend_splits(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
+  // enough workgroups for the chip, each wave with two steps of 32 keys at the
+  // table's length at least
+  const long long groups = tiles_bound(c, b, type, q_heads) * c.kv_heads;
+  long long len = (long long)b.max_pages * c.page_tokens;
+  if (window > 0 && window + 64 < len) len = window + 64;
+  const long long most = (len + 64 * kWaves - 1) / (64 * kWaves), want = (1024 + groups - 1) / groups;
+  long long n = want < most ? want : most;
+  if (n > 32) n = 32;
+  return n < 1 ? 1 : (int)n;
+}
 
-size_t kv_attend_ws_bytes(const KvCache &, const KvBatch &, int, int, int) { return 0; }
+size_t kv_attend_ws_bytes(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
+  const int splits = kv_attend_splits(c, b, type, q_heads, window);
+  if (splits == 1) return 0;
+  return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * splits * rows_per_tile(type) *
+         (c.head_dim + 2) * sizeof(float);
+}
 
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s) {
   if (a.b.T == 0) return hipSuccess;
-  kv_attend_kernel<<<dim3((unsigned)a.b.T, (unsigned)a.q_heads), 64, 0, s>>>(a);
-  return hipGetLastError();
+  return a.type == kF32 ? launch_dim<2>(a, s) : launch_dim<1>(a, s);
 }
 
 }  // namespace moe
