@@ -48,10 +48,9 @@ constexpr float kSlack = 4.f;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int PL>
-constexpr int rows_of() {
-  return 16 / PL;
-}
+// Columns a row takes, and rows of a tile.
+constexpr int parts_of(int type) { return type == kF32 ? 2 : 1; }
+constexpr int rows_of(int type) { return 16 / parts_of(type); }
 
 // First tile of sequence s when tiles of RT rows never span sequences: an upper
 // bound of the tiles before it that needs no running count.
@@ -132,11 +131,12 @@ struct Scales {  // 4 keys' block scales, as they lie in memory
 
 template <int D, int PL>
 struct Attend {
-  static constexpr int NB = D / 32, RT = rows_of<PL>();
+  static constexpr int NB = D / 32;
   static constexpr int KW = NB >= 4 ? NB / 2 : 1;  // 16-byte loads of 32 keys' codes per lane
   const KvAttendArgs &a;
   const int lane, n, g, kvh, tiles_per_page;
   const int32_t *table;  // the sequence's pages
+  const CodeBits bits;
   // the next step's two 16-key tiles: page index and tile in the page
   uint4 kc[KW];
   Scales<NB> ks[2], vs[2];
@@ -216,7 +216,7 @@ struct Attend {
         const int x = NB == 2 ? k >> 1 : j / (KW > 1 ? KW / 2 : 1);
         const int b = NB == 2 ? k & 1 : (j % (KW > 1 ? KW / 2 : 1)) * 4 + k;
         const floatx4 c =
-            __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_word(w[k]), Q[b], z, 0, 0, 0);
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_word(bits, w[k]), Q[b], z, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
       }
@@ -227,6 +227,16 @@ struct Attend {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[x][i] += other_half(s[x][i]);
     }
+  }
+
+  // Binary16 products p0 s0 and p1 s1, each rounded once: a mixed multiply-add
+  // per product takes the scale as binary16.  (The first half is made opaque,
+  // else the compiler converts scales and products one by one: 5 instructions
+  // a pair in place of 2.)
+  static __device__ __forceinline__ half2_t scaled(float p0, float s0, float p1, float s1) {
+    _Float16 x = (_Float16)fmaf(p0, s0, 0.f);
+    asm("" : "+v"(x));
+    return half2_t{x, (_Float16)fmaf(p1, s1, 0.f)};
   }
 
   // O += V^T P^T for the step's probabilities p (key j of K slot j).
@@ -241,7 +251,7 @@ struct Attend {
         const Scales<NB> &sc = vs[j >> 1];
         const int k = 2 * (j & 1);
         const float s0 = sc.at(k, b), s1 = sc.at(k + 1, b);
-        half2_t h = {(_Float16)(p[2 * j] * s0), (_Float16)(p[2 * j + 1] * s1)};
+        half2_t h = scaled(p[2 * j], s0, p[2 * j + 1], s1);
         if constexpr (PL == 2) {
           // the second part's columns hold what the first part's rounding left.
           // The compiler may round the product in two ways for two uses (once
@@ -258,8 +268,8 @@ struct Attend {
         // keys 2 j and 2 j + 1: the half of their words that holds block b
         const uint32_t w0 = vc[2 * j][b / 4], w1 = vc[2 * j + 1][b / 4];
         const uint32_t w = __builtin_amdgcn_perm(w1, w0, (b & 2) ? 0x07060302u : 0x05040100u);
-        A[0][j] = codes_lo(b & 1 ? w >> 8 : w);
-        A[1][j] = codes_hi(b & 1 ? w >> 8 : w);
+        A[0][j] = bits.low(b & 1 ? w >> 8 : w);
+        A[1][j] = bits.high(b & 1 ? w >> 8 : w);
       }
       const half8_t B = join8(P[0], P[1], P[2], P[3]);
 #pragma unroll
@@ -270,20 +280,12 @@ struct Attend {
   }
 };
 
-// Partial results of one workgroup in the workspace: per slot RT rows of D sums,
-// then the slots' references and sums of probabilities.
-struct Parts {
-  float *o, *ref, *sum;
-};
-template <int D, int PL>
-__device__ __host__ inline size_t part_floats() {
-  return (size_t)rows_of<PL>() * (D + 2);
-}
-
-template <int D, int PL>
-__global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, int splits,
+// The workspace holds, per slot (tile, KV head, split): RT rows of D sums; then
+// all slots' references, then their sums of probabilities.
+template <int D, int TY>
+__global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void kv_attend_kernel(KvAttendArgs a, int splits,
                                                                 int aligned) {
-  constexpr int NB = D / 32, RT = rows_of<PL>();
+  constexpr int NB = D / 32, PL = parts_of(TY), RT = rows_of(TY);
   __shared__ float lo[kWaves][RT][D + 4];
   __shared__ float lref[kWaves][RT], lsum[kWaves][RT];
   const int G = a.q_heads / a.c.kv_heads;
@@ -334,12 +336,12 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, 
       if (live) {
         const long long i = t * a.ldq + head * D + b * 32 + 4 * g;
         if (aligned) {
-          x = load4(a.q, a.type, i), y = load4(a.q, a.type, i + 16);
+          x = load4(a.q, TY, i), y = load4(a.q, TY, i + 16);
         } else {
-          x = make_float4(load1(a.q, a.type, i), load1(a.q, a.type, i + 1),
-                          load1(a.q, a.type, i + 2), load1(a.q, a.type, i + 3));
-          y = make_float4(load1(a.q, a.type, i + 16), load1(a.q, a.type, i + 17),
-                          load1(a.q, a.type, i + 18), load1(a.q, a.type, i + 19));
+          x = make_float4(load1(a.q, TY, i), load1(a.q, TY, i + 1),
+                          load1(a.q, TY, i + 2), load1(a.q, TY, i + 3));
+          y = make_float4(load1(a.q, TY, i + 16), load1(a.q, TY, i + 17),
+                          load1(a.q, TY, i + 18), load1(a.q, TY, i + 19));
         }
       }
       unit_order(x, y, v[b]);
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, 
         split_half(v[b][j] * f, x, y);
         Q[b][j] = PL == 2 && n >= 8 ? y : x;
       }
-    const float unit = exp2_int(e), cq = a.scale * kLog2e;
+    const float unit = exp2_int(e) * (a.scale * kLog2e);
 
     for (int i = i0; i < i1; ++i) {
       const int key0 = (step0 + i) * 32;
@@ -373,7 +375,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, 
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[x][j] = s[x][j] * unit * cq;
+        for (int j = 0; j < 4; ++j) s[x][j] *= unit;
       if (!whole) {
         // keys the row does not see; and places that hold no key of the
         // sequence, whose scales may be anything
@@ -472,16 +474,16 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attend_kernel(KvAttendArgs a, 
       if (rr < tile.rows && tt >= 0 && tt < a.b.T) {
         const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) store1(a.out, a.type, at + k, l == 0.f ? 0.f : o[k] / l);
+        for (int k = 0; k < 4; ++k) store1(a.out, TY, at + k, l == 0.f ? 0.f : o[k] / l);
       }
     }
   }
 }
 
 // Joins the splits of a tile.
-template <int D, int PL>
+template <int D, int TY>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int splits) {
-  constexpr int RT = rows_of<PL>();
+  constexpr int RT = rows_of(TY);
   const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y;
   Tile tile;
   if (!find_tile(a.b, G, RT, blockIdx.x, tile)) return;
@@ -509,33 +511,31 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int splits
     }
     const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) store1(a.out, a.type, at + k, l == 0.f ? 0.f : o[k] / l);
+    for (int k = 0; k < 4; ++k) store1(a.out, TY, at + k, l == 0.f ? 0.f : o[k] / l);
   }
 }
 
-int rows_per_tile(int type) { return type == kF32 ? 8 : 16; }
-
 long long tiles_bound(const KvCache &c, const KvBatch &b, int type, int q_heads) {
-  return (long long)b.T * (q_heads / c.kv_heads) / rows_per_tile(type) + b.n_seqs;
+  return (long long)b.T * (q_heads / c.kv_heads) / rows_of(type) + b.n_seqs;
 }
 
-template <int D, int PL>
+template <int D, int TY>
 hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
   const int splits = kv_attend_splits(a.c, a.b, a.type, a.q_heads, a.window);
   const long long tiles = tiles_bound(a.c, a.b, a.type, a.q_heads);
   const int al = (uintptr_t)a.q % (4 * type_bytes(a.type)) == 0 && a.ldq % 4 == 0;
-  kv_attend_kernel<D, PL><<<dim3((unsigned)tiles, (unsigned)(a.c.kv_heads * splits)), kWaves * 64,
+  kv_attend_kernel<D, TY><<<dim3((unsigned)tiles, (unsigned)(a.c.kv_heads * splits)), kWaves * 64,
                             0, s>>>(a, splits, al);
   if (splits > 1)
-    kv_join_kernel<D, PL><<<dim3((unsigned)tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, splits);
+    kv_join_kernel<D, TY><<<dim3((unsigned)tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, splits);
   return hipGetLastError();
 }
 
-template <int PL>
+template <int TY>
 hipError_t launch_dim(const KvAttendArgs &a, hipStream_t s) {
-  if (a.c.head_dim == 64) return launch_one<64, PL>(a, s);
-  if (a.c.head_dim == 128) return launch_one<128, PL>(a, s);
-  return launch_one<256, PL>(a, s);
+  if (a.c.head_dim == 64) return launch_one<64, TY>(a, s);
+  if (a.c.head_dim == 128) return launch_one<128, TY>(a, s);
+  return launch_one<256, TY>(a, s);
 }
 
 }  // namespace
@@ -555,13 +555,14 @@ int kv_attend_splits(const KvCache &c, const KvBatch &b, int type, int q_heads, 
 size_t kv_attend_ws_bytes(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
   const int splits = kv_attend_splits(c, b, type, q_heads, window);
   if (splits == 1) return 0;
-  return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * splits * rows_per_tile(type) *
+  return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * splits * rows_of(type) *
          (c.head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s) {
   if (a.b.T == 0) return hipSuccess;
-  return a.type == kF32 ? launch_dim<2>(a, s) : launch_dim<1>(a, s);
+  if (a.type == kF32) return launch_dim<kF32>(a, s);
+  return a.type == kBf16 ? launch_dim<kBf16>(a, s) : launch_dim<kF16>(a, s);
 }
 
 }  // namespace moe

@@ -153,6 +153,7 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
   const int tiles = (a.rows + 15) / 16, nb = m.nb, per_pass = m.waves * KT * 4;
   uint4 w[RB > 1 ? 1 : 2][KT];
   uint32_t s[RB > 1 ? 1 : 2][KT];
+  const CodeBits bits;
   // the wave's KT chunks of tile `tile`; blocks and rows past the end re-read a
   // valid place (their scale, or their row's output, is dropped)
   auto load = [&](int tile, int first, uint4 (&ww)[KT], uint32_t (&ss)[KT]) {
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
         floatx4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < GB; ++j)
-          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(m.X[4 * k + b + j], decode_word(tw[b + j]), c,
+          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(m.X[4 * k + b + j], decode_word(bits, tw[b + j]), c,
                                                      0, 0, 0);
         const float d = f16_to_f32((uint16_t)sw[b]);
 #pragma unroll

@@ -17,18 +17,28 @@ typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 
-// Two codes minus 8 from the low nibbles of a word's halves: or-ing a nibble
-// into binary16 1024 gives 1024 + q; both steps are exact.
-__device__ __forceinline__ half2_t codes_lo(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x000f000fu) | 0x64006400u);
-  return v - half2_t{(_Float16)1032.f, (_Float16)1032.f};
-}
-// The same from the second nibbles: 1024 + 16 q, so (1024 + 16 q) / 16 - 72 = q - 8.
-__device__ __forceinline__ half2_t codes_hi(uint32_t w) {
-  const half2_t v = __builtin_bit_cast(half2_t, (w & 0x00f000f0u) | 0x64006400u);
-  return __builtin_elementwise_fma(v, half2_t{(_Float16)0.0625f, (_Float16)0.0625f},
-                                   half2_t{(_Float16)-72.f, (_Float16)-72.f});
-}
+// The constants of the decoding, held in registers: with literals the compiler
+// takes an and and an or where v_and_or_b32 does both.
+struct CodeBits {
+  uint32_t lo = 0x000f000fu, hi = 0x00f000f0u, one = 0x64006400u;
+  __device__ __forceinline__ CodeBits() {
+    asm("" : "+s"(lo));
+    asm("" : "+s"(hi));
+    asm("" : "+v"(one));
+  }
+  // Two codes minus 8 from the low nibbles of a word's halves: or-ing a nibble
+  // into binary16 1024 gives 1024 + q; both steps are exact.
+  __device__ __forceinline__ half2_t low(uint32_t w) const {
+    const half2_t v = __builtin_bit_cast(half2_t, (w & lo) | one);
+    return v - half2_t{(_Float16)1032.f, (_Float16)1032.f};
+  }
+  // The same from the second nibbles: 1024 + 16 q, so (1024 + 16 q) / 16 - 72 = q - 8.
+  __device__ __forceinline__ half2_t high(uint32_t w) const {
+    const half2_t v = __builtin_bit_cast(half2_t, (w & hi) | one);
+    return __builtin_elementwise_fma(v, half2_t{(_Float16)0.0625f, (_Float16)0.0625f},
+                                     half2_t{(_Float16)-72.f, (_Float16)-72.f});
+  }
+};
 
 __device__ __forceinline__ half8_t join8(half2_t a, half2_t b, half2_t c, half2_t d) {
   return half8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -36,8 +46,8 @@ __device__ __forceinline__ half8_t join8(half2_t a, half2_t b, half2_t c, half2_
 
 // The eight values q - 8 of a word: elements (0, 2, 16, 18, 1, 3, 17, 19) + 4 g
 // of its block when the word is word g.
-__device__ __forceinline__ half8_t decode_word(uint32_t w) {
-  return join8(codes_lo(w), codes_hi(w), codes_lo(w >> 8), codes_hi(w >> 8));
+__device__ __forceinline__ half8_t decode_word(const CodeBits &c, uint32_t w) {
+  return join8(c.low(w), c.high(w), c.low(w >> 8), c.high(w >> 8));
 }
 
 // Puts x[4 g .. 4 g + 3] (a) and x[4 g + 16 .. 4 g + 19] (b) into decode_word's order.
