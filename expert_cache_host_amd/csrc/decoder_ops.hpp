@@ -78,8 +78,7 @@ struct KvAttendArgs {
   float scale;
   void *ws;
 };
-// Splits of the keys for this call's sizes, and the workspace they need.
-int kv_attend_splits(const KvCache &c, const KvBatch &b, int type, int q_heads, int window);
+// Workspace of a call of these sizes.
 size_t kv_attend_ws_bytes(const KvCache &c, const KvBatch &b, int type, int q_heads, int window);
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s);
 

@@ -52,36 +52,65 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 constexpr int parts_of(int type) { return type == kF32 ? 2 : 1; }
 constexpr int rows_of(int type) { return 16 / parts_of(type); }
 
-// First tile of sequence s when tiles of RT rows never span sequences: an upper
-// bound of the tiles before it that needs no running count.
-__device__ __forceinline__ long long tile_base(const KvBatch &b, int s, int G, int RT) {
-  return ((long long)b.start[s] - b.start[0]) * G / RT + s;
-}
-
+// Rows of a tile of sequence s, and the 32-key steps that some row of it sees.
 struct Tile {
   int s, first, rows;  // sequence, first row of the tile in it, rows of the sequence
   int t0;              // packed row of the sequence's first token
-  long long past;
+  int past;
+  int step0, steps;
 };
 
-__device__ __forceinline__ bool find_tile(const KvBatch &b, int G, int RT, long long tile, Tile &o) {
-  int lo = 0, hi = b.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tile_base(b, mid, G, RT) <= tile)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  o.s = uniform(lo);
-  o.t0 = uniform(b.start[o.s]);
-  o.rows = uniform((b.start[o.s + 1] - o.t0)) * G;
-  const long long first = (tile - tile_base(b, o.s, G, RT)) * RT;
-  o.past = b.past[o.s];
+// First tile of sequence s when tiles of RT rows never span sequences: an upper
+// bound of the tiles before it that needs no running count.
+__device__ __forceinline__ long long tile_base(int start_s, int start_0, int s, int G, int RT) {
+  return ((long long)start_s - start_0) * G / RT + s;
+}
+
+__device__ __forceinline__ long long position_cap(const KvAttendArgs &a) {
+  return min((long long)a.b.max_pages * a.c.page_tokens, (long long)kMaxPos);
+}
+
+// Fills in a tile of sequence o.s from the sequence's rows start .. end; false
+// when the tile has no row.
+__device__ __forceinline__ bool fill_tile(const KvAttendArgs &a, int G, int RT, long long tile,
+                                          int start_0, int start, int end, Tile &o) {
+  o.t0 = start;
+  o.rows = (end - start) * G;
+  o.steps = 0;
+  const long long first = (tile - tile_base(start, start_0, o.s, G, RT)) * RT;
   if (first < 0 || first >= o.rows) return false;
   o.first = (int)first;
+  if (o.past < 0) return true;
+  const int tok0 = o.first / G, tok1 = (min(o.first + RT, o.rows) - 1) / G;
+  const long long cap = position_cap(a);
+  const int hi = (int)min((long long)o.past + tok1 + 1, cap);
+  const int lo =
+      a.window > 0 ? (int)min(max((long long)o.past + tok0 + 1 - a.window, 0ll), cap) : 0;
+  o.step0 = lo / 32;
+  o.steps = max(0, (hi + 31) / 32 - o.step0);
   return true;
 }
+
+// The tile with this number: a search over the batch's sequences, 64 of them a
+// probe (one load's latency for up to 64 sequences, two up to 4096).
+__device__ __forceinline__ bool find_tile(const KvAttendArgs &a, int G, int RT, long long tile,
+                                          Tile &o) {
+  const int lane = threadIdx.x & 63, start_0 = a.b.start[0];
+  int lo = 0, hi = a.b.n_seqs;  // the last s in [lo, hi) whose first tile is at most `tile`
+  while (hi - lo > 1) {
+    const int each = (hi - lo + 63) / 64, s = lo + lane * each;
+    const bool before = s < hi && tile_base(a.b.start[min(s, hi - 1)], start_0, s, G, RT) <= tile;
+    lo += (max(__popcll(__ballot(before)), 1) - 1) * each;
+    hi = min(hi, lo + each);
+  }
+  o.s = uniform(lo);
+  o.past = uniform(a.b.past[o.s]);
+  return fill_tile(a, G, RT, tile, uniform(start_0), uniform(a.b.start[o.s]),
+                   uniform(a.b.start[o.s + 1]), o);
+}
+
+// Parts that `steps` steps are cut into: equal ones, of at most `chunk` steps.
+__device__ __forceinline__ int parts_in(int steps, int chunk) { return (steps + chunk - 1) / chunk; }
 
 __device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
@@ -112,10 +141,10 @@ __device__ __forceinline__ float other_half(float v) {
 template <int NB>
 struct Scales {  // 4 keys' block scales, as they lie in memory
   uint32_t w[2 * NB];
-  __device__ __forceinline__ void load(const uint16_t *p) {
+  __device__ __forceinline__ void load(const char *tile, uint32_t offset) {
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) {
-      const uint4 v = *(const uint4 *)(p + 8 * i);
+      const uint4 v = *(const uint4 *)(tile + offset + 16 * i);
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
@@ -134,60 +163,75 @@ struct Attend {
   static constexpr int NB = D / 32;
   static constexpr int KW = NB >= 4 ? NB / 2 : 1;  // 16-byte loads of 32 keys' codes per lane
   const KvAttendArgs &a;
-  const int lane, n, g, kvh, tiles_per_page;
+  const int lane, n, g, tiles_per_page;
+  const long long page_rows, head_row;  // cache rows of a page, and before the KV head's in it
   const int32_t *table;  // the sequence's pages
   const CodeBits bits;
-  // the next step's two 16-key tiles: page index and tile in the page
+  int pi, off;  // the cursor: next step's first 16-key tile as page index and tile in the page
+  // a step's codes and scales
   uint4 kc[KW];
   Scales<NB> ks[2], vs[2];
   uint32_t vc[8][NB == 8 ? 2 : 1];
   uint32_t vtop[NB == 8 ? 2 : 1];  // one share of the step's value scales
 
   __device__ Attend(const KvAttendArgs &args, int kv_head, int s)
-      : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), kvh(kv_head),
-        tiles_per_page(args.c.page_tokens / 16), table(args.b.pages + (long long)s * args.b.max_pages) {}
+      : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4),
+        tiles_per_page(args.c.page_tokens / 16),
+        page_rows((long long)args.c.kv_heads * args.c.page_tokens),
+        head_row((long long)kv_head * args.c.page_tokens), table(args.b.pages + (long long)s * args.b.max_pages) {}
 
-  // First cache row of 16-key tile number `kt` (clamped to a valid place), and
-  // whether the sequence has a page there.
-  __device__ __forceinline__ bool tile_row(int kt, long long &row) const {
-    const int pi = kt / tiles_per_page, off = kt - pi * tiles_per_page;
-    const int page = pi < a.b.max_pages ? uniform(table[pi]) : -1;
-    const bool ok = page >= 0 && page < a.c.n_pages;
-    row = ((long long)(ok ? page : 0) * a.c.kv_heads + kvh) * a.c.page_tokens + off * 16;
-    return ok;
+  __device__ __forceinline__ void seek(int step) {
+    pi = 2 * step / tiles_per_page;
+    off = 2 * step - pi * tiles_per_page;
+  }
+  // First cache rows of the step's two 16-key tiles (clamped to a valid place)
+  // and whether the sequence has pages there; then to the next step.
+  __device__ __forceinline__ void next(long long (&row)[2], bool (&ok)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int page = pi < a.b.max_pages ? uniform(table[pi]) : -1;
+      ok[x] = page >= 0 && page < a.c.n_pages;
+      row[x] = (ok[x] ? page : 0) * page_rows + head_row + off * 16;
+      if (++off == tiles_per_page) off = 0, ++pi;
+    }
   }
 
-  __device__ __forceinline__ void load_k(long long ra, long long rb) {
+  // The loads take a uniform base (a tile's first row) and the lane's 32-bit
+  // offset in the tile, which costs no vector instruction.
+  __device__ __forceinline__ void load_k(const long long (&row)[2]) {
     if constexpr (NB == 2) {
-      const long long r = g < 2 ? ra : rb;
-      kc[0] = *(const uint4 *)(a.c.k_q + (r + n) * 32 + (g & 1) * 16);
+      // a tile's codes are 512 bytes: half the lanes to a tile
+      const uint8_t *p = a.c.k_q + (g < 2 ? row[0] : row[1]) * 32;
+      kc[0] = *(const uint4 *)(p + (uint32_t)(n * 32 + (g & 1) * 16));
     } else {
+      const uint32_t o = (uint32_t)(n * (D / 2) + g * 16);
 #pragma unroll
-      for (int j = 0; j < KW / 2; ++j) {
-        kc[j] = *(const uint4 *)(a.c.k_q + (ra + n) * (D / 2) + j * 64 + g * 16);
-        kc[KW / 2 + j] = *(const uint4 *)(a.c.k_q + (rb + n) * (D / 2) + j * 64 + g * 16);
+      for (int j = 0; j < KW; ++j) {
+        const uint8_t *p = a.c.k_q + row[j / (KW / 2)] * (D / 2);
+        kc[j] = *(const uint4 *)(p + o + j % (KW / 2) * 64);
       }
     }
-    ks[0].load(a.c.k_s + (ra + 4 * g) * NB);
-    ks[1].load(a.c.k_s + (rb + 4 * g) * NB);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ks[x].load((const char *)(a.c.k_s + row[x] * NB), (uint32_t)(8 * g * NB));
   }
 
-  __device__ __forceinline__ void load_v(long long ra, long long rb) {
+  __device__ __forceinline__ void load_v(const long long (&row)[2]) {
+    const uint32_t o = (uint32_t)(g * 2 * D + n * NB);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint8_t *p = a.c.v_q + ((j < 4 ? ra : rb) + 4 * g + (j & 3)) * (D / 2) + n * NB;
+      const uint8_t *p = a.c.v_q + row[j >> 2] * (D / 2);
       if constexpr (NB == 2) {
-        vc[j][0] = *(const uint16_t *)p;
+        vc[j][0] = *(const uint16_t *)(p + o + (j & 3) * (D / 2));
       } else if constexpr (NB == 4) {
-        vc[j][0] = *(const uint32_t *)p;
+        vc[j][0] = *(const uint32_t *)(p + o + (j & 3) * (D / 2));
       } else {
-        const uint2 v = *(const uint2 *)p;
+        const uint2 v = *(const uint2 *)(p + o + (j & 3) * (D / 2));
         vc[j][0] = v.x, vc[j][1] = v.y;
       }
     }
-    vs[0].load(a.c.v_s + (ra + 4 * g) * NB);
-    vs[1].load(a.c.v_s + (rb + 4 * g) * NB);
-    const uint16_t *p = a.c.v_s + (lane < 32 ? ra : rb) * NB + (lane & 31) * (NB / 2);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) vs[x].load((const char *)(a.c.v_s + row[x] * NB), (uint32_t)(8 * g * NB));
+    const uint16_t *p = a.c.v_s + (lane < 32 ? row[0] : row[1]) * NB + (lane & 31) * (NB / 2);
     if constexpr (NB == 2) {
       vtop[0] = *p;
     } else if constexpr (NB == 4) {
@@ -280,39 +324,37 @@ struct Attend {
   }
 };
 
-// The workspace holds, per slot (tile, KV head, split): RT rows of D sums; then
-// all slots' references, then their sums of probabilities.
 template <int D, int TY>
-__global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void kv_attend_kernel(KvAttendArgs a, int splits,
-                                                                int aligned) {
+struct Shared {
+  static constexpr int RT = rows_of(TY);
+  float o[kWaves][RT][D + 4];
+  float ref[kWaves][RT], sum[kWaves][RT];
+};
+
+// Steps c0 .. c1 - 1 of a tile and KV head by one workgroup: to `out` when they
+// are all of its steps, else as a part: RT rows of D sums in part_o, their
+// references and sums of probabilities in part_l.
+template <int D, int TY>
+__device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kvh, const Tile &tile,
+                                            int c0, int c1, bool aligned, float *part_o,
+                                            float *part_l, Shared<D, TY> &sh) {
   constexpr int NB = D / 32, PL = parts_of(TY), RT = rows_of(TY);
-  __shared__ float lo[kWaves][RT][D + 4];
-  __shared__ float lref[kWaves][RT], lsum[kWaves][RT];
-  const int G = a.q_heads / a.c.kv_heads;
-  const int kvh = blockIdx.y / splits, split = blockIdx.y % splits;
-  Tile tile;
-  if (!find_tile(a.b, G, RT, blockIdx.x, tile)) return;
   Attend<D, PL> w(a, kvh, tile.s);
   const int n = w.n, g = w.g, wave = uniform(threadIdx.x >> 6);
 
   // the lane's column: row n % RT of the tile, part n / RT of it
   const int row = tile.first + n % RT, tok = row / G, head = kvh * G + row % G;
-  const long long t = (long long)tile.t0 + tok;
-  const bool live = row < tile.rows && t >= 0 && t < a.b.T && tile.past >= 0;
-  const long long cap = min((long long)a.b.max_pages * a.c.page_tokens, (long long)kMaxPos);
-  const int hi = live ? (int)min(tile.past + tok + 1, cap) : 0;
-  const int lo_key =
-      a.window > 0 ? (int)min(max(tile.past + tok + 1 - a.window, 0ll), cap) : 0;
-  // the tile's range: every key some row sees, and the keys every row sees
+  const long long t = (long long)tile.t0 + tok, past = tile.past;
+  const bool live = row < tile.rows && t >= 0 && t < a.b.T;
+  const long long cap = position_cap(a);
+  const int hi = live ? (int)min(past + tok + 1, cap) : 0;
+  const int lo_key = a.window > 0 ? (int)min(max(past + tok + 1 - a.window, 0ll), cap) : 0;
+  // keys that every row sees, and the end of the keys that some row sees
   const int tok0 = tile.first / G, tok1 = (min(tile.first + RT, tile.rows) - 1) / G;
-  const long long past = max(tile.past, 0ll);
-  const int hi_max = tile.past < 0 ? 0 : (int)min(past + tok1 + 1, cap);
-  const int hi_min = (int)min(past + tok0 + 1, cap);
-  const int lo_min = a.window > 0 ? (int)min(max(past + tok0 + 1 - a.window, 0ll), cap) : 0;
+  const int hi_max = (int)min(past + tok1 + 1, cap), hi_min = (int)min(past + tok0 + 1, cap);
   const int lo_max = a.window > 0 ? (int)min(max(past + tok1 + 1 - a.window, 0ll), cap) : 0;
-  const int step0 = lo_min / 32, steps = max(0, (hi_max + 31) / 32 - step0);
-  const int per = (steps + splits * kWaves - 1) / (splits * kWaves);
-  const int i0 = min((split * kWaves + wave) * per, steps), i1 = min(i0 + per, steps);
+  const int per = (c1 - c0 + kWaves - 1) / kWaves;
+  const int i0 = min(c0 + wave * per, c1), i1 = min(i0 + per, c1);
 
   floatx4 O[2 * NB];
 #pragma unroll
@@ -321,10 +363,12 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void k
   int vexp = -14;                    // value scales met so far lie below 2^(vexp + 1)
 
   if (i0 < i1) {
-    long long ra, rb;
-    bool oka = w.tile_row((step0 + i0) * 2, ra), okb = w.tile_row((step0 + i0) * 2 + 1, rb);
-    w.load_k(ra, rb);
-    w.load_v(ra, rb);
+    long long at[2];
+    bool ok[2];
+    w.seek(tile.step0 + i0);
+    w.next(at, ok);
+    w.load_k(at);
+    w.load_v(at);
 
     // q: the column's elements in the codes' order, at the row's power of two
     half8_t Q[NB];
@@ -338,10 +382,10 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void k
         if (aligned) {
           x = load4(a.q, TY, i), y = load4(a.q, TY, i + 16);
         } else {
-          x = make_float4(load1(a.q, TY, i), load1(a.q, TY, i + 1),
-                          load1(a.q, TY, i + 2), load1(a.q, TY, i + 3));
-          y = make_float4(load1(a.q, TY, i + 16), load1(a.q, TY, i + 17),
-                          load1(a.q, TY, i + 18), load1(a.q, TY, i + 19));
+          x = make_float4(load1(a.q, TY, i), load1(a.q, TY, i + 1), load1(a.q, TY, i + 2),
+                          load1(a.q, TY, i + 3));
+          y = make_float4(load1(a.q, TY, i + 16), load1(a.q, TY, i + 17), load1(a.q, TY, i + 18),
+                          load1(a.q, TY, i + 19));
         }
       }
       unit_order(x, y, v[b]);
@@ -362,16 +406,14 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void k
     const float unit = exp2_int(e) * (a.scale * kLog2e);
 
     for (int i = i0; i < i1; ++i) {
-      const int key0 = (step0 + i) * 32;
-      const bool whole = oka && okb && key0 >= lo_max && key0 + 32 <= hi_min;
-      const bool ok_now[2] = {oka, okb};
-      const int nx = min(i + 1, i1 - 1);
-      oka = w.tile_row((step0 + nx) * 2, ra);
-      okb = w.tile_row((step0 + nx) * 2 + 1, rb);
+      const int key0 = (tile.step0 + i) * 32;
+      const bool whole = ok[0] && ok[1] && key0 >= lo_max && key0 + 32 <= hi_min;
+      const bool ok_now[2] = {ok[0], ok[1]};
+      w.next(at, ok);  // past the last step: loaded from a valid place and not used
 
       float s[2][4];
       w.scores(Q, s);
-      w.load_k(ra, rb);
+      w.load_k(at);
 #pragma unroll
       for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -418,15 +460,15 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void k
 #pragma unroll
           for (int j = 0; j < 4; ++j) O[b][j] *= f;
       }
-      const float off = (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
+      const float ref = (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(s[j >> 2][j & 3] - off);
+        p[j] = __builtin_amdgcn_exp2f(s[j >> 2][j & 3] - ref);
         sum += p[j];
       }
       w.weigh(p, O);
-      w.load_v(ra, rb);
+      w.load_v(at);
     }
   }
 
@@ -434,84 +476,104 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 4 : D == 128 ? 3 : 2) void k
   sum = rows_sum(sum);
   const float ref =
       sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
-  if (g == 0 && n < RT) lref[wave][n] = ref, lsum[wave][n] = sum;
+  __syncthreads();  // an earlier part's sums have been read
+  if (g == 0 && n < RT) sh.ref[wave][n] = ref, sh.sum[wave][n] = sum;
 #pragma unroll
   for (int b = 0; b < 2 * NB; ++b) {
     if constexpr (PL == 2) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) O[b][j] += other_half(O[b][j]);
     }
-    if (n < RT) *(floatx4 *)&lo[wave][n][b * 16 + 4 * g] = O[b];
+    if (n < RT) *(floatx4 *)&sh.o[wave][n][b * 16 + 4 * g] = O[b];
   }
   __syncthreads();
-  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * splits + split;
-  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * splits;
-  float *ws = (float *)a.ws;
+  const bool all = c0 == 0 && c1 == tile.steps;
   for (int j = threadIdx.x; j < RT * D / 4; j += kWaves * 64) {
-    const int r = j / (D / 4), d = j % (D / 4) * 4;
-    float best = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < kWaves; ++x) best = fmaxf(best, lref[x][r]);
-    float l = 0.f;
-    floatx4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < kWaves; ++x) {
-      const float f = lref[x][r] == -INFINITY ? 0.f : exp2f(lref[x][r] - best);
-      l = fmaf(f, lsum[x][r], l);
-      const floatx4 v = *(const floatx4 *)&lo[x][r][d];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
-    }
-    if (splits > 1) {
-      *(floatx4 *)(ws + (slot * RT + r) * D + d) = o;
-      if (d == 0) {
-        ws[slots * RT * D + slot * RT + r] = best;
-        ws[slots * RT * (D + 1) + slot * RT + r] = l;
-      }
-    } else {
-      const int rr = tile.first + r, tk = rr / G;
-      const long long tt = (long long)tile.t0 + tk;
-      if (rr < tile.rows && tt >= 0 && tt < a.b.T) {
-        const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) store1(a.out, TY, at + k, l == 0.f ? 0.f : o[k] / l);
-      }
-    }
-  }
-}
-
-// Joins the splits of a tile.
-template <int D, int TY>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int splits) {
-  constexpr int RT = rows_of(TY);
-  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y;
-  Tile tile;
-  if (!find_tile(a.b, G, RT, blockIdx.x, tile)) return;
-  const size_t slot0 = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * splits;
-  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * splits;
-  const float *ws = (const float *)a.ws;
-  const float *refs = ws + slots * RT * D, *sums = refs + slots * RT;
-  for (int j = threadIdx.x; j < RT * D / 4; j += 256) {
     const int r = j / (D / 4), d = j % (D / 4) * 4;
     const int rr = tile.first + r, tk = rr / G;
     const long long tt = (long long)tile.t0 + tk;
     if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
     float best = -INFINITY;
-    for (int x = 0; x < splits; ++x) best = fmaxf(best, refs[(slot0 + x) * RT + r]);
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) best = fmaxf(best, sh.ref[x][r]);
     float l = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int x = 0; x < splits; ++x) {
-      const float ref = refs[(slot0 + x) * RT + r];
-      if (ref == -INFINITY) continue;
-      const float f = exp2f(ref - best);
-      l = fmaf(f, sums[(slot0 + x) * RT + r], l);
-      const floatx4 v = *(const floatx4 *)(ws + ((slot0 + x) * RT + r) * D + d);
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) {
+      const float f = sh.ref[x][r] == -INFINITY ? 0.f : exp2f(sh.ref[x][r] - best);
+      l = fmaf(f, sh.sum[x][r], l);
+      const floatx4 v = *(const floatx4 *)&sh.o[x][r][d];
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
     }
-    const long long at = tt * a.ldo + (kvh * G + rr % G) * D + d;
+    if (all) {
+      const long long to = tt * a.ldo + (kvh * G + rr % G) * D + d;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) store1(a.out, TY, at + k, l == 0.f ? 0.f : o[k] / l);
+      for (int k = 0; k < 4; ++k) store1(a.out, TY, to + k, l == 0.f ? 0.f : o[k] / l);
+    } else {
+      *(floatx4 *)(part_o + r * D + d) = o;
+      if (d == 0) part_l[r] = best, part_l[RT + r] = l;
+    }
+  }
+}
+
+template <int D>
+constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+
+// A workgroup per tile, KV head and part.  The workspace holds RT rows of D sums
+// per part, then the parts' references and sums of probabilities.
+template <int D, int TY>
+__global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_kernel(
+    KvAttendArgs a, int most, int chunk, int aligned) {
+  constexpr int RT = rows_of(TY);
+  __shared__ Shared<D, TY> sh;
+  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y / most, part = blockIdx.y % most;
+  Tile tile;
+  if (!find_tile(a, G, RT, blockIdx.x, tile)) return;
+  const int parts = max(parts_in(tile.steps, chunk), 1);
+  if (part >= parts) return;
+  const int c0 = (int)((long long)tile.steps * part / parts);
+  const int c1 = (int)((long long)tile.steps * (part + 1) / parts);
+  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * most + part;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * most;
+  float *ws = (float *)a.ws;
+  attend_part<D, TY>(a, G, kvh, tile, c0, c1, aligned, ws + slot * RT * D,
+                     ws + slots * RT * D + slot * RT * 2, sh);
+}
+
+// Joins a tile's parts where there are several.
+template <int D, int TY>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int most, int chunk) {
+  constexpr int RT = rows_of(TY);
+  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y;
+  Tile tile;
+  if (!find_tile(a, G, RT, blockIdx.x, tile)) return;
+  const int parts = parts_in(tile.steps, chunk);
+  if (parts < 2) return;
+  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * most;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * most;
+  const float *o_parts = (const float *)a.ws + slot * RT * D;
+  const float *l_parts = (const float *)a.ws + slots * RT * D + slot * RT * 2;
+  for (int j = threadIdx.x; j < RT * D / 4; j += 256) {
+    const int r = j / (D / 4), d = j % (D / 4) * 4;
+    const int rr = tile.first + r;
+    const long long tt = (long long)tile.t0 + rr / G;
+    if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    float best = -INFINITY;
+    for (int x = 0; x < parts; ++x) best = fmaxf(best, l_parts[x * RT * 2 + r]);
+    float l = 0.f;
+    floatx4 o = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < parts; ++x) {
+      const float ref = l_parts[x * RT * 2 + r];
+      const float f = ref == -INFINITY ? 0.f : exp2f(ref - best);
+      l = fmaf(f, l_parts[x * RT * 2 + RT + r], l);
+      const floatx4 v = *(const floatx4 *)(o_parts + ((size_t)x * RT + r) * D + d);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
+    }
+    const long long to = tt * a.ldo + (kvh * G + rr % G) * D + d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store1(a.out, TY, to + k, l == 0.f ? 0.f : o[k] / l);
   }
 }
 
@@ -519,15 +581,36 @@ long long tiles_bound(const KvCache &c, const KvBatch &b, int type, int q_heads)
   return (long long)b.T * (q_heads / c.kv_heads) / rows_of(type) + b.n_seqs;
 }
 
+#ifndef CHUNK
+#define CHUNK 64
+#endif
+struct Split {
+  int most, chunk;  // parts of the longest possible row; steps of a part at most
+};
+
+Split split_of(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
+  const long long groups = tiles_bound(c, b, type, q_heads) * c.kv_heads;
+  long long len = (long long)b.max_pages * c.page_tokens;
+  // a tile of RT rows spans at most RT tokens beside the window
+  if (window > 0 && window + 16ll < len) len = window + 16ll;
+  const long long steps = len / 32 + 2;
+  long long chunk = groups * steps / 1024;
+  if (chunk > CHUNK) chunk = CHUNK;
+  if (chunk < 8) chunk = 8;
+  if (chunk < (steps + 63) / 64) chunk = (steps + 63) / 64;
+  return {(int)((steps + chunk - 1) / chunk), (int)chunk};
+}
+
 template <int D, int TY>
 hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
-  const int splits = kv_attend_splits(a.c, a.b, a.type, a.q_heads, a.window);
-  const long long tiles = tiles_bound(a.c, a.b, a.type, a.q_heads);
+  const auto [most, chunk] = split_of(a.c, a.b, a.type, a.q_heads, a.window);
+  const unsigned tiles = (unsigned)tiles_bound(a.c, a.b, a.type, a.q_heads);
   const int al = (uintptr_t)a.q % (4 * type_bytes(a.type)) == 0 && a.ldq % 4 == 0;
-  kv_attend_kernel<D, TY><<<dim3((unsigned)tiles, (unsigned)(a.c.kv_heads * splits)), kWaves * 64,
-                            0, s>>>(a, splits, al);
-  if (splits > 1)
-    kv_join_kernel<D, TY><<<dim3((unsigned)tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, splits);
+  kv_attend_kernel<D, TY><<<dim3(tiles, (unsigned)(a.c.kv_heads * most)), kWaves * 64, 0, s>>>(
+      a, most, chunk, al);
+  if (most > 1)
+    kv_join_kernel<D, TY>
+        <<<dim3(tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, most, chunk);
   return hipGetLastError();
 }
 
@@ -540,22 +623,10 @@ hipError_t launch_dim(const KvAttendArgs &a, hipStream_t s) {
 
 }  // namespace
 
-int kv_attend_splits(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
-  // enough workgroups for the chip, each wave with two steps of 32 keys at the
-  // table's length at least
-  const long long groups = tiles_bound(c, b, type, q_heads) * c.kv_heads;
-  long long len = (long long)b.max_pages * c.page_tokens;
-  if (window > 0 && window + 64 < len) len = window + 64;
-  const long long most = (len + 64 * kWaves - 1) / (64 * kWaves), want = (1024 + groups - 1) / groups;
-  long long n = want < most ? want : most;
-  if (n > 32) n = 32;
-  return n < 1 ? 1 : (int)n;
-}
-
 size_t kv_attend_ws_bytes(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
-  const int splits = kv_attend_splits(c, b, type, q_heads, window);
-  if (splits == 1) return 0;
-  return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * splits * rows_of(type) *
+  const int most = split_of(c, b, type, q_heads, window).most;
+  if (most == 1) return 0;
+  return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * most * rows_of(type) *
          (c.head_dim + 2) * sizeof(float);
 }
 
