@@ -166,7 +166,6 @@ struct Attend {
   const int lane, n, g, tiles_per_page;
   const long long page_rows, head_row;  // cache rows of a page, and before the KV head's in it
   const int32_t *table;  // the sequence's pages
-  const CodeBits bits;
   int pi, off;  // the cursor: next step's first 16-key tile as page index and tile in the page
   // a step's codes and scales
   uint4 kc[KW];
@@ -242,27 +241,38 @@ struct Attend {
     }
   }
 
-  // Scores of the step's keys, as the matrix cores leave them: s[x][i] is key
-  // 4 g + i of tile x against the lane's column.
+  // Scores of the step's keys in units of `unit`, as the matrix cores leave them:
+  // s[x][i] is key 4 g + i of tile x against the lane's column.
   __device__ __forceinline__ void scores(const half8_t (&Q)[NB], float (&s)[2][4]) const {
+    constexpr int per = NB == 2 ? 2 : 4;  // blocks of a transposed word group
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
     const floatx4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < KW; ++j) {
-      const uint4 t = transpose_rows(kc[j]);
-      const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+    for (int h = 0; h < NB / per; ++h) {
+      uint32_t w[2][4];
+      const uint4 t = transpose_rows(kc[h]);
+      if constexpr (NB == 2) {  // both tiles' two blocks in one group
+        w[0][0] = t.x, w[0][1] = t.y, w[1][0] = t.z, w[1][1] = t.w;
+      } else {
+        const uint4 u = transpose_rows(kc[KW / 2 + h]);
+        w[0][0] = t.x, w[0][1] = t.y, w[0][2] = t.z, w[0][3] = t.w;
+        w[1][0] = u.x, w[1][1] = u.y, w[1][2] = u.z, w[1][3] = u.w;
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        // item k: NB 2: (tile k / 2, block k % 2); else block 4 (j % (KW / 2)) + k of tile j / (KW / 2)
-        const int x = NB == 2 ? k >> 1 : j / (KW > 1 ? KW / 2 : 1);
-        const int b = NB == 2 ? k & 1 : (j % (KW > 1 ? KW / 2 : 1)) * 4 + k;
-        const floatx4 c =
-            __builtin_amdgcn_mfma_f32_16x16x32_f16(decode_word(bits, w[k]), Q[b], z, 0, 0, 0);
+      for (int k = 0; k < per; ++k) {
+        const int b = h * per + k;
+        // -8 times the block's sum of q, which the codes' offset takes away
+        const floatx4 m = __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::minus_eight(), Q[b], z, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
+        for (int x = 0; x < 2; ++x) {
+          const floatx4 c =
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::word(w[x][k]), Q[b], m, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
+        }
       }
     }
     if constexpr (PL == 2) {
@@ -283,13 +293,15 @@ struct Attend {
     return half2_t{x, (_Float16)fmaf(p1, s1, 0.f)};
   }
 
-  // O += V^T P^T for the step's probabilities p (key j of K slot j).
-  __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB]) const {
+  // O += V^T P^T for the step's probabilities p (key j of K slot j), with the codes
+  // as they are; off[b] sums what their offset of 8 multiplies.
+  __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB],
+                                        float (&off)[NB]) const {
     const uint32_t lo_part = PL == 2 && n >= 8 ? 0xffffffffu : 0u;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       half2_t P[4];
-      half2_t A[2][4];
+      uint32_t A[2][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const Scales<NB> &sc = vs[j >> 1];
@@ -312,14 +324,15 @@ struct Attend {
         // keys 2 j and 2 j + 1: the half of their words that holds block b
         const uint32_t w0 = vc[2 * j][b / 4], w1 = vc[2 * j + 1][b / 4];
         const uint32_t w = __builtin_amdgcn_perm(w1, w0, (b & 2) ? 0x07060302u : 0x05040100u);
-        A[0][j] = bits.low(b & 1 ? w >> 8 : w);
-        A[1][j] = bits.high(b & 1 ? w >> 8 : w);
+        A[0][j] = RawCodes::low(b & 1 ? w >> 8 : w);
+        A[1][j] = RawCodes::high(b & 1 ? w >> 8 : w);
+        off[b] = __builtin_amdgcn_fdot2(h, half2_t{(_Float16)1.f, (_Float16)1.f}, off[b], false);
       }
       const half8_t B = join8(P[0], P[1], P[2], P[3]);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         O[2 * b + h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            join8(A[h][0], A[h][1], A[h][2], A[h][3]), B, O[2 * b + h], 0, 0, 0);
+            RawCodes::join(A[h][0], A[h][1], A[h][2], A[h][3]), B, O[2 * b + h], 0, 0, 0);
     }
   }
 };
@@ -359,7 +372,10 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   floatx4 O[2 * NB];
 #pragma unroll
   for (int b = 0; b < 2 * NB; ++b) O[b] = floatx4{0.f, 0.f, 0.f, 0.f};
-  float top = -INFINITY, sum = 0.f;  // running maximum (log2 units) and sum
+  float off[NB] = {};
+  // running maximum (in units of `unit`) and sum
+  float top = -INFINITY, sum = 0.f;
+  float unit = 1.f;
   int vexp = -14;                    // value scales met so far lie below 2^(vexp + 1)
 
   if (i0 < i1) {
@@ -394,16 +410,19 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
         big = max(big, __builtin_bit_cast(uint32_t, v[b][j]) & 0x7fffffffu);
     }
     const int e = scale_exp(rows_max_u32(big));
-    const float f = exp2_int(-e);
+    const float f = a.scale == 0.f ? 0.f : a.scale < 0.f ? -exp2_int(-e) : exp2_int(-e);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         _Float16 x, y;
-        split_half(v[b][j] * f, x, y);
+        split_half(v[b][j] * (f * RawCodes::slot(j)), x, y);
         Q[b][j] = PL == 2 && n >= 8 ? y : x;
       }
-    const float unit = exp2_int(e) * (a.scale * kLog2e);
+    // a score's unit in log2: positive (a negative scale is q's sign), the codes'
+    // 2^24 in it.  (Beyond 2^116 in q the unit saturates: such rows' scores differ
+    // by far more than an exponential tells apart.)
+    unit = fmaxf(exp2_int(min(e + 24, 126)) * fabsf(a.scale * kLog2e), 1e-37f);
 
     for (int i = i0; i < i1; ++i) {
       const int key0 = (tile.step0 + i) * 32;
@@ -414,10 +433,6 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       float s[2][4];
       w.scores(Q, s);
       w.load_k(at);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[x][j] *= unit;
       if (!whole) {
         // keys the row does not see; and places that hold no key of the
         // sequence, whose scales may be anything
@@ -437,11 +452,13 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       }
       float m = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      if (__any(m > top + kSlack)) {
+      if (__any((m - top) * unit > kSlack)) {
         const float to = fmaxf(top, rows_max(m));
-        const float f = to == -INFINITY ? 1.f : exp2f(top - to);
+        const float f = to == -INFINITY ? 1.f : exp2f((top - to) * unit);
         top = to;
         sum *= f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) off[b] *= f;
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
@@ -456,18 +473,20 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
         vexp = uniform(to);
         sum *= f;
 #pragma unroll
+        for (int b = 0; b < NB; ++b) off[b] *= f;
+#pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
           for (int j = 0; j < 4; ++j) O[b][j] *= f;
       }
-      const float ref = (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
+      const float ref = fmaf(top == -INFINITY ? 0.f : top, unit, (float)(vexp - kHead));
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(s[j >> 2][j & 3] - ref);
+        p[j] = __builtin_amdgcn_exp2f(fmaf(s[j >> 2][j & 3], unit, -ref));
         sum += p[j];
       }
-      w.weigh(p, O);
+      w.weigh(p, O, off);
       w.load_v(at);
     }
   }
@@ -475,11 +494,16 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   // join the waves: reference of the column's sums, -inf when it saw no key
   sum = rows_sum(sum);
   const float ref =
-      sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + (float)(vexp - kHead);
+      sum == 0.f ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, unit, (float)(vexp - kHead));
   __syncthreads();  // an earlier part's sums have been read
   if (g == 0 && n < RT) sh.ref[wave][n] = ref, sh.sum[wave][n] = sum;
 #pragma unroll
   for (int b = 0; b < 2 * NB; ++b) {
+    // the sums of the raw codes (units of 2^-24, of 2^-20 for the second nibbles)
+    // without their offset of 8
+    const float eight = 8.f * rows_sum(off[b / 2]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) O[b][j] = fmaf(O[b][j], b & 1 ? 0x1p20f : 0x1p24f, -eight);
     if constexpr (PL == 2) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) O[b][j] += other_half(O[b][j]);

@@ -50,6 +50,29 @@ __device__ __forceinline__ half8_t decode_word(const CodeBits &c, uint32_t w) {
   return join8(c.low(w), c.high(w), c.low(w >> 8), c.high(w >> 8));
 }
 
+// Codes as the matrix cores can take them without any arithmetic: a nibble q in
+// the low bits of a half is the subnormal q 2^-24, one in the next four bits 16 q
+// 2^-24, and the products of subnormals are exact.  The second nibbles' factor
+// 16 is for the other operand or the result to take away, as are the 2^-24 and
+// the codes' offset of 8.
+struct RawCodes {
+  static __device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000f000fu; }
+  static __device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x00f000f0u; }
+  static __device__ __forceinline__ half8_t join(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __builtin_bit_cast(half8_t, make_uint4(a, b, c, d));
+  }
+  // A word in decode_word's order; K slots 2, 3, 6 and 7 hold 16 times the code.
+  static __device__ __forceinline__ half8_t word(uint32_t w) {
+    return join(low(w), high(w), low(w >> 8), high(w >> 8));
+  }
+  // -8 as a word's slots would hold it.
+  static __device__ __forceinline__ half8_t minus_eight() {
+    return join(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);
+  }
+  // What slot j of the other operand is multiplied by.
+  static __device__ __forceinline__ constexpr float slot(int j) { return j & 2 ? 0.0625f : 1.f; }
+};
+
 // Puts x[4 g .. 4 g + 3] (a) and x[4 g + 16 .. 4 g + 19] (b) into decode_word's order.
 __device__ __forceinline__ void unit_order(const float4 a, const float4 b, float (&v)[8]) {
   v[0] = a.x, v[1] = a.z, v[2] = b.x, v[3] = b.z;

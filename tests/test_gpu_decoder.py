@@ -450,6 +450,7 @@ def check_attend(c, q, pages, start, past, scale, window, got, ty, rows=None):
         kk = o.q4_decode(np.concatenate([kq[pc, :, at % P] & 15, kq[pc, :, at % P] >> 4], -1), ks[pc, :, at % P])
         vt = vq[pc, :, at % P].transpose(0, 1, 3, 2)
         vv = o.q4_decode(np.concatenate([vt & 15, vt >> 4], -1), vs[pc, :, at % P])
+        sk, sv = (np.repeat(np.abs(a[pc, :, at % P].astype(np.float64)), 32, -1) for a in (ks, vs))
         for t in range(int(st[s]), int(st[s + 1])):
             if rows is not None and t not in rows:
                 continue
@@ -469,13 +470,18 @@ def check_attend(c, q, pages, start, past, scale, window, got, ty, rows=None):
                 p = np.exp(z - z.max())
                 p /= p.sum()
                 # a score: 32 products a block, D / 32 scaled adds, the pair of query parts (2^-22) and three
-                # factors; its exponential carries the absolute error of score and reference plus 2 ulp
-                dz = (32 + D // 32 + 8) * U + 2.0 ** -22
-                ep = 2 * (dz * mag + 4 * U * (np.abs(z) + np.abs(z.max()))) + 8 * U
+                # factors; its exponential carries the absolute error of score and reference plus 2 ulp.
+                # The products are of codes 0..15 as stored and the offset of 8 is subtracted as a sum of its
+                # own, so a rounding is u of up to (15 + 8) scale |q|, whatever |code - 8| is
+                raw = 23 * sk[idx, h // G] @ np.abs(qn[t, h]) * abs(scale)
+                dz = (32 + D // 32 + 8) * U
+                ep = 2 * (dz * raw + 2.0 ** -22 * mag + 4 * U * (np.abs(z) + np.abs(z.max()))) + 8 * U
                 # the weighted sum: probabilities times scales in binary16 (one part for half-width types, a
                 # pair for float32), sums of n terms; both sums share the probabilities' error
                 part = 2.0 ** -11 if ty != "f32" else 2.0 ** -21
-                avg = np.abs(vh).T @ (p * (2 * ep + 2 * (ep * p).sum() + part + 2 * (n + 40) * U))
+                avg = np.abs(vh).T @ (p * (2 * ep + 2 * (ep * p).sum() + part))
+                # its roundings likewise: u of up to 23 scale p a term
+                avg += 2 * (n + 40) * U * 23 * (sv[idx, h // G].T @ p)
                 tol = avg + n * 2.0 ** -32 * np.abs(vh).max() * p.max()
                 tol = tol + HALF[ty] * (np.abs(ref[h]) + tol) + float(torch.finfo(TYPES[ty]).smallest_normal)
                 bad = np.abs(gn[t, h] - ref[h]) / tol
