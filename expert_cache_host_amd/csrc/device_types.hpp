@@ -37,10 +37,16 @@ __device__ __forceinline__ void store1(void *p, int type, long long i, float v) 
     ((uint16_t *)p)[i] = type == kBf16 ? f32_to_bf16(v) : f32_to_f16(v);
 }
 
-// Four elements from an address aligned to four elements.
+// Four elements in one access, at any address aligned to one (the hardware takes
+// vector accesses at any byte).
 __device__ __forceinline__ float4 load4(const void *p, int type, long long i) {
-  if (type == kF32) return *(const float4 *)((const float *)p + i);
-  const uint2 b = *(const uint2 *)((const uint16_t *)p + i);
+  float4 v;
+  if (type == kF32) {
+    __builtin_memcpy(&v, (const float *)p + i, 16);
+    return v;
+  }
+  uint2 b;
+  __builtin_memcpy(&b, (const uint16_t *)p + i, 8);
   if (type == kBf16)
     return make_float4(bf16_to_f32(b.x & 0xffffu), bf16_to_f32(b.x >> 16),
                        bf16_to_f32(b.y & 0xffffu), bf16_to_f32(b.y >> 16));
@@ -50,7 +56,7 @@ __device__ __forceinline__ float4 load4(const void *p, int type, long long i) {
 
 __device__ __forceinline__ void store4(void *p, int type, long long i, float4 v) {
   if (type == kF32) {
-    *(float4 *)((float *)p + i) = v;
+    __builtin_memcpy((float *)p + i, &v, 16);
     return;
   }
   uint2 b;
@@ -61,22 +67,37 @@ __device__ __forceinline__ void store4(void *p, int type, long long i, float4 v)
     b.x = f32_to_f16(v.x) | ((uint32_t)f32_to_f16(v.y) << 16);
     b.y = f32_to_f16(v.z) | ((uint32_t)f32_to_f16(v.w) << 16);
   }
-  *(uint2 *)((uint16_t *)p + i) = b;
+  __builtin_memcpy((uint16_t *)p + i, &b, 8);
 }
 
+// The same for the last n < 4 elements of a row; the missing ones are 0.
+__device__ __forceinline__ float4 load_few(const void *p, int type, long long i, int n) {
+  return make_float4(load1(p, type, i), n > 1 ? load1(p, type, i + 1) : 0.f,
+                     n > 2 ? load1(p, type, i + 2) : 0.f, 0.f);
+}
+__device__ __forceinline__ void store_few(void *p, int type, long long i, float4 v, int n) {
+  store1(p, type, i, v.x);
+  if (n > 1) store1(p, type, i + 1, v.y);
+  if (n > 2) store1(p, type, i + 2, v.z);
+}
+
+constexpr int kMaxPos = 0x7fffff00;  // positions from here on are out of the cache
+
 // Sequence of packed row t (the last s with start[s] <= t), or -1 for a row
-// before the first or behind the last sequence.
+// before the first or behind the last sequence: 64 sequences are compared at a
+// time (one load's latency for up to 64 of them, two up to 4096).  Every lane of
+// the wave takes part.
 __device__ __forceinline__ int seq_of_row(const KvBatch &b, int t) {
-  if (t < b.start[0] || t >= b.start[b.n_seqs]) return -1;
-  int lo = 0, hi = b.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (b.start[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = b.n_seqs;  // the last s in [lo, hi) with start[s] <= t
+  const int first = b.start[0], end = b.start[b.n_seqs];
+  while (hi - lo > 1) {
+    const int each = (hi - lo + 63) / 64, s = lo + lane * each;
+    const bool before = s < hi && b.start[min(s, hi - 1)] <= t;
+    lo += (max(__popcll(__ballot(before)), 1) - 1) * each;
+    hi = min(hi, lo + each);
   }
-  return lo;
+  return t < first || t >= end ? -1 : __builtin_amdgcn_readfirstlane(lo);
 }
 
 }  // namespace moe

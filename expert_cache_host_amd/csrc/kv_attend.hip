@@ -38,7 +38,6 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kMaxPos = 0x7fffff00;  // positions from here on are out of the cache
 constexpr float kLog2e = 1.4426950408889634f;
 // Probabilities stand at 2^kHead over the running maximum's, and may rise by
 // 2^kSlack before the maximum is raised: with scales below 2 a product stays
@@ -349,7 +348,7 @@ struct Shared {
 // references and sums of probabilities in part_l.
 template <int D, int TY>
 __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kvh, const Tile &tile,
-                                            int c0, int c1, bool aligned, float *part_o,
+                                            int c0, int c1, float *part_o,
                                             float *part_l, Shared<D, TY> &sh) {
   constexpr int NB = D / 32, PL = parts_of(TY), RT = rows_of(TY);
   Attend<D, PL> w(a, kvh, tile.s);
@@ -395,14 +394,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (live) {
         const long long i = t * a.ldq + head * D + b * 32 + 4 * g;
-        if (aligned) {
-          x = load4(a.q, TY, i), y = load4(a.q, TY, i + 16);
-        } else {
-          x = make_float4(load1(a.q, TY, i), load1(a.q, TY, i + 1), load1(a.q, TY, i + 2),
-                          load1(a.q, TY, i + 3));
-          y = make_float4(load1(a.q, TY, i + 16), load1(a.q, TY, i + 17), load1(a.q, TY, i + 18),
-                          load1(a.q, TY, i + 19));
-        }
+        x = load4(a.q, TY, i), y = load4(a.q, TY, i + 16);
       }
       unit_order(x, y, v[b]);
 #pragma unroll
@@ -548,7 +540,7 @@ constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 // per part, then the parts' references and sums of probabilities.
 template <int D, int TY>
 __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_kernel(
-    KvAttendArgs a, int most, int chunk, int aligned) {
+    KvAttendArgs a, int most, int chunk) {
   constexpr int RT = rows_of(TY);
   __shared__ Shared<D, TY> sh;
   const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y / most, part = blockIdx.y % most;
@@ -561,7 +553,7 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_ke
   const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * most + part;
   const size_t slots = (size_t)gridDim.x * a.c.kv_heads * most;
   float *ws = (float *)a.ws;
-  attend_part<D, TY>(a, G, kvh, tile, c0, c1, aligned, ws + slot * RT * D,
+  attend_part<D, TY>(a, G, kvh, tile, c0, c1, ws + slot * RT * D,
                      ws + slots * RT * D + slot * RT * 2, sh);
 }
 
@@ -629,9 +621,8 @@ template <int D, int TY>
 hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
   const auto [most, chunk] = split_of(a.c, a.b, a.type, a.q_heads, a.window);
   const unsigned tiles = (unsigned)tiles_bound(a.c, a.b, a.type, a.q_heads);
-  const int al = (uintptr_t)a.q % (4 * type_bytes(a.type)) == 0 && a.ldq % 4 == 0;
   kv_attend_kernel<D, TY><<<dim3(tiles, (unsigned)(a.c.kv_heads * most)), kWaves * 64, 0, s>>>(
-      a, most, chunk, al);
+      a, most, chunk);
   if (most > 1)
     kv_join_kernel<D, TY>
         <<<dim3(tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, most, chunk);

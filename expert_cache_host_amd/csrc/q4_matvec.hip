@@ -36,28 +36,18 @@ template <int PL, int KT, int FI>
 struct Matvec {
   const Q4MatvecArgs &a;
   const int lane, n, g, wave, waves, nb, t0, parts;
-  const bool aligned;  // x's rows allow loads of four elements
   half8_t X[KT * 4];  // the lane's part, 8 K slots of every block
   float xs[FI];       // 2^e of the parts in this lane's C registers
 
-  __device__ Matvec(const Q4MatvecArgs &args, int first_token, bool al)
+  __device__ Matvec(const Q4MatvecArgs &args, int first_token)
       : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), wave(threadIdx.x >> 6),
         waves(blockDim.x >> 6), nb(args.cols / 32), t0(first_token),
-        parts(min(args.T - first_token, 4 * FI / PL) * PL), aligned(al) {}
+        parts(min(args.T - first_token, 4 * FI / PL) * PL) {}
 
   // Word gg of a block of token t, in the codes' order.
   __device__ __forceinline__ void load_unit(int t, int block, int gg, float (&v)[8]) const {
     const long long i = (long long)t * a.ldx + block * 32 + 4 * gg;
-    float4 p, q;
-    if (aligned) {
-      p = load4(a.x, a.type, i);
-      q = load4(a.x, a.type, i + 16);
-    } else {
-      p = make_float4(load1(a.x, a.type, i), load1(a.x, a.type, i + 1), load1(a.x, a.type, i + 2),
-                      load1(a.x, a.type, i + 3));
-      q = make_float4(load1(a.x, a.type, i + 16), load1(a.x, a.type, i + 17),
-                      load1(a.x, a.type, i + 18), load1(a.x, a.type, i + 19));
-    }
+    const float4 p = load4(a.x, a.type, i), q = load4(a.x, a.type, i + 16);
     unit_order(p, q, v);
   }
 
@@ -138,12 +128,11 @@ struct Matvec {
 
 // GB: blocks per scale; RB: row tiles per visit, above 1 when K takes passes.
 template <int PL, int KT, int FI, int GB, int RB>
-__global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4MatvecArgs a, int passes,
-                                                                         int aligned) {
+__global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4MatvecArgs a, int passes) {
   __shared__ float red[2][kMaxWaves][FI * 64];
   // FI == 1: the waves' units of x on their way to X
   __shared__ uint4 units[FI == 1 ? (KT == 4 ? 12 : kMaxWaves) : 1][4][KT * 16 + 4];
-  Matvec<PL, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL), aligned);
+  Matvec<PL, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL));
   auto stage = [&](int first) {
     if constexpr (FI == 1)
       m.stage_few(first, units[m.wave]);
@@ -244,49 +233,48 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
 }
 
 template <int PL, int KT, int FI, int GB>
-hipError_t launch_one(const Q4MatvecArgs &a, int waves, int passes, bool aligned, hipStream_t s) {
+hipError_t launch_one(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
   const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / PL;
   const unsigned gy = (unsigned)((a.T + tokens - 1) / tokens);
   if (KT < 4 || passes == 1) {
     const dim3 grid((unsigned)min(tiles, 512), gy);
-    q4_matvec_kernel<PL, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1, aligned);
+    q4_matvec_kernel<PL, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1);
   } else if constexpr (KT == 4) {
     const dim3 grid((unsigned)min((tiles + 3) / 4, 512), gy);
-    q4_matvec_kernel<PL, KT, FI, GB, 4><<<grid, waves * 64, 0, s>>>(a, passes, aligned);
+    q4_matvec_kernel<PL, KT, FI, GB, 4><<<grid, waves * 64, 0, s>>>(a, passes);
   }
   return hipGetLastError();
 }
 
 template <int PL, int KT, int FI>
-hipError_t launch_group(const Q4MatvecArgs &a, int waves, int passes, bool al, hipStream_t s) {
-  if (a.group == 32) return launch_one<PL, KT, FI, 1>(a, waves, passes, al, s);
-  if (a.group == 64) return launch_one<PL, KT, FI, 2>(a, waves, passes, al, s);
-  return launch_one<PL, KT, FI, 4>(a, waves, passes, al, s);
+hipError_t launch_group(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
+  if (a.group == 32) return launch_one<PL, KT, FI, 1>(a, waves, passes, s);
+  if (a.group == 64) return launch_one<PL, KT, FI, 2>(a, waves, passes, s);
+  return launch_one<PL, KT, FI, 4>(a, waves, passes, s);
 }
 
 template <int PL, int KT>
-hipError_t launch_parts(const Q4MatvecArgs &a, int waves, int passes, bool al, hipStream_t s) {
+hipError_t launch_parts(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
   const int parts = a.T * PL;
-  if (parts <= 4) return launch_group<PL, KT, 1>(a, waves, passes, al, s);
-  if (parts <= 8) return launch_group<PL, KT, 2>(a, waves, passes, al, s);
-  return launch_group<PL, KT, 4>(a, waves, passes, al, s);
+  if (parts <= 4) return launch_group<PL, KT, 1>(a, waves, passes, s);
+  if (parts <= 8) return launch_group<PL, KT, 2>(a, waves, passes, s);
+  return launch_group<PL, KT, 4>(a, waves, passes, s);
 }
 
 template <int PL>
-hipError_t launch_cols(const Q4MatvecArgs &a, bool al, hipStream_t s) {
+hipError_t launch_cols(const Q4MatvecArgs &a, hipStream_t s) {
   const int chunks = (a.cols / 32 + 3) / 4;
-  if (chunks <= 16) return launch_parts<PL, 1>(a, chunks, 1, al, s);
-  if (chunks <= 32) return launch_parts<PL, 2>(a, (chunks + 1) / 2, 1, al, s);
-  if (chunks <= 48) return launch_parts<PL, 4>(a, (chunks + 3) / 4, 1, al, s);
+  if (chunks <= 16) return launch_parts<PL, 1>(a, chunks, 1, s);
+  if (chunks <= 32) return launch_parts<PL, 2>(a, (chunks + 1) / 2, 1, s);
+  if (chunks <= 48) return launch_parts<PL, 4>(a, (chunks + 3) / 4, 1, s);
   const int passes = (chunks + 47) / 48;
-  return launch_parts<PL, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, al, s);
+  return launch_parts<PL, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, s);
 }
 
 }  // namespace
 
 hipError_t launch_q4_matvec(const Q4MatvecArgs &a, hipStream_t s) {
-  const bool al = (uintptr_t)a.x % (4 * type_bytes(a.type)) == 0 && a.ldx % 4 == 0;
-  return a.type == kF32 ? launch_cols<2>(a, al, s) : launch_cols<1>(a, al, s);
+  return a.type == kF32 ? launch_cols<2>(a, s) : launch_cols<1>(a, s);
 }
 
 }  // namespace moe

@@ -54,23 +54,27 @@ def _library():
     return _lib
 
 
-class _on:
-    """Makes `device` and the call's stream current (so that what the call allocates
-    belongs to that stream) and yields the raw stream."""
+# the current stream's handle by device index (a Stream object costs a microsecond)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
+
+class _At:
+    """Makes a device and a stream current, so that the launch and what the call allocates
+    belong to them; yields the raw stream."""
+
+    def __init__(self, index, stream):
+        self.guards = [torch.cuda.device(index)]
         if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
             self.guards.append(torch.cuda.stream(stream))
+        self.index = index
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -78,26 +82,60 @@ class _on:
         return False
 
 
-def _rows(t, name, device, d=None, dtype=None):
-    """Checks a [rows, d] tensor with contiguous rows; returns its row stride."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 2 or (d is not None and t.shape[1] != d):
-        raise ValueError(f"{name} must be [rows, {'d' if d is None else d}]")
+class _Here:
+    """The same where both are current already."""
+
+    def __init__(self, index):
+        self.raw = _raw_stream(index)
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *exc):
+        return False
+
+
+def _on(index, stream):
+    if stream is None and torch.cuda.current_device() == index:
+        return _Here(index)
+    return _At(index, stream)
+
+
+def _fault(t, name, index, rows, d, dtype):
+    if t.get_device() != index:
+        return f"{name} is on {t.device}, not on cuda:{index}"
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (d is not None and t.shape[1] != d):
+        return f"{name} must be [{'rows' if rows is None else rows}, {'d' if d is None else d}], not {list(t.shape)}"
     if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
+        return f"{name}'s rows must be contiguous"
     if dtype is None:
-        if t.dtype not in _TYPES:
-            raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    elif t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    return t.stride(0)
+        return f"{name} must be float32, bfloat16 or float16"
+    return f"{name} must be {dtype}"
+
+
+def _rows(t, name, index, rows=None, d=None, dtype=None):
+    """Checks a [rows, d] tensor with contiguous rows; returns its row stride."""
+    shape = t.shape
+    if t.get_device() == index and len(shape) == 2 and (rows is None or shape[0] == rows) and \
+            (d is None or shape[1] == d) and (t.dtype in _TYPES if dtype is None else t.dtype == dtype):
+        st = t.stride()
+        if st[1] == 1 or shape[1] <= 1:
+            return st[0]
+    raise ValueError(_fault(t, name, index, rows, d, dtype))
 
 
 def _cuda(t, name):
-    if not t.is_cuda:
+    i = t.get_device()
+    if i < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
-    return t.device
+    return i
+
+
+def _weight(w, name, index, d):
+    if w.get_device() != index or w.dtype != torch.float32 or w.dim() != 1 or w.shape[0] != d or \
+            not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous float32 [{d}] on cuda:{index}")
+    return w.data_ptr()
 
 
 def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: float = 1.0,
@@ -117,54 +155,53 @@ def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: floa
     dev = _cuda(h, "h")
     ldh = _rows(h, "h", dev)
     T, d = h.shape
-    if y is None and (post_w is not None or gate is not None):
-        raise ValueError("post_w and gate need y")
-    ldy = yt = ldg = gt = 0
+    hd = xd = h.dtype
+    yp = gp = wp = vp = hp = xp = None
+    ldy = yt = ldg = gt = ldho = ldx = xt = 0
     if y is not None:
-        ldy = _rows(y, "y", dev, d)
-        yt = _TYPES[y.dtype]
-        if y.shape[0] != T:
-            raise ValueError("y must have h's rows")
-    if gate is not None:
-        if gate.dim() == 1:
-            ldg = _rows(gate.unsqueeze(0), "gate", dev, d) * 0
-        else:
-            ldg = _rows(gate, "gate", dev, d)
-            if gate.shape[0] != T:
-                raise ValueError("gate must be [d] or have h's rows")
-        gt = _TYPES[gate.dtype]
-    for w, name in ((post_w, "post_w"), (pre_w, "pre_w")):
-        if w is not None and (w.device != dev or w.dtype != torch.float32 or w.dim() != 1 or
-                              w.shape[0] != d or not w.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous float32 [d] on {dev}")
-    if x_out is not None and pre_w is None:
+        ldy = _rows(y, "y", dev, T, d)
+        xd = y.dtype
+        yt = _TYPES[xd]
+        yp = y.data_ptr()
+        if gate is not None:
+            if gate.dim() == 1:
+                _rows(gate.unsqueeze(0), "gate", dev, 1, d)
+            else:
+                ldg = _rows(gate, "gate", dev, T, d)
+            gt = _TYPES[gate.dtype]
+            gp = gate.data_ptr()
+        if post_w is not None:
+            wp = _weight(post_w, "post_w", dev, d)
+    elif post_w is not None or gate is not None:
+        raise ValueError("post_w and gate need y")
+    if pre_w is not None:
+        vp = _weight(pre_w, "pre_w", dev, d)
+    elif x_out is not None:
         raise ValueError("x_out needs pre_w")
     keep = y is None and res_scale == 1.0 and h_out is None
     if keep and pre_w is None:
         raise ValueError("nothing to compute: y and pre_w are None")
     with _on(dev, stream) as s:
-        if h_out is None:
-            if not keep:
-                h_out = torch.empty((T, d), dtype=h.dtype, device=dev)
-        elif h_out.shape[0] != T:
-            raise ValueError("h_out must have h's shape")
-        x = x_out
-        if pre_w is not None and x is None:
-            x = torch.empty((T, d), device=dev, dtype=x_dtype or (h if y is None else y).dtype)
-        ldx = xt = ldho = 0
-        if x is not None:
-            ldx = _rows(x, "x_out", dev, d, x_dtype)
-            xt = _TYPES[x.dtype]
-            if x.shape[0] != T:
-                raise ValueError("x_out must have h's shape")
         if h_out is not None:
-            ldho = _rows(h_out, "h_out", dev, d, h.dtype)
-        _check(_library().moe_block_norm(
-            h.data_ptr(), _TYPES[h.dtype], ldh, None if y is None else y.data_ptr(), yt, ldy,
-            None if post_w is None else post_w.data_ptr(), None if gate is None else gate.data_ptr(),
-            gt, ldg, None if pre_w is None else pre_w.data_ptr(), T, d, res_scale, block_scale, eps,
-            None if h_out is None else h_out.data_ptr(), ldho, None if x is None else x.data_ptr(), xt,
-            ldx, s))
+            ldho = _rows(h_out, "h_out", dev, T, d, hd)
+            hp = h_out.data_ptr()
+        elif not keep:
+            h_out = torch.empty((T, d), dtype=hd, device=h.device)
+            ldho, hp = d, h_out.data_ptr()
+        x = x_out
+        if x is not None:
+            ldx = _rows(x, "x_out", dev, T, d, x_dtype)
+            xt, xp = _TYPES[x.dtype], x.data_ptr()
+        elif pre_w is not None:
+            xd = x_dtype or xd
+            if xd not in _TYPES:
+                raise ValueError("x_dtype must be float32, bfloat16 or float16")
+            x = torch.empty((T, d), dtype=xd, device=h.device)
+            ldx, xt, xp = d, _TYPES[xd], x.data_ptr()
+        rc = _library().moe_block_norm(h.data_ptr(), _TYPES[hd], ldh, yp, yt, ldy, wp, gp, gt, ldg, vp, T, d,
+                                       res_scale, block_scale, eps, hp, ldho, xp, xt, ldx, s)
+        if rc:
+            _check(rc)
     return (h if keep else h_out), x
 
 
@@ -178,14 +215,15 @@ class Q4Matrix:
                 not codes.is_contiguous():
             raise ValueError("codes must be contiguous uint8 [rows, cols / 32, 16]")
         self.rows, self.cols = codes.shape[0], codes.shape[1] * 32
-        if scales.device != dev or scales.dtype != torch.float16 or scales.dim() != 2 or \
+        if scales.get_device() != dev or scales.dtype != torch.float16 or scales.dim() != 2 or \
                 scales.shape[0] != self.rows or not scales.is_contiguous():
             raise ValueError("scales must be contiguous float16 [rows, cols / group] beside the codes")
         if self.rows < 1 or scales.shape[1] < 1 or \
                 scales.shape[1] * (g := self.cols // scales.shape[1]) != self.cols or g not in (32, 64, 128):
             raise ValueError("scales must hold one scale per 32, 64 or 128 weights")
         self.group = g
-        self.codes, self.scales, self.device = codes, scales, dev
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self._index = dev
         self._head = (codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, g)
 
     @classmethod
@@ -206,19 +244,18 @@ class Q4Matrix:
 
 def q4_matvec(x, w: Q4Matrix, out=None, stream=None):
     """out [T, rows] = x [T, cols] times w transposed, in x's type (float32 sums)."""
-    dev = w.device
-    ldx = _rows(x, "x", dev, w.cols)
-    T = x.shape[0]
+    dev = w._index
+    ldx = _rows(x, "x", dev, None, w.cols)
+    T, dt = x.shape[0], x.dtype
     with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((T, w.rows), dtype=x.dtype, device=dev)
+            out = torch.empty((T, w.rows), dtype=dt, device=w.device)
             ldo = w.rows
         else:
-            ldo = _rows(out, "out", dev, w.rows, x.dtype)
-            if out.shape[0] != T:
-                raise ValueError("out must have x's rows")
-        _check(_library().moe_q4_matvec(*w._head, x.data_ptr(), _TYPES[x.dtype], ldx, T, out.data_ptr(),
-                                        ldo, s))
+            ldo = _rows(out, "out", dev, T, w.rows, dt)
+        rc = _library().moe_q4_matvec(*w._head, x.data_ptr(), _TYPES[dt], ldx, T, out.data_ptr(), ldo, s)
+        if rc:
+            _check(rc)
     return out
 
 
@@ -245,12 +282,13 @@ class KVCache:
                 "v_codes": (v_codes, torch.uint8, (n, h, p, 16, nb)),
                 "v_scales": (v_scales, torch.float16, (n, h, p, nb))}
         for name, (t, dtype, shape) in want.items():
-            if t.device != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on {dev}")
+            if t.get_device() != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on cuda:{dev}")
         if n < 1 or h < 1 or h > 1024 or p < 16 or p % 16 or p > 65536 or nb not in (2, 4, 8):
             raise ValueError("head_dim must be 64, 128 or 256, page_tokens a multiple of 16 up to 65536, "
                              "kv_heads at most 1024")
-        self.device, self.tensors = dev, (k_codes, k_scales, v_codes, v_scales)
+        self.device, self.tensors = k_codes.device, (k_codes, k_scales, v_codes, v_scales)
+        self._index = dev
         self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = n, h, p, nb * 32
         self._c = _KvCache(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                            v_scales.data_ptr(), n, p, h, nb * 32)
@@ -267,94 +305,98 @@ class KVCache:
                    z((nb,), torch.float16))
 
     def _batch(self, pages, start, past, rows):
-        dev = self.device
-        for t, name in ((pages, "pages"), (start, "start"), (past, "past")):
-            if t.device != dev or t.dtype != torch.int32 or not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous int32 on {dev}")
-        if pages.dim() != 2 or start.dim() != 1 or past.dim() != 1:
-            raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1], past [n_seqs]")
-        n, m = pages.shape
-        if n < 1 or m < 1 or start.shape[0] != n + 1 or past.shape[0] != n:
-            raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1], past [n_seqs]")
+        dev, i32 = self._index, torch.int32
+        n, m = pages.shape if pages.dim() == 2 else (0, 0)
+        if pages.get_device() != dev or start.get_device() != dev or past.get_device() != dev or \
+                pages.dtype != i32 or start.dtype != i32 or past.dtype != i32 or \
+                n < 1 or m < 1 or start.shape != (n + 1,) or past.shape != (n,) or \
+                not (pages.is_contiguous() and start.is_contiguous() and past.is_contiguous()):
+            raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1] and past [n_seqs], "
+                             f"contiguous int32 on cuda:{dev}")
         return _KvBatch(pages.data_ptr(), start.data_ptr(), past.data_ptr(), n, m, rows)
 
     def append(self, k, v, pages, start, past, q=None, inv_freq=None, interleaved: bool = False,
                q_out=None, stream=None):
         """Writes k, v [T, kv_heads * head_dim] into the cache, the keys rotated by their
         positions (inv_freq float32 [rot_dim / 2] or None); returns q [T, q_heads * head_dim]
-        rotated likewise, or None."""
-        dev, D = self.device, self.head_dim
-        ldk = _rows(k, "k", dev, self.kv_heads * D)
-        T, dt = k.shape[0], k.dtype
-        ldv = _rows(v, "v", dev, self.kv_heads * D, dt)
-        if v.shape[0] != T:
-            raise ValueError("v must have k's rows")
-        rot = 0
+        rotated likewise, or None.  Rows of no sequence are left as they are in `q_out`
+        (undefined in a new one)."""
+        dev, D, dt = self._index, self.head_dim, k.dtype
+        ldk = _rows(k, "k", dev, None, self.kv_heads * D)
+        T = k.shape[0]
+        ldv = _rows(v, "v", dev, T, self.kv_heads * D, dt)
+        rot, fp = 0, None
         if inv_freq is not None:
             rot = 2 * inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-            if rot < 0 or rot > D or inv_freq.dtype != torch.float32 or inv_freq.device != dev or \
+            if rot < 0 or rot > D or inv_freq.dtype != torch.float32 or inv_freq.get_device() != dev or \
                     not inv_freq.is_contiguous():
-                raise ValueError(f"inv_freq must be contiguous float32 [rot_dim / 2] on {dev}, rot_dim <= head_dim")
+                raise ValueError("inv_freq must be contiguous float32 [rot_dim / 2] beside the cache, "
+                                 "rot_dim <= head_dim")
+            fp = inv_freq.data_ptr() if rot else None
         b = self._batch(pages, start, past, T)
+        qp = op = None
         ldq = ldqo = heads = 0
-        if q is None:
-            if q_out is not None:
-                raise ValueError("q_out needs q")
-        else:
-            ldq = _rows(q, "q", dev, None, dt)
-            heads = self._heads(q, T)
+        if q is not None:
+            ldq = _rows(q, "q", dev, T, None, dt)
+            heads, qp = self._heads(q), q.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
         with _on(dev, stream) as s:
             if q is not None:
                 if q_out is None:
-                    q_out = torch.empty((T, heads * D), dtype=dt, device=dev)
-                ldqo = _rows(q_out, "q_out", dev, heads * D, dt)
-                if q_out.shape[0] != T:
-                    raise ValueError("q_out must have q's rows")
-            _check(_library().moe_kv_append(
-                self._cp, b, _TYPES[dt], k.data_ptr(), ldk, v.data_ptr(), ldv,
-                inv_freq.data_ptr() if rot else None, rot, 1 if interleaved else 0,
-                None if q is None else q.data_ptr(), ldq, heads,
-                None if q is None else q_out.data_ptr(), ldqo, s))
+                    q_out = torch.empty((T, heads * D), dtype=dt, device=self.device)
+                    ldqo = heads * D
+                else:
+                    ldqo = _rows(q_out, "q_out", dev, T, heads * D, dt)
+                op = q_out.data_ptr()
+            rc = _library().moe_kv_append(self._cp, b, _TYPES[dt], k.data_ptr(), ldk, v.data_ptr(), ldv, fp, rot,
+                                          1 if interleaved else 0, qp, ldq, heads, op, ldqo, s)
+            if rc:
+                _check(rc)
         return q_out
 
-    def _heads(self, q, T) -> int:
-        n, D = q.shape[1], self.head_dim
-        if q.shape[0] != T or n < 1 or n % (self.kv_heads * D):
+    def _heads(self, q) -> int:
+        n = q.shape[1]
+        if n < 1 or n % (self.kv_heads * self.head_dim):
             raise ValueError("q must be [T, q_heads * head_dim], q_heads a multiple of kv_heads")
-        return n // D
+        return n // self.head_dim
 
     def read(self, pages, start, past, rows: int, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(k, v) float32 [rows, kv_heads, head_dim]: the values the cache holds for the
         batch's rows (0 in a hole; undefined for rows of no sequence)."""
-        b = self._batch(pages, start, past, rows)
         if rows < 0:
             raise ValueError("rows must be >= 0")
-        with _on(self.device, stream) as s:
+        b = self._batch(pages, start, past, rows)
+        with _on(self._index, stream) as s:
             k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
             v = torch.empty_like(k)
-            _check(_library().moe_kv_read(self._cp, b, k.data_ptr(), v.data_ptr(), s))
+            rc = _library().moe_kv_read(self._cp, b, k.data_ptr(), v.data_ptr(), s)
+            if rc:
+                _check(rc)
         return k, v
 
     def attend(self, q, pages, start, past, scale: float, window: int = 0, out=None, stream=None):
         """out [T, q_heads * head_dim] = softmax(scale * q K^T) V over the keys each row
         sees: positions up to its own, within `window` when window > 0.  Rows of no sequence
         are left as they are in `out` (undefined in a new one)."""
-        dev, D = self.device, self.head_dim
+        dev, dt = self._index, q.dtype
         ldq = _rows(q, "q", dev)
-        T = q.shape[0]
-        heads = self._heads(q, T)
+        T, n = q.shape
+        heads = self._heads(q)
         b = self._batch(pages, start, past, T)
-        lib, ty = _library(), _TYPES[q.dtype]
+        lib, ty = _library(), _TYPES[dt]
         with _on(dev, stream) as s:
             if out is None:
-                out = torch.empty((T, heads * D), dtype=q.dtype, device=dev)
-            ldo = _rows(out, "out", dev, heads * D, q.dtype)
-            if out.shape[0] != T:
-                raise ValueError("out must have q's rows")
-            n = lib.moe_kv_attend_workspace(self._cp, b, ty, heads, window)
-            if n < 0:
-                _check(n)
-            ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-            _check(lib.moe_kv_attend(self._cp, b, ty, q.data_ptr(), ldq, heads, scale, window,
-                                     out.data_ptr(), ldo, None if ws is None else ws.data_ptr(), n, s))
+                out = torch.empty((T, n), dtype=dt, device=self.device)
+                ldo = n
+            else:
+                ldo = _rows(out, "out", dev, T, n, dt)
+            need = lib.moe_kv_attend_workspace(self._cp, b, ty, heads, window)
+            if need < 0:
+                _check(need)
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+            rc = lib.moe_kv_attend(self._cp, b, ty, q.data_ptr(), ldq, heads, scale, window, out.data_ptr(), ldo,
+                                   ws.data_ptr() if need else None, need, s)
+            if rc:
+                _check(rc)
         return out
