@@ -16,6 +16,8 @@
 // columns in registers for the whole launch and streams its slice of 16 rows
 // after 16 rows, the next tile's loads in flight while the present one is
 // multiplied; the waves' sums meet in LDS, a barrier per tile.
+#include <algorithm>
+
 #include "device_types.hpp"
 #include "q4_tile.hpp"
 
@@ -30,10 +32,14 @@ constexpr int kMaxWaves = 16;
 // tokens need few scaled adds.
 __device__ __forceinline__ int part_of_row(int m) { return 4 * (m & 3) + (m >> 2); }
 
-// PL: binary16 parts per token; KT: chunks of 4 blocks per wave and pass; FI: C
-// registers in use (4 FI parts).
-template <int PL, int KT, int FI>
+// Binary16 parts of a token.
+constexpr int parts_of(int type) { return type == kF32 ? 2 : 1; }
+
+// TY: element type; KT: chunks of 4 blocks per wave and pass; FI: C registers in
+// use (4 FI parts).
+template <int TY, int KT, int FI>
 struct Matvec {
+  static constexpr int PL = parts_of(TY);
   const Q4MatvecArgs &a;
   const int lane, n, g, wave, waves, nb, t0, parts;
   half8_t X[KT * 4];  // the lane's part, 8 K slots of every block
@@ -44,11 +50,16 @@ struct Matvec {
         waves(blockDim.x >> 6), nb(args.cols / 32), t0(first_token),
         parts(min(args.T - first_token, 4 * FI / PL) * PL) {}
 
-  // Word gg of a block of token t, in the codes' order.
-  __device__ __forceinline__ void load_unit(int t, int block, int gg, float (&v)[8]) const {
-    const long long i = (long long)t * a.ldx + block * 32 + 4 * gg;
-    const float4 p = load4(a.x, a.type, i), q = load4(a.x, a.type, i + 16);
+  // Word gg of a block of token t, in the codes' order; zeros unless `live`.  The
+  // load is from a valid place either way: a branch around it would make the
+  // loads wait for each other.
+  __device__ __forceinline__ void load_unit(bool live, int t, int block, int gg, float (&v)[8]) const {
+    const long long i = (long long)min(t, a.T - 1) * a.ldx + min(block, nb - 1) * 32 + 4 * gg;
+    const float4 p = load4(a.x, TY, i), q = load4(a.x, TY, i + 16);
     unit_order(p, q, v);
+    live = live && block < nb;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = live ? v[j] : 0.f;
   }
 
   // The wave's K slice of every token into X and xs; `first` is its first block.
@@ -59,10 +70,10 @@ struct Matvec {
     const int u = part_of_row(n), t = t0 + u / PL, p = u % PL;
     const bool mine = u < parts;
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll
     for (int b = 0; b < KT * 4; ++b) {
-      float v[8] = {};
-      if (mine && first + b < nb) load_unit(t, first + b, g, v);
+      float v[8];
+      load_unit(mine, t, first + b, g, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
     }
@@ -70,8 +81,8 @@ struct Matvec {
     const float f = exp2_int(-e);
 #pragma unroll
     for (int b = 0; b < KT * 4; ++b) {
-      float v[8] = {};
-      if (mine && first + b < nb) load_unit(t, first + b, g, v);
+      float v[8];
+      load_unit(mine, t, first + b, g, v);
       _Float16 hi[8], lo[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) split_half(v[j] * f, hi[j], lo[j]);
@@ -86,14 +97,20 @@ struct Matvec {
   // Up to four parts: a lane converts one unit (word g' of block b') of each
   // token, and the wave shares them through its own LDS, where a lane then reads
   // the units of its row of A.
-  __device__ __forceinline__ void stage_few(int first, uint4 (*buf)[KT * 16 + 4]) {
+  // (All tokens' loads go out together, and ahead of the weights': loads return in
+  // order.)
+  __device__ __forceinline__ void load_few(int first, float (&x)[4 / PL][8]) const {
+#pragma unroll
+    for (int t = 0; t < 4 / PL; ++t)
+      load_unit(lane < KT * 16, t0 + t, first + (lane >> 2), lane & 3, x[t]);
+  }
+  __device__ __forceinline__ void stage_few(const float (&xt)[4 / PL][8], uint4 (*buf)[KT * 16 + 4]) {
     const int b = lane >> 2, u = part_of_row(n);
     xs[0] = 1.f;
 #pragma unroll
     for (int t = 0; t < 4 / PL; ++t) {
       if (t * PL >= parts) break;
-      float v[8] = {};
-      if (b < KT * 4 && first + b < nb) load_unit(t0 + t, first + b, lane & 3, v);
+      const float(&v)[8] = xt[t];
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
@@ -127,18 +144,13 @@ struct Matvec {
 };
 
 // GB: blocks per scale; RB: row tiles per visit, above 1 when K takes passes.
-template <int PL, int KT, int FI, int GB, int RB>
+template <int TY, int KT, int FI, int GB, int RB>
 __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4MatvecArgs a, int passes) {
+  constexpr int PL = parts_of(TY);
   __shared__ float red[2][kMaxWaves][FI * 64];
   // FI == 1: the waves' units of x on their way to X
   __shared__ uint4 units[FI == 1 ? (KT == 4 ? 12 : kMaxWaves) : 1][4][KT * 16 + 4];
-  Matvec<PL, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL));
-  auto stage = [&](int first) {
-    if constexpr (FI == 1)
-      m.stage_few(first, units[m.wave]);
-    else
-      m.stage_many(first);
-  };
+  Matvec<TY, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL));
   const int tiles = (a.rows + 15) / 16, nb = m.nb, per_pass = m.waves * KT * 4;
   uint4 w[RB > 1 ? 1 : 2][KT];
   uint32_t s[RB > 1 ? 1 : 2][KT];
@@ -189,14 +201,21 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
           const int u = t * PL + p;
           v += red[buf][x][(u >> 2) * 64 + (u & 3) * 16 + (j & 15)];
         }
-      if (row < a.rows) store1(a.out, a.type, (long long)(m.t0 + t) * a.ldo + row, v);
+      if (row < a.rows) store1(a.out, TY, (long long)(m.t0 + t) * a.ldo + row, v);
     }
   };
   if constexpr (RB == 1) {
     const int first = m.wave * KT * 4;
     int tile = blockIdx.x, it = 0;
-    load(tile, first, w[0], s[0]);
-    stage(first);
+    if constexpr (FI == 1) {
+      float x[4 / PL][8];
+      m.load_few(first, x);
+      load(tile, first, w[0], s[0]);
+      m.stage_few(x, units[m.wave]);
+    } else {
+      load(tile, first, w[0], s[0]);
+      m.stage_many(first);
+    }
     for (; tile < tiles; tile += gridDim.x, ++it) {
       load(min(tile + (int)gridDim.x, tiles - 1), first, w[1], s[1]);
       float acc[FI] = {};
@@ -215,7 +234,13 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
       float acc[RB][FI] = {};
       for (int p = 0; p < passes; ++p) {
         const int first = p * per_pass + m.wave * KT * 4;
-        stage(first);
+        if constexpr (FI == 1) {
+          float x[4 / PL][8];
+          m.load_few(first, x);
+          m.stage_few(x, units[m.wave]);
+        } else {
+          m.stage_many(first);
+        }
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
           load(min(tile + r, tiles - 1), first, w[0], s[0]);
@@ -232,49 +257,53 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
   }
 }
 
-template <int PL, int KT, int FI, int GB>
+template <int TY, int KT, int FI, int GB>
 hipError_t launch_one(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
-  const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / PL;
-  const unsigned gy = (unsigned)((a.T + tokens - 1) / tokens);
-  if (KT < 4 || passes == 1) {
-    const dim3 grid((unsigned)min(tiles, 512), gy);
-    q4_matvec_kernel<PL, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1);
-  } else if constexpr (KT == 4) {
-    const dim3 grid((unsigned)min((tiles + 3) / 4, 512), gy);
-    q4_matvec_kernel<PL, KT, FI, GB, 4><<<grid, waves * 64, 0, s>>>(a, passes);
-  }
+  constexpr int RB = 4;  // row tiles a visit when K takes passes
+  const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / parts_of(TY);
+  const int gy = (a.T + tokens - 1) / tokens, visits = passes == 1 ? tiles : (tiles + RB - 1) / RB;
+  // as many workgroups as the chip holds at a time, each with the same number of
+  // tiles, so that the tokens are laid out no more often than that
+  const int fit = (KT == 4 ? 12 : KT == 2 ? 16 : 32) / waves;
+  const int most = std::max(1, 256 * std::max(1, fit) / gy), each = (visits + most - 1) / most;
+  const dim3 grid((unsigned)((visits + each - 1) / each), (unsigned)gy);
+  if (KT < 4 || passes == 1)
+    q4_matvec_kernel<TY, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1);
+  else if constexpr (KT == 4)
+    q4_matvec_kernel<TY, KT, FI, GB, RB><<<grid, waves * 64, 0, s>>>(a, passes);
   return hipGetLastError();
 }
 
-template <int PL, int KT, int FI>
+template <int TY, int KT, int FI>
 hipError_t launch_group(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
-  if (a.group == 32) return launch_one<PL, KT, FI, 1>(a, waves, passes, s);
-  if (a.group == 64) return launch_one<PL, KT, FI, 2>(a, waves, passes, s);
-  return launch_one<PL, KT, FI, 4>(a, waves, passes, s);
+  if (a.group == 32) return launch_one<TY, KT, FI, 1>(a, waves, passes, s);
+  if (a.group == 64) return launch_one<TY, KT, FI, 2>(a, waves, passes, s);
+  return launch_one<TY, KT, FI, 4>(a, waves, passes, s);
 }
 
-template <int PL, int KT>
+template <int TY, int KT>
 hipError_t launch_parts(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
-  const int parts = a.T * PL;
-  if (parts <= 4) return launch_group<PL, KT, 1>(a, waves, passes, s);
-  if (parts <= 8) return launch_group<PL, KT, 2>(a, waves, passes, s);
-  return launch_group<PL, KT, 4>(a, waves, passes, s);
+  const int parts = a.T * parts_of(TY);
+  if (parts <= 4) return launch_group<TY, KT, 1>(a, waves, passes, s);
+  if (parts <= 8) return launch_group<TY, KT, 2>(a, waves, passes, s);
+  return launch_group<TY, KT, 4>(a, waves, passes, s);
 }
 
-template <int PL>
+template <int TY>
 hipError_t launch_cols(const Q4MatvecArgs &a, hipStream_t s) {
   const int chunks = (a.cols / 32 + 3) / 4;
-  if (chunks <= 16) return launch_parts<PL, 1>(a, chunks, 1, s);
-  if (chunks <= 32) return launch_parts<PL, 2>(a, (chunks + 1) / 2, 1, s);
-  if (chunks <= 48) return launch_parts<PL, 4>(a, (chunks + 3) / 4, 1, s);
+  if (chunks <= 4) return launch_parts<TY, 1>(a, chunks, 1, s);
+  if (chunks <= 32) return launch_parts<TY, 2>(a, (chunks + 1) / 2, 1, s);
+  if (chunks <= 48) return launch_parts<TY, 4>(a, (chunks + 3) / 4, 1, s);
   const int passes = (chunks + 47) / 48;
-  return launch_parts<PL, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, s);
+  return launch_parts<TY, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, s);
 }
 
 }  // namespace
 
 hipError_t launch_q4_matvec(const Q4MatvecArgs &a, hipStream_t s) {
-  return a.type == kF32 ? launch_cols<2>(a, s) : launch_cols<1>(a, s);
+  if (a.type == kF32) return launch_cols<kF32>(a, s);
+  return a.type == kBf16 ? launch_cols<kBf16>(a, s) : launch_cols<kF16>(a, s);
 }
 
 }  // namespace moe
