@@ -160,6 +160,19 @@ struct Scales {  // 4 keys' block scales, as they lie in memory
 template <int D, int PL>
 struct Attend {
   static constexpr int NB = D / 32;
+  // Half-width types take the codes as they are, with their offset of 8 summed
+  // apart; float32 takes them minus 8: keys and values of either sign cancel in
+  // the sums and the offset would not, which costs float32 more than a digit over a
+  // few hundred keys (an error of 4.6e-6 against 1.3e-7).
+  static constexpr bool kRaw = PL == 1;
+  const CodeBits bits;
+  __device__ __forceinline__ half8_t codes_of(uint32_t w) const {
+    if constexpr (kRaw) return RawCodes::word(w);
+    return decode_word(bits, w);
+  }
+  // What slot j of q and a score's unit are multiplied by.
+  static __device__ __forceinline__ constexpr float slot(int j) { return kRaw ? RawCodes::slot(j) : 1.f; }
+  static constexpr int kUnitBits = kRaw ? 24 : 0;
   static constexpr int KW = NB >= 4 ? NB / 2 : 1;  // 16-byte loads of 32 keys' codes per lane
   const KvAttendArgs &a;
   const int lane, n, g, tiles_per_page;
@@ -263,12 +276,14 @@ struct Attend {
 #pragma unroll
       for (int k = 0; k < per; ++k) {
         const int b = h * per + k;
-        // -8 times the block's sum of q, which the codes' offset takes away
-        const floatx4 m = __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::minus_eight(), Q[b], z, 0, 0, 0);
+        // raw: -8 times the block's sum of q, which the codes' offset takes away
+        floatx4 m = z;
+        if constexpr (kRaw)
+          m = __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::minus_eight(), Q[b], z, 0, 0, 0);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const floatx4 c =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::word(w[x][k]), Q[b], m, 0, 0, 0);
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(w[x][k]), Q[b], m, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
         }
@@ -292,8 +307,8 @@ struct Attend {
     return half2_t{x, (_Float16)fmaf(p1, s1, 0.f)};
   }
 
-  // O += V^T P^T for the step's probabilities p (key j of K slot j), with the codes
-  // as they are; off[b] sums what their offset of 8 multiplies.
+  // O += V^T P^T for the step's probabilities p (key j of K slot j); with raw codes
+  // off[b] sums what their offset of 8 multiplies.
   __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB],
                                         float (&off)[NB]) const {
     const uint32_t lo_part = PL == 2 && n >= 8 ? 0xffffffffu : 0u;
@@ -323,9 +338,14 @@ struct Attend {
         // keys 2 j and 2 j + 1: the half of their words that holds block b
         const uint32_t w0 = vc[2 * j][b / 4], w1 = vc[2 * j + 1][b / 4];
         const uint32_t w = __builtin_amdgcn_perm(w1, w0, (b & 2) ? 0x07060302u : 0x05040100u);
-        A[0][j] = RawCodes::low(b & 1 ? w >> 8 : w);
-        A[1][j] = RawCodes::high(b & 1 ? w >> 8 : w);
-        off[b] = __builtin_amdgcn_fdot2(h, half2_t{(_Float16)1.f, (_Float16)1.f}, off[b], false);
+        if constexpr (kRaw) {
+          A[0][j] = RawCodes::low(b & 1 ? w >> 8 : w);
+          A[1][j] = RawCodes::high(b & 1 ? w >> 8 : w);
+          off[b] = __builtin_amdgcn_fdot2(h, half2_t{(_Float16)1.f, (_Float16)1.f}, off[b], false);
+        } else {
+          A[0][j] = __builtin_bit_cast(uint32_t, bits.low(b & 1 ? w >> 8 : w));
+          A[1][j] = __builtin_bit_cast(uint32_t, bits.high(b & 1 ? w >> 8 : w));
+        }
       }
       const half8_t B = join8(P[0], P[1], P[2], P[3]);
 #pragma unroll
@@ -408,13 +428,13 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         _Float16 x, y;
-        split_half(v[b][j] * (f * RawCodes::slot(j)), x, y);
+        split_half(v[b][j] * (f * Attend<D, PL>::slot(j)), x, y);
         Q[b][j] = PL == 2 && n >= 8 ? y : x;
       }
-    // a score's unit in log2: positive (a negative scale is q's sign), the codes'
-    // 2^24 in it.  (Beyond 2^116 in q the unit saturates: such rows' scores differ
+    // a score's unit in log2: positive (a negative scale is q's sign), the raw
+    // codes' 2^24 in it.  (Beyond 2^116 in q the unit saturates: such rows' scores differ
     // by far more than an exponential tells apart.)
-    unit = fmaxf(exp2_int(min(e + 24, 126)) * fabsf(a.scale * kLog2e), 1e-37f);
+    unit = fmaxf(exp2_int(min(e + Attend<D, PL>::kUnitBits, 126)) * fabsf(a.scale * kLog2e), 1e-37f);
 
     for (int i = i0; i < i1; ++i) {
       const int key0 = (tile.step0 + i) * 32;
@@ -493,9 +513,11 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   for (int b = 0; b < 2 * NB; ++b) {
     // the sums of the raw codes (units of 2^-24, of 2^-20 for the second nibbles)
     // without their offset of 8
-    const float eight = 8.f * rows_sum(off[b / 2]);
+    if constexpr (Attend<D, PL>::kRaw) {
+      const float eight = 8.f * rows_sum(off[b / 2]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) O[b][j] = fmaf(O[b][j], b & 1 ? 0x1p20f : 0x1p24f, -eight);
+      for (int j = 0; j < 4; ++j) O[b][j] = fmaf(O[b][j], b & 1 ? 0x1p20f : 0x1p24f, -eight);
+    }
     if constexpr (PL == 2) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) O[b][j] += other_half(O[b][j]);
