@@ -137,13 +137,17 @@ __device__ __forceinline__ float other_half(float v) {
       float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x128, 0xF, 0xF, true));
 }
 
+// Block scales of 4 keys.  Every one of a tile's 16 rows of A needs those of 4
+// keys in 16 lanes each, so a lane loads its share of a step's scales once (NB
+// bytes), the wave puts them into its LDS and the lanes read what they need: a
+// sixteenth of the loads, and registers only while the scales are used.
 template <int NB>
-struct Scales {  // 4 keys' block scales, as they lie in memory
+struct Scales {
   uint32_t w[2 * NB];
-  __device__ __forceinline__ void load(const char *tile, uint32_t offset) {
+  __device__ __forceinline__ void read(const char *p) {
 #pragma unroll
     for (int i = 0; i < NB / 2; ++i) {
-      const uint4 v = *(const uint4 *)(tile + offset + 16 * i);
+      const uint4 v = *(const uint4 *)(p + 16 * i);
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
@@ -151,9 +155,36 @@ struct Scales {  // 4 keys' block scales, as they lie in memory
     const half2_t h = __builtin_bit_cast(half2_t, w[(key * NB + b) / 2]);
     return (float)h[(key * NB + b) & 1];
   }
-  __device__ __forceinline__ void drop(int key) {
-#pragma unroll
-    for (int i = 0; i < NB / 2; ++i) w[key * NB / 2 + i] = 0;
+};
+
+// A lane's share of a step's scales: NB / 2 of key (lane % 32) / 2 of tile lane / 32.
+template <int NB>
+struct Share {
+  uint32_t w[NB == 8 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint16_t *scales, const long long (&row)[2], int lane) {
+    const uint16_t *p = scales + (lane < 32 ? row[0] : row[1]) * NB + (lane & 31) * (NB / 2);
+    if constexpr (NB == 2) {
+      w[0] = *p;
+    } else if constexpr (NB == 4) {
+      w[0] = *(const uint32_t *)p;
+    } else {
+      const uint2 v = *(const uint2 *)p;
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void write(char *lds, int lane) const {
+    if constexpr (NB == 2)
+      *(uint16_t *)(lds + lane * NB) = (uint16_t)w[0];
+    else if constexpr (NB == 4)
+      *(uint32_t *)(lds + lane * NB) = w[0];
+    else
+      *(uint2 *)(lds + lane * NB) = make_uint2(w[0], w[1]);
+  }
+  // Bits of the largest magnitude in it.
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = max(w[0] & 0x7fffu, (w[0] >> 16) & 0x7fffu);
+    if constexpr (NB == 8) m = max(m, max(w[1] & 0x7fffu, (w[1] >> 16) & 0x7fffu));
+    return m;
   }
 };
 
@@ -181,15 +212,15 @@ struct Attend {
   int pi, off;  // the cursor: next step's first 16-key tile as page index and tile in the page
   // a step's codes and scales
   uint4 kc[KW];
-  Scales<NB> ks[2], vs[2];
+  Share<NB> sk, sv;
+  char *lds;  // the wave's room for a step's scales: keys', then values'
   uint32_t vc[8][NB == 8 ? 2 : 1];
-  uint32_t vtop[NB == 8 ? 2 : 1];  // one share of the step's value scales
 
-  __device__ Attend(const KvAttendArgs &args, int kv_head, int s)
+  __device__ Attend(const KvAttendArgs &args, int kv_head, int s, char *room)
       : a(args), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4),
         tiles_per_page(args.c.page_tokens / 16),
         page_rows((long long)args.c.kv_heads * args.c.page_tokens),
-        head_row((long long)kv_head * args.c.page_tokens), table(args.b.pages + (long long)s * args.b.max_pages) {}
+        head_row((long long)kv_head * args.c.page_tokens), table(args.b.pages + (long long)s * args.b.max_pages), lds(room) {}
 
   __device__ __forceinline__ void seek(int step) {
     pi = 2 * step / tiles_per_page;
@@ -222,8 +253,7 @@ struct Attend {
         kc[j] = *(const uint4 *)(p + o + j % (KW / 2) * 64);
       }
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) ks[x].load((const char *)(a.c.k_s + row[x] * NB), (uint32_t)(8 * g * NB));
+    sk.load(a.c.k_s, row, lane);
   }
 
   __device__ __forceinline__ void load_v(const long long (&row)[2]) {
@@ -240,17 +270,7 @@ struct Attend {
         vc[j][0] = v.x, vc[j][1] = v.y;
       }
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) vs[x].load((const char *)(a.c.v_s + row[x] * NB), (uint32_t)(8 * g * NB));
-    const uint16_t *p = a.c.v_s + (lane < 32 ? row[0] : row[1]) * NB + (lane & 31) * (NB / 2);
-    if constexpr (NB == 2) {
-      vtop[0] = *p;
-    } else if constexpr (NB == 4) {
-      vtop[0] = *(const uint32_t *)p;
-    } else {
-      const uint2 v = *(const uint2 *)p;
-      vtop[0] = v.x, vtop[1] = v.y;
-    }
+    sv.load(a.c.v_s, row, lane);
   }
 
   // Scores of the step's keys in units of `unit`, as the matrix cores leave them:
@@ -261,6 +281,9 @@ struct Attend {
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
+    Scales<NB> ks[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ks[x].read(lds + (16 * x + 4 * g) * NB * 2);
     const floatx4 z = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int h = 0; h < NB / per; ++h) {
@@ -312,6 +335,9 @@ struct Attend {
   __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB],
                                         float (&off)[NB]) const {
     const uint32_t lo_part = PL == 2 && n >= 8 ? 0xffffffffu : 0u;
+    Scales<NB> vs[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) vs[x].read(lds + 64 * NB + (16 * x + 4 * g) * NB * 2);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       half2_t P[4];
@@ -361,6 +387,7 @@ struct Shared {
   static constexpr int RT = rows_of(TY);
   float o[kWaves][RT][D + 4];
   float ref[kWaves][RT], sum[kWaves][RT];
+  __attribute__((aligned(16))) char scales[kWaves][128 * (D / 32)];
 };
 
 // Steps c0 .. c1 - 1 of a tile and KV head by one workgroup: to `out` when they
@@ -371,8 +398,9 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
                                             int c0, int c1, float *part_o,
                                             float *part_l, Shared<D, TY> &sh) {
   constexpr int NB = D / 32, PL = parts_of(TY), RT = rows_of(TY);
-  Attend<D, PL> w(a, kvh, tile.s);
-  const int n = w.n, g = w.g, wave = uniform(threadIdx.x >> 6);
+  const int wave = uniform(threadIdx.x >> 6);
+  Attend<D, PL> w(a, kvh, tile.s, sh.scales[wave]);
+  const int n = w.n, g = w.g;
 
   // the lane's column: row n % RT of the tile, part n / RT of it
   const int row = tile.first + n % RT, tok = row / G, head = kvh * G + row % G;
@@ -442,25 +470,29 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       const bool ok_now[2] = {ok[0], ok[1]};
       w.next(at, ok);  // past the last step: loaded from a valid place and not used
 
+      if (!whole) {
+        // places that hold no key of the sequence, whose scales may be anything
+        const int key = key0 + (w.lane >> 1);
+        if (!((w.lane < 32 ? ok_now[0] : ok_now[1]) && key < hi_max)) {
+          w.sv.w[0] = 0;
+          if constexpr (NB == 8) w.sv.w[1] = 0;
+        }
+      }
+      w.sk.write(w.lds, w.lane);
+      w.sv.write(w.lds + 64 * NB, w.lane);
+      const uint32_t sb = w.sv.top();
       float s[2][4];
       w.scores(Q, s);
       w.load_k(at);
       if (!whole) {
-        // keys the row does not see; and places that hold no key of the
-        // sequence, whose scales may be anything
+        // keys the row does not see
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = key0 + 16 * x + 4 * g + j;
             if (!(ok_now[x] && key >= lo_key && key < hi)) s[x][j] = -INFINITY;
-            if (!(ok_now[x] && key < hi_max)) w.vs[x].drop(j);
           }
-        const int x = w.lane >> 5, key = key0 + 16 * x + ((w.lane & 31) >> 1);
-        if (!((x ? ok_now[1] : ok_now[0]) && key < hi_max)) {
-          w.vtop[0] = 0;
-          if constexpr (NB == 8) w.vtop[1] = 0;
-        }
       }
       float m = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
@@ -476,9 +508,6 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
 #pragma unroll
           for (int j = 0; j < 4; ++j) O[b][j] *= f;
       }
-      uint32_t sb = max(w.vtop[0] & 0x7fffu, (w.vtop[0] >> 16) & 0x7fffu);
-      if constexpr (NB == 8)
-        sb = max(sb, max(w.vtop[1] & 0x7fffu, (w.vtop[1] >> 16) & 0x7fffu));
       if (__any((int)(sb >> 10) - 15 > vexp)) {
         const int to = max(vexp, (int)(wave_max_u32(sb) >> 10) - 15);
         const float f = exp2_int(vexp - to);
@@ -555,8 +584,14 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   }
 }
 
+#ifndef WPE
+#define WPE 4
+#endif
+#ifndef WPE64
+#define WPE64 4
+#endif
 template <int D>
-constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
+constexpr int waves_per_simd() { return D == 64 ? WPE64 : D == 128 ? WPE : 2; }
 
 // A workgroup per tile, KV head and part.  The workspace holds RT rows of D sums
 // per part, then the parts' references and sums of probabilities.
