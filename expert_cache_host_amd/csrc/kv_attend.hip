@@ -276,39 +276,34 @@ struct Attend {
   // Scores of the step's keys in units of `unit`, as the matrix cores leave them:
   // s[x][i] is key 4 g + i of tile x against the lane's column.
   __device__ __forceinline__ void scores(const half8_t (&Q)[NB], float (&s)[2][4]) const {
-    constexpr int per = NB == 2 ? 2 : 4;  // blocks of a transposed word group
+    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+    uint4 both = make_uint4(0, 0, 0, 0);
+    if constexpr (NB == 2) both = transpose_rows(kc[0]);  // both tiles' two blocks
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x) {
+      Scales<NB> ks;
+      ks.read(lds + (16 * x + 4 * g) * NB * 2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
-    Scales<NB> ks[2];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) ks[x].read(lds + (16 * x + 4 * g) * NB * 2);
-    const floatx4 z = {0.f, 0.f, 0.f, 0.f};
+      for (int h = 0; h < (NB + 3) / 4; ++h) {
+        uint4 t = both;
+        if constexpr (NB == 2) {
+          if (x) t.x = both.z, t.y = both.w;
+        } else {
+          t = transpose_rows(kc[x * (KW / 2) + h]);
+        }
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-    for (int h = 0; h < NB / per; ++h) {
-      uint32_t w[2][4];
-      const uint4 t = transpose_rows(kc[h]);
-      if constexpr (NB == 2) {  // both tiles' two blocks in one group
-        w[0][0] = t.x, w[0][1] = t.y, w[1][0] = t.z, w[1][1] = t.w;
-      } else {
-        const uint4 u = transpose_rows(kc[KW / 2 + h]);
-        w[0][0] = t.x, w[0][1] = t.y, w[0][2] = t.z, w[0][3] = t.w;
-        w[1][0] = u.x, w[1][1] = u.y, w[1][2] = u.z, w[1][3] = u.w;
-      }
+        for (int k = 0; k < (NB == 2 ? 2 : 4); ++k) {
+          const int b = h * 4 + k;
+          // raw: -8 times the block's sum of q, which the codes' offset takes away
+          floatx4 c = z;
+          if constexpr (kRaw)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::minus_eight(), Q[b], z, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(w[k]), Q[b], c, 0, 0, 0);
 #pragma unroll
-      for (int k = 0; k < per; ++k) {
-        const int b = h * per + k;
-        // raw: -8 times the block's sum of q, which the codes' offset takes away
-        floatx4 m = z;
-        if constexpr (kRaw)
-          m = __builtin_amdgcn_mfma_f32_16x16x32_f16(RawCodes::minus_eight(), Q[b], z, 0, 0, 0);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const floatx4 c =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_of(w[x][k]), Q[b], m, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks[x].at(i, b), c[i], s[x][i]);
+          for (int i = 0; i < 4; ++i) s[x][i] = fmaf(ks.at(i, b), c[i], s[x][i]);
         }
       }
     }
@@ -584,14 +579,10 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   }
 }
 
-#ifndef WPE
-#define WPE 4
-#endif
-#ifndef WPE64
-#define WPE64 4
-#endif
+// What the registers allow without spilling (at D = 128 four waves spill eight
+// registers and take 121 us where three take 103: 32 sequences of ~12000 keys).
 template <int D>
-constexpr int waves_per_simd() { return D == 64 ? WPE64 : D == 128 ? WPE : 2; }
+constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
 // A workgroup per tile, KV head and part.  The workspace holds RT rows of D sums
 // per part, then the parts' references and sums of probabilities.
@@ -633,9 +624,11 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int most, 
     const long long tt = (long long)tile.t0 + rr / G;
     if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
     float best = -INFINITY;
+#pragma unroll 8
     for (int x = 0; x < parts; ++x) best = fmaxf(best, l_parts[x * RT * 2 + r]);
     float l = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int x = 0; x < parts; ++x) {
       const float ref = l_parts[x * RT * 2 + r];
       const float f = ref == -INFINITY ? 0.f : exp2f(ref - best);
@@ -654,9 +647,6 @@ long long tiles_bound(const KvCache &c, const KvBatch &b, int type, int q_heads)
   return (long long)b.T * (q_heads / c.kv_heads) / rows_of(type) + b.n_seqs;
 }
 
-#ifndef CHUNK
-#define CHUNK 64
-#endif
 struct Split {
   int most, chunk;  // parts of the longest possible row; steps of a part at most
 };
@@ -667,9 +657,13 @@ Split split_of(const KvCache &c, const KvBatch &b, int type, int q_heads, int wi
   // a tile of RT rows spans at most RT tokens beside the window
   if (window > 0 && window + 16ll < len) len = window + 16ll;
   const long long steps = len / 32 + 2;
+  // Steps of a part: as few as give the chip 4 workgroups to a CU at the table's
+  // length, at most 64 (a part's start and end cost about two steps, the last
+  // part to end sets the time: 32 sequences of 6000 to 16000 keys take 125 us with
+  // 48, 123 with 64, 128 with 96), at least two a wave, and at most 64 parts.
   long long chunk = groups * steps / 1024;
-  if (chunk > CHUNK) chunk = CHUNK;
-  if (chunk < 8) chunk = 8;
+  if (chunk > 64) chunk = 64;
+  if (chunk < 2 * kWaves) chunk = 2 * kWaves;
   if (chunk < (steps + 63) / 64) chunk = (steps + 63) / 64;
   return {(int)((steps + chunk - 1) / chunk), (int)chunk};
 }
