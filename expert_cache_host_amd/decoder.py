@@ -61,7 +61,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 class _At:
     """Makes a device and a stream current, so that the launch and what the call allocates
-    belong to them; yields the raw stream."""
+    belong to them."""
 
     def __init__(self, index, stream):
         self.guards = [torch.cuda.device(index)]
@@ -69,12 +69,10 @@ class _At:
             if stream.device.index != index:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
             self.guards.append(torch.cuda.stream(stream))
-        self.index = index
 
     def __enter__(self):
         for g in self.guards:
             g.__enter__()
-        return _raw_stream(self.index)
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -82,23 +80,9 @@ class _At:
         return False
 
 
-class _Here:
-    """The same where both are current already."""
-
-    def __init__(self, index):
-        self.raw = _raw_stream(index)
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *exc):
-        return False
-
-
-def _on(index, stream):
-    if stream is None and torch.cuda.current_device() == index:
-        return _Here(index)
-    return _At(index, stream)
+def _elsewhere(index, stream):
+    """Whether the call must make its device or stream current first."""
+    return stream is not None or torch.cuda.current_device() != index
 
 
 def _fault(t, name, index, rows, d, dtype):
@@ -132,8 +116,7 @@ def _cuda(t, name):
 
 
 def _weight(w, name, index, d):
-    if w.get_device() != index or w.dtype != torch.float32 or w.dim() != 1 or w.shape[0] != d or \
-            not w.is_contiguous():
+    if w.get_device() != index or w.dtype != torch.float32 or w.shape != (d,) or not w.is_contiguous():
         raise ValueError(f"{name} must be contiguous float32 [{d}] on cuda:{index}")
     return w.data_ptr()
 
@@ -153,6 +136,10 @@ def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: floa
     h_out is given.
     """
     dev = _cuda(h, "h")
+    if _elsewhere(dev, stream):
+        with _At(dev, stream):
+            return block_norm(h, y, post_w, gate, pre_w, res_scale=res_scale, block_scale=block_scale, eps=eps,
+                              h_out=h_out, x_out=x_out, x_dtype=x_dtype)
     ldh = _rows(h, "h", dev)
     T, d = h.shape
     hd = xd = h.dtype
@@ -164,11 +151,11 @@ def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: floa
         yt = _TYPES[xd]
         yp = y.data_ptr()
         if gate is not None:
-            if gate.dim() == 1:
-                _rows(gate.unsqueeze(0), "gate", dev, 1, d)
-            else:
+            gt = _TYPES.get(gate.dtype)
+            if gate.dim() != 1:
                 ldg = _rows(gate, "gate", dev, T, d)
-            gt = _TYPES[gate.dtype]
+            elif gate.get_device() != dev or gt is None or gate.shape != (d,) or not gate.is_contiguous():
+                raise ValueError("gate must be [d] or have h's rows, beside h, float32, bfloat16 or float16")
             gp = gate.data_ptr()
         if post_w is not None:
             wp = _weight(post_w, "post_w", dev, d)
@@ -181,28 +168,26 @@ def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: floa
     keep = y is None and res_scale == 1.0 and h_out is None
     if keep and pre_w is None:
         raise ValueError("nothing to compute: y and pre_w are None")
-    with _on(dev, stream) as s:
-        if h_out is not None:
-            ldho = _rows(h_out, "h_out", dev, T, d, hd)
-            hp = h_out.data_ptr()
-        elif not keep:
-            h_out = torch.empty((T, d), dtype=hd, device=h.device)
-            ldho, hp = d, h_out.data_ptr()
-        x = x_out
-        if x is not None:
-            ldx = _rows(x, "x_out", dev, T, d, x_dtype)
-            xt, xp = _TYPES[x.dtype], x.data_ptr()
-        elif pre_w is not None:
-            xd = x_dtype or xd
-            if xd not in _TYPES:
-                raise ValueError("x_dtype must be float32, bfloat16 or float16")
-            x = torch.empty((T, d), dtype=xd, device=h.device)
-            ldx, xt, xp = d, _TYPES[xd], x.data_ptr()
-        rc = _library().moe_block_norm(h.data_ptr(), _TYPES[hd], ldh, yp, yt, ldy, wp, gp, gt, ldg, vp, T, d,
-                                       res_scale, block_scale, eps, hp, ldho, xp, xt, ldx, s)
-        if rc:
-            _check(rc)
-    return (h if keep else h_out), x
+    if h_out is not None:
+        ldho = _rows(h_out, "h_out", dev, T, d, hd)
+        hp = h_out.data_ptr()
+    elif not keep:
+        h_out = h.new_empty((T, d))
+        ldho, hp = d, h_out.data_ptr()
+    if x_out is not None:
+        ldx = _rows(x_out, "x_out", dev, T, d, x_dtype)
+        xt, xp = _TYPES[x_out.dtype], x_out.data_ptr()
+    elif pre_w is not None:
+        xd = x_dtype or xd
+        if xd not in _TYPES:
+            raise ValueError("x_dtype must be float32, bfloat16 or float16")
+        x_out = h.new_empty((T, d), dtype=xd)
+        ldx, xt, xp = d, _TYPES[xd], x_out.data_ptr()
+    rc = _library().moe_block_norm(h.data_ptr(), _TYPES[hd], ldh, yp, yt, ldy, wp, gp, gt, ldg, vp, T, d, res_scale,
+                                   block_scale, eps, hp, ldho, xp, xt, ldx, _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return (h if keep else h_out), x_out
 
 
 class Q4Matrix:
@@ -245,17 +230,19 @@ class Q4Matrix:
 def q4_matvec(x, w: Q4Matrix, out=None, stream=None):
     """out [T, rows] = x [T, cols] times w transposed, in x's type (float32 sums)."""
     dev = w._index
+    if _elsewhere(dev, stream):
+        with _At(dev, stream):
+            return q4_matvec(x, w, out)
     ldx = _rows(x, "x", dev, None, w.cols)
     T, dt = x.shape[0], x.dtype
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty((T, w.rows), dtype=dt, device=w.device)
-            ldo = w.rows
-        else:
-            ldo = _rows(out, "out", dev, T, w.rows, dt)
-        rc = _library().moe_q4_matvec(*w._head, x.data_ptr(), _TYPES[dt], ldx, T, out.data_ptr(), ldo, s)
-        if rc:
-            _check(rc)
+    if out is None:
+        out = x.new_empty((T, w.rows))
+        ldo = w.rows
+    else:
+        ldo = _rows(out, "out", dev, T, w.rows, dt)
+    rc = _library().moe_q4_matvec(*w._head, x.data_ptr(), _TYPES[dt], ldx, T, out.data_ptr(), ldo, _raw_stream(dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -322,6 +309,9 @@ class KVCache:
         rotated likewise, or None.  Rows of no sequence are left as they are in `q_out`
         (undefined in a new one)."""
         dev, D, dt = self._index, self.head_dim, k.dtype
+        if _elsewhere(dev, stream):
+            with _At(dev, stream):
+                return self.append(k, v, pages, start, past, q, inv_freq, interleaved, q_out)
         ldk = _rows(k, "k", dev, None, self.kv_heads * D)
         T = k.shape[0]
         ldv = _rows(v, "v", dev, T, self.kv_heads * D, dt)
@@ -341,18 +331,17 @@ class KVCache:
             heads, qp = self._heads(q), q.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out needs q")
-        with _on(dev, stream) as s:
-            if q is not None:
-                if q_out is None:
-                    q_out = torch.empty((T, heads * D), dtype=dt, device=self.device)
-                    ldqo = heads * D
-                else:
-                    ldqo = _rows(q_out, "q_out", dev, T, heads * D, dt)
-                op = q_out.data_ptr()
-            rc = _library().moe_kv_append(self._cp, b, _TYPES[dt], k.data_ptr(), ldk, v.data_ptr(), ldv, fp, rot,
-                                          1 if interleaved else 0, qp, ldq, heads, op, ldqo, s)
-            if rc:
-                _check(rc)
+        if q is not None:
+            if q_out is None:
+                q_out = q.new_empty((T, heads * D))
+                ldqo = heads * D
+            else:
+                ldqo = _rows(q_out, "q_out", dev, T, heads * D, dt)
+            op = q_out.data_ptr()
+        rc = _library().moe_kv_append(self._cp, b, _TYPES[dt], k.data_ptr(), ldk, v.data_ptr(), ldv, fp, rot,
+                                      1 if interleaved else 0, qp, ldq, heads, op, ldqo, _raw_stream(dev))
+        if rc:
+            _check(rc)
         return q_out
 
     def _heads(self, q) -> int:
@@ -366,13 +355,15 @@ class KVCache:
         batch's rows (0 in a hole; undefined for rows of no sequence)."""
         if rows < 0:
             raise ValueError("rows must be >= 0")
+        if _elsewhere(self._index, stream):
+            with _At(self._index, stream):
+                return self.read(pages, start, past, rows)
         b = self._batch(pages, start, past, rows)
-        with _on(self._index, stream) as s:
-            k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
-            v = torch.empty_like(k)
-            rc = _library().moe_kv_read(self._cp, b, k.data_ptr(), v.data_ptr(), s)
-            if rc:
-                _check(rc)
+        k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
+        v = torch.empty_like(k)
+        rc = _library().moe_kv_read(self._cp, b, k.data_ptr(), v.data_ptr(), _raw_stream(self._index))
+        if rc:
+            _check(rc)
         return k, v
 
     def attend(self, q, pages, start, past, scale: float, window: int = 0, out=None, stream=None):
@@ -380,23 +371,25 @@ class KVCache:
         sees: positions up to its own, within `window` when window > 0.  Rows of no sequence
         are left as they are in `out` (undefined in a new one)."""
         dev, dt = self._index, q.dtype
+        if _elsewhere(dev, stream):
+            with _At(dev, stream):
+                return self.attend(q, pages, start, past, scale, window, out)
         ldq = _rows(q, "q", dev)
         T, n = q.shape
         heads = self._heads(q)
         b = self._batch(pages, start, past, T)
         lib, ty = _library(), _TYPES[dt]
-        with _on(dev, stream) as s:
-            if out is None:
-                out = torch.empty((T, n), dtype=dt, device=self.device)
-                ldo = n
-            else:
-                ldo = _rows(out, "out", dev, T, n, dt)
-            need = lib.moe_kv_attend_workspace(self._cp, b, ty, heads, window)
-            if need < 0:
-                _check(need)
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            rc = lib.moe_kv_attend(self._cp, b, ty, q.data_ptr(), ldq, heads, scale, window, out.data_ptr(), ldo,
-                                   ws.data_ptr() if need else None, need, s)
-            if rc:
-                _check(rc)
+        if out is None:
+            out = q.new_empty((T, n))
+            ldo = n
+        else:
+            ldo = _rows(out, "out", dev, T, n, dt)
+        need = lib.moe_kv_attend_workspace(self._cp, b, ty, heads, window)
+        if need < 0:
+            _check(need)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        rc = lib.moe_kv_attend(self._cp, b, ty, q.data_ptr(), ldq, heads, scale, window, out.data_ptr(), ldo,
+                               ws.data_ptr() if need else None, need, _raw_stream(dev))
+        if rc:
+            _check(rc)
         return out
