@@ -116,7 +116,7 @@ moe_status moe_q4_matvec(const void *codes, const void *scales, int32_t rows, in
   clear_error();
   if (bad_type(type)) return einval("element type must be MOE_F32, MOE_BF16 or MOE_F16");
   if (group != 32 && group != 64 && group != 128) return einval("group must be 32, 64 or 128");
-  if (rows < 1) return einval("rows must be >= 1");
+  if (rows < 1 || rows > MOE_Q4_MAX_ROWS) return einval("rows must be in [1, 2^30]");
   if (cols < group || cols % group) return einval("cols must be a multiple of group");
   if (n_tokens < 0 || n_tokens > MOE_Q4_MAX_TOKENS) return einval("n_tokens must be in [0, 65536]");
   if (x_stride < 0) return einval("x_stride must be >= 0");

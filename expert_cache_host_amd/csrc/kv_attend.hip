@@ -30,6 +30,8 @@
 // Keys are split over the waves of a workgroup and over workgroups; the parts
 // are joined in LDS, and by a second kernel when there is more than one
 // workgroup to a tile.
+#include <algorithm>
+
 #include "device_types.hpp"
 #include "q4_tile.hpp"
 
@@ -74,7 +76,8 @@ __device__ __forceinline__ long long position_cap(const KvAttendArgs &a) {
 __device__ __forceinline__ bool fill_tile(const KvAttendArgs &a, int G, int RT, long long tile,
                                           int start_0, int start, int end, Tile &o) {
   o.t0 = start;
-  o.rows = (end - start) * G;
+  // at most the batch's rows, whatever stands in `start`
+  o.rows = (int)min(max((long long)end - start, 0ll), (long long)a.b.T) * G;
   o.steps = 0;
   const long long first = (tile - tile_base(start, start_0, o.s, G, RT)) * RT;
   if (first < 0 || first >= o.rows) return false;
@@ -660,11 +663,14 @@ Split split_of(const KvCache &c, const KvBatch &b, int type, int q_heads, int wi
   // Steps of a part: as few as give the chip 4 workgroups to a CU at the table's
   // length, at most 64 (a part's start and end cost about two steps, the last
   // part to end sets the time: 32 sequences of 6000 to 16000 keys take 125 us with
-  // 48, 123 with 64, 128 with 96), at least two a wave, and at most 64 parts.
+  // 48, 123 with 64, 128 with 96), at least two a wave; at most 64 parts a tile
+  // and 16384 in all, which bounds the workspace (136 MB at D = 128) where a long
+  // prompt's tiles fill the chip many times over by themselves.
   long long chunk = groups * steps / 1024;
   if (chunk > 64) chunk = 64;
   if (chunk < 2 * kWaves) chunk = 2 * kWaves;
-  if (chunk < (steps + 63) / 64) chunk = (steps + 63) / 64;
+  const long long most = std::min(64ll, std::max(1ll, 16384 / groups));
+  if (chunk < (steps + most - 1) / most) chunk = (steps + most - 1) / most;
   return {(int)((steps + chunk - 1) / chunk), (int)chunk};
 }
 

@@ -15,6 +15,7 @@ import torch
 
 from .binding import _check, load_library
 
+_I32 = 0x7fffffff  # sizes and counts are 32-bit integers at the C interface
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -92,6 +93,8 @@ def _fault(t, name, index, rows, d, dtype):
         return f"{name} must be [{'rows' if rows is None else rows}, {'d' if d is None else d}], not {list(t.shape)}"
     if t.shape[1] > 1 and t.stride(1) != 1:
         return f"{name}'s rows must be contiguous"
+    if max(t.shape) > _I32:
+        return f"{name} has more than 2^31 - 1 rows or columns"
     if dtype is None:
         return f"{name} must be float32, bfloat16 or float16"
     return f"{name} must be {dtype}"
@@ -103,7 +106,7 @@ def _rows(t, name, index, rows=None, d=None, dtype=None):
     if t.get_device() == index and len(shape) == 2 and (rows is None or shape[0] == rows) and \
             (d is None or shape[1] == d) and (t.dtype in _TYPES if dtype is None else t.dtype == dtype):
         st = t.stride()
-        if st[1] == 1 or shape[1] <= 1:
+        if (st[1] == 1 or shape[1] <= 1) and shape[0] <= _I32 and shape[1] <= _I32:
             return st[0]
     raise ValueError(_fault(t, name, index, rows, d, dtype))
 
@@ -203,7 +206,7 @@ class Q4Matrix:
         if scales.get_device() != dev or scales.dtype != torch.float16 or scales.dim() != 2 or \
                 scales.shape[0] != self.rows or not scales.is_contiguous():
             raise ValueError("scales must be contiguous float16 [rows, cols / group] beside the codes")
-        if self.rows < 1 or scales.shape[1] < 1 or \
+        if not 1 <= self.rows <= 1 << 30 or self.cols > _I32 or scales.shape[1] < 1 or \
                 scales.shape[1] * (g := self.cols // scales.shape[1]) != self.cols or g not in (32, 64, 128):
             raise ValueError("scales must hold one scale per 32, 64 or 128 weights")
         self.group = g
@@ -271,7 +274,7 @@ class KVCache:
         for name, (t, dtype, shape) in want.items():
             if t.get_device() != dev or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous {dtype} {list(shape)} on cuda:{dev}")
-        if n < 1 or h < 1 or h > 1024 or p < 16 or p % 16 or p > 65536 or nb not in (2, 4, 8):
+        if n < 1 or n > _I32 or h < 1 or h > 1024 or p < 16 or p % 16 or p > 65536 or nb not in (2, 4, 8):
             raise ValueError("head_dim must be 64, 128 or 256, page_tokens a multiple of 16 up to 65536, "
                              "kv_heads at most 1024")
         self.device, self.tensors = k_codes.device, (k_codes, k_scales, v_codes, v_scales)
@@ -353,8 +356,8 @@ class KVCache:
     def read(self, pages, start, past, rows: int, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """(k, v) float32 [rows, kv_heads, head_dim]: the values the cache holds for the
         batch's rows (0 in a hole; undefined for rows of no sequence)."""
-        if rows < 0:
-            raise ValueError("rows must be >= 0")
+        if not 0 <= rows <= _I32:
+            raise ValueError("rows must be in [0, 2^31)")
         if _elsewhere(self._index, stream):
             with _At(self._index, stream):
                 return self.read(pages, start, past, rows)
@@ -379,6 +382,8 @@ class KVCache:
         heads = self._heads(q)
         b = self._batch(pages, start, past, T)
         lib, ty = _library(), _TYPES[dt]
+        if not 0 <= window <= _I32:
+            raise ValueError("window must be in [0, 2^31)")
         if out is None:
             out = q.new_empty((T, n))
             ldo = n

@@ -445,6 +445,7 @@ moe_status moe_host_expert_forward(const void *expert_q4, int32_t d_model, int32
 
 #define MOE_NORM_MAX_D 32768
 #define MOE_Q4_MAX_TOKENS 65536
+#define MOE_Q4_MAX_ROWS (1 << 30)
 #define MOE_KV_MAX_PAGE_TOKENS 65536
 #define MOE_KV_MAX_HEADS 1024
 
@@ -484,8 +485,8 @@ moe_status moe_block_norm(const void *h, int32_t h_type, int64_t h_stride, const
  *   x, out  [n_tokens][cols] and [n_tokens][rows] of `type`
  *
  * Meant for the few tokens of decode (weights are read once for up to 8 float32
- * or 16 half-width tokens); n_tokens <= MOE_Q4_MAX_TOKENS.  Sums are float32.
- * cols must be a multiple of group. */
+ * or 16 half-width tokens); n_tokens <= MOE_Q4_MAX_TOKENS, rows <=
+ * MOE_Q4_MAX_ROWS.  Sums are float32.  cols must be a multiple of group. */
 moe_status moe_q4_matvec(const void *codes, const void *scales, int32_t rows, int32_t cols,
                          int32_t group, const void *x, int32_t type, int64_t x_stride,
                          int32_t n_tokens, void *out, int64_t out_stride, moe_stream_t stream);

@@ -45,6 +45,7 @@ def matvec(**kw):
 
 @pytest.mark.parametrize("kw,msg", [
     (dict(t=3), "element type"), (dict(group=16), "group"), (dict(group=256), "group"), (dict(rows=0), "rows"),
+    (dict(rows=(1 << 30) + 1, ldo=1 << 31), "rows"),
     (dict(cols=0), "cols"), (dict(cols=96, group=64), "cols"), (dict(cols=48), "cols"), (dict(T=-1), "n_tokens"),
     (dict(T=65537), "n_tokens"), (dict(ldx=-1), "x_stride"), (dict(ldo=15), "out_stride"), (dict(q=None), "NULL"),
     (dict(s=None), "NULL"), (dict(x=None), "NULL"), (dict(out=None), "NULL"), (dict(q=P + 8), "16-byte"),

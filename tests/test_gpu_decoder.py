@@ -560,6 +560,60 @@ def test_attend_magnitudes(ty, ksize, vsize, qsize):
     check_attend(c, q, pages, start, pst, D ** -0.5, 0, got, ty)
 
 
+def test_attend_shared_prefix_and_many_sequences():
+    """300 sequences in one call (more than one probe of the search), many of them on the same prefix pages."""
+    D, P, Hkv, G, S = 64, 16, 2, 2, 300
+    g = gen(23)
+    rng = np.random.default_rng(3)
+    past = rng.integers(0, 90, S)
+    pages = np.full((S, 6), -1, np.int32)
+    for s in range(S):
+        k = (past[s] + P) // P
+        pages[s, :k] = [(s % 7) * 6 + j if j + 1 < k else 42 + s for j in range(k)]
+    new = np.ones(S, np.int64)
+    new[[5, 100, 299]] = 0
+    new[[50, 250]] = 7
+    start = np.concatenate([[0], np.cumsum(new)])
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    c = fill_cache(g, 42 + S, P, Hkv, D)
+    q = rnd(g, int(start[-1]), Hkv * G * D)
+    got = c.attend(q, t(pages), t(start), t(past), D ** -0.5)
+    check_attend(c, q, t(pages), t(start), t(past), D ** -0.5, 0, got, "f32")
+
+
+def test_rows_past_the_tensors_are_not_touched():
+    """start may promise more rows than the tensors hold (n_rows): those are neither read nor written."""
+    D, P, Hkv, G = 128, 16, 1, 2
+    g = gen(24)
+    pages = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8)
+    start = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    past = torch.tensor([3], dtype=torch.int32, device="cuda")
+    c = fill_cache(g, 8, P, Hkv, D)
+    before = [t.clone() for t in c.tensors]
+    q, k = rnd(g, 64, Hkv * G * D), rnd(g, 64, Hkv * D)
+    full = torch.full((64, Hkv * G * D), 7.5, device="cuda")
+    c.append(k[:10], k[:10], pages, start, past, q=q[:10], q_out=full[:10])
+    assert bool((full[10:] == 7.5).all())
+    for t, b in zip(c.tensors, before):
+        flat, old = t.transpose(1, 2).reshape(8 * P, -1), b.transpose(1, 2).reshape(8 * P, -1)
+        assert torch.equal(flat[:3], old[:3]) and torch.equal(flat[13:], old[13:])
+    full.fill_(7.5)
+    c.attend(q[:10], pages, start, past, 0.1, out=full[:10])
+    assert bool((full[10:] == 7.5).all())
+    check_attend(c, q, pages, torch.tensor([0, 10], dtype=torch.int32), past, 0.1, 0, full, "f32")
+
+
+def test_workspace_stays_bounded():
+    """A long prompt over a long table asks for no workspace that grows with both."""
+    from expert_cache_host_amd.decoder import _KvBatch, _library
+    c = m.KVCache.create(4, 64, 8, 128)
+    for rows, seqs in ((1, 1), (32, 32), (512, 1), (8192, 1), (100000, 64), (4096, 4096)):
+        b = _KvBatch(4096, 4096, 4096, seqs, 4096, rows)
+        for ty in (0, 1):
+            n = _library().moe_kv_attend_workspace(c._cp, b, ty, 64, 0)
+            assert 0 <= n <= 300 << 20, (rows, seqs, ty, n)
+
+
 def test_attend_long():
     """Long contexts (many splits), a few rows checked in full."""
     D, P, Hkv, G = 128, 64, 2, 4
@@ -786,8 +840,11 @@ def test_cache_refusals():
         a.update(bad)
         with pytest.raises(ValueError):
             c.attend(**a)
-    with pytest.raises(MoeError):
-        c.attend(k, pages, start, past, 1.0, window=-1)
+    for w in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            c.attend(k, pages, start, past, 1.0, window=w)
+    with pytest.raises(ValueError):
+        c.read(pages, start, past, -1)
     with pytest.raises(MoeError):
         c.attend(k, pages, start, past, float("nan"))
     with pytest.raises(ValueError):
