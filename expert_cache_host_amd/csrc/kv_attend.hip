@@ -256,7 +256,10 @@ struct Attend {
         kc[j] = *(const uint4 *)(p + o + j % (KW / 2) * 64);
       }
     }
+    // both scales with the keys: a step begins by sharing them, with the values'
+    // codes still on their way (loads return in order)
     sk.load(a.c.k_s, row, lane);
+    sv.load(a.c.v_s, row, lane);
   }
 
   __device__ __forceinline__ void load_v(const long long (&row)[2]) {
@@ -273,7 +276,6 @@ struct Attend {
         vc[j][0] = v.x, vc[j][1] = v.y;
       }
     }
-    sv.load(a.c.v_s, row, lane);
   }
 
   // Scores of the step's keys in units of `unit`, as the matrix cores leave them:
