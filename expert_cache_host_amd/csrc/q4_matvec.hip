@@ -15,7 +15,13 @@
 // A workgroup owns all of K: wave w holds the tokens' slice of KT chunks of 128
 // columns in registers for the whole launch and streams its slice of 16 rows
 // after 16 rows, the next tile's loads in flight while the present one is
-// multiplied; the waves' sums meet in LDS, a barrier per tile.
+// multiplied; the waves' sums meet in LDS, a barrier per tile.  K beyond 6144
+// columns takes passes, the tokens laid out again for each.
+//
+// Measured (GPU time): one float32 token, 131072 x 2048: 36-38 us, 4.1 TB/s (a large
+// copy reaches 4.85); 8192 x 2816: 6.3 us, of which the weights need 2.7; four
+// bfloat16 tokens, 10240 x 6144: 14.6 us, where twelve waves a CU wait for loads
+// half of their time.
 #include <algorithm>
 
 #include "device_types.hpp"
@@ -143,7 +149,8 @@ struct Matvec {
   }
 };
 
-// GB: blocks per scale; RB: row tiles per visit, above 1 when K takes passes.
+// GB: blocks per scale; RB: 0 when one pass takes all of K, else row tiles per
+// visit.
 template <int TY, int KT, int FI, int GB, int RB>
 __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4MatvecArgs a, int passes) {
   constexpr int PL = parts_of(TY);
@@ -152,8 +159,8 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
   __shared__ uint4 units[FI == 1 ? (KT == 4 ? 12 : kMaxWaves) : 1][4][KT * 16 + 4];
   Matvec<TY, KT, FI> m(a, (int)blockIdx.y * (4 * FI / PL));
   const int tiles = (a.rows + 15) / 16, nb = m.nb, per_pass = m.waves * KT * 4;
-  uint4 w[RB > 1 ? 1 : 2][KT];
-  uint32_t s[RB > 1 ? 1 : 2][KT];
+  uint4 w[RB > 0 ? 1 : 2][KT];
+  uint32_t s[RB > 0 ? 1 : 2][KT];
   const CodeBits bits;
   // the wave's KT chunks of tile `tile`; blocks and rows past the end re-read a
   // valid place (their scale, or their row's output, is dropped)
@@ -204,7 +211,7 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
       if (row < a.rows) store1(a.out, TY, (long long)(m.t0 + t) * a.ldo + row, v);
     }
   };
-  if constexpr (RB == 1) {
+  if constexpr (RB == 0) {
     const int first = m.wave * KT * 4;
     int tile = blockIdx.x, it = 0;
     if constexpr (FI == 1) {
@@ -237,13 +244,15 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
         if constexpr (FI == 1) {
           float x[4 / PL][8];
           m.load_few(first, x);
+          load(tile, first, w[0], s[0]);
           m.stage_few(x, units[m.wave]);
         } else {
+          load(tile, first, w[0], s[0]);
           m.stage_many(first);
         }
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-          load(min(tile + r, tiles - 1), first, w[0], s[0]);
+          if (r) load(min(tile + r, tiles - 1), first, w[0], s[0]);
           float part[FI] = {};
           multiply(w[0], s[0], part);
 #pragma unroll
@@ -257,46 +266,65 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
   }
 }
 
+// Chunks of K that one pass can take: 12 waves of 4.
+constexpr int kPassChunks = 48;
+
 template <int TY, int KT, int FI, int GB>
-hipError_t launch_one(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
-  constexpr int RB = 4;  // row tiles a visit when K takes passes
+hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / parts_of(TY);
-  const int gy = (a.T + tokens - 1) / tokens, visits = passes == 1 ? tiles : (tiles + RB - 1) / RB;
+  const int gy = (a.T + tokens - 1) / tokens;
   // as many workgroups as the chip holds at a time, each with the same number of
-  // tiles, so that the tokens are laid out no more often than that
-  const int fit = (KT == 4 ? 12 : KT == 2 ? 16 : 32) / waves;
-  const int most = std::max(1, 256 * std::max(1, fit) / gy), each = (visits + most - 1) / most;
-  const dim3 grid((unsigned)((visits + each - 1) / each), (unsigned)gy);
-  if (KT < 4 || passes == 1)
-    q4_matvec_kernel<TY, KT, FI, GB, 1><<<grid, waves * 64, 0, s>>>(a, 1);
-  else if constexpr (KT == 4)
-    q4_matvec_kernel<TY, KT, FI, GB, RB><<<grid, waves * 64, 0, s>>>(a, passes);
+  // visits, so that the tokens are laid out no more often than that (45 x 2144 x
+  // 5003 f16: 12.3 us; with a workgroup per tile 25.7)
+  auto grid = [&](int waves, int visits) {
+    const int fit = std::max(1, (KT == 4 ? 12 : KT == 2 ? 16 : 32) / waves);
+    const int most = std::max(1, 256 * fit / gy), each = (visits + most - 1) / most;
+    return dim3((unsigned)((visits + each - 1) / each), (unsigned)gy);
+  };
+  if (KT < 4 || chunks <= kPassChunks) {
+    const int waves = (chunks + KT - 1) / KT;
+    q4_matvec_kernel<TY, KT, FI, GB, 0><<<grid(waves, tiles), waves * 64, 0, s>>>(a, 1);
+  } else if constexpr (KT == 4) {
+    const int passes = (chunks + kPassChunks - 1) / kPassChunks;
+    const int waves = (chunks + 4 * passes - 1) / (4 * passes);
+    // Four tiles a visit share the laying out of many tokens, one spreads the tiles
+    // over the chip (one token, 8192 x 12288: 31 us with four, 23 with one; 16
+    // float32 tokens, 8192 x 8192: 54 with four, 105 with one); below 128 visits of
+    // four the chip stands too empty for it.
+    if (FI > 1 && (long long)(tiles / 4) * gy >= 128) {
+      if constexpr (FI > 1)
+        q4_matvec_kernel<TY, 4, FI, GB, 4>
+            <<<grid(waves, (tiles + 3) / 4), waves * 64, 0, s>>>(a, passes);
+    } else {
+      q4_matvec_kernel<TY, 4, FI, GB, 1><<<grid(waves, tiles), waves * 64, 0, s>>>(a, passes);
+    }
+  }
   return hipGetLastError();
 }
 
 template <int TY, int KT, int FI>
-hipError_t launch_group(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
-  if (a.group == 32) return launch_one<TY, KT, FI, 1>(a, waves, passes, s);
-  if (a.group == 64) return launch_one<TY, KT, FI, 2>(a, waves, passes, s);
-  return launch_one<TY, KT, FI, 4>(a, waves, passes, s);
+hipError_t launch_group(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
+  if (a.group == 32) return launch_one<TY, KT, FI, 1>(a, chunks, s);
+  if (a.group == 64) return launch_one<TY, KT, FI, 2>(a, chunks, s);
+  return launch_one<TY, KT, FI, 4>(a, chunks, s);
 }
 
 template <int TY, int KT>
-hipError_t launch_parts(const Q4MatvecArgs &a, int waves, int passes, hipStream_t s) {
+hipError_t launch_parts(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   const int parts = a.T * parts_of(TY);
-  if (parts <= 4) return launch_group<TY, KT, 1>(a, waves, passes, s);
-  if (parts <= 8) return launch_group<TY, KT, 2>(a, waves, passes, s);
-  return launch_group<TY, KT, 4>(a, waves, passes, s);
+  if (parts <= 4) return launch_group<TY, KT, 1>(a, chunks, s);
+  if (parts <= 8) return launch_group<TY, KT, 2>(a, chunks, s);
+  return launch_group<TY, KT, 4>(a, chunks, s);
 }
 
+// Chunks of K per wave: 2 up to 32 chunks (one float32 token, 131072 x 2048: 38 us
+// with 2, 40 with 1, 42 with 4), 4 above.
 template <int TY>
 hipError_t launch_cols(const Q4MatvecArgs &a, hipStream_t s) {
   const int chunks = (a.cols / 32 + 3) / 4;
-  if (chunks <= 4) return launch_parts<TY, 1>(a, chunks, 1, s);
-  if (chunks <= 32) return launch_parts<TY, 2>(a, (chunks + 1) / 2, 1, s);
-  if (chunks <= 48) return launch_parts<TY, 4>(a, (chunks + 3) / 4, 1, s);
-  const int passes = (chunks + 47) / 48;
-  return launch_parts<TY, 4>(a, (chunks + 4 * passes - 1) / (4 * passes), passes, s);
+  if (chunks <= 4) return launch_parts<TY, 1>(a, chunks, s);
+  if (chunks <= 32) return launch_parts<TY, 2>(a, chunks, s);
+  return launch_parts<TY, 4>(a, chunks, s);
 }
 
 }  // namespace
