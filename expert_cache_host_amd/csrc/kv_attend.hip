@@ -117,8 +117,22 @@ __device__ __forceinline__ bool find_tile(const KvAttendArgs &a, int G, int RT, 
                    uniform(a.b.start[o.s + 1]), o);
 }
 
-// Parts that `steps` steps are cut into: equal ones, of at most `chunk` steps.
-__device__ __forceinline__ int parts_in(int steps, int chunk) { return (steps + chunk - 1) / chunk; }
+// How tiles are cut into parts, a workgroup each.
+struct Split {
+  int most;  // parts of a tile at most
+  int want;  // parts that would give the chip 4 workgroups to a CU
+};
+// Equal parts of a tile of `steps` steps, by its own length and not the page
+// table's: as many as are wanted, if they leave every wave two steps, and none of
+// more than 64 steps.  (A part's start and end cost about two steps, the last one
+// to end sets the time: 32 sequences of 6000 to 16000 keys take 125 us with parts
+// of 48, 123 with 64, 128 with 96.)
+__host__ __device__ __forceinline__ long long parts_of_steps(const Split &sp, long long steps) {
+  const long long by_size = (steps + 63) / 64, by_waves = (steps + 2 * kWaves - 1) / (2 * kWaves);
+  const long long few = by_waves < sp.want ? by_waves : sp.want;
+  const long long parts = by_size > few ? by_size : few;
+  return parts < sp.most ? (parts > 1 ? parts : 1) : sp.most;
+}
 
 __device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
 __device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
@@ -599,18 +613,18 @@ constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 // per part, then the parts' references and sums of probabilities.
 template <int D, int TY>
 __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_kernel(
-    KvAttendArgs a, int most, int chunk) {
+    KvAttendArgs a, Split sp) {
   constexpr int RT = rows_of(TY);
   __shared__ Shared<D, TY> sh;
-  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y / most, part = blockIdx.y % most;
+  const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y % a.c.kv_heads, part = blockIdx.y / a.c.kv_heads;
   Tile tile;
   if (!find_tile(a, G, RT, blockIdx.x, tile)) return;
-  const int parts = max(parts_in(tile.steps, chunk), 1);
+  const int parts = (int)parts_of_steps(sp, tile.steps);
   if (part >= parts) return;
   const int c0 = (int)((long long)tile.steps * part / parts);
   const int c1 = (int)((long long)tile.steps * (part + 1) / parts);
-  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * most + part;
-  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * most;
+  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * sp.most + part;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * sp.most;
   float *ws = (float *)a.ws;
   attend_part<D, TY>(a, G, kvh, tile, c0, c1, ws + slot * RT * D,
                      ws + slots * RT * D + slot * RT * 2, sh);
@@ -618,15 +632,15 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_ke
 
 // Joins a tile's parts where there are several.
 template <int D, int TY>
-__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, int most, int chunk) {
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, Split sp) {
   constexpr int RT = rows_of(TY);
   const int G = a.q_heads / a.c.kv_heads, kvh = blockIdx.y;
   Tile tile;
   if (!find_tile(a, G, RT, blockIdx.x, tile)) return;
-  const int parts = parts_in(tile.steps, chunk);
+  const int parts = (int)parts_of_steps(sp, tile.steps);
   if (parts < 2) return;
-  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * most;
-  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * most;
+  const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * sp.most;
+  const size_t slots = (size_t)gridDim.x * a.c.kv_heads * sp.most;
   const float *o_parts = (const float *)a.ws + slot * RT * D;
   const float *l_parts = (const float *)a.ws + slots * RT * D + slot * RT * 2;
   for (int j = threadIdx.x; j < RT * D / 4; j += 256) {
@@ -658,39 +672,31 @@ long long tiles_bound(const KvCache &c, const KvBatch &b, int type, int q_heads)
   return (long long)b.T * (q_heads / c.kv_heads) / rows_of(type) + b.n_seqs;
 }
 
-struct Split {
-  int most, chunk;  // parts of the longest possible row; steps of a part at most
-};
-
+// The lengths are on the device; here the page table bounds them.  At most 64
+// parts a tile and 8192 in all: that bounds the workspace (68 MB at D = 128) where
+// a long prompt's tiles fill the chip many times over by themselves, and the
+// workgroups that find no part to do where the table is much longer than the
+// sequences.
 Split split_of(const KvCache &c, const KvBatch &b, int type, int q_heads, int window) {
   const long long groups = tiles_bound(c, b, type, q_heads) * c.kv_heads;
   long long len = (long long)b.max_pages * c.page_tokens;
   // a tile of RT rows spans at most RT tokens beside the window
   if (window > 0 && window + 16ll < len) len = window + 16ll;
-  const long long steps = len / 32 + 2;
-  // Steps of a part: as few as give the chip 4 workgroups to a CU at the table's
-  // length, at most 64 (a part's start and end cost about two steps, the last
-  // part to end sets the time: 32 sequences of 6000 to 16000 keys take 125 us with
-  // 48, 123 with 64, 128 with 96), at least two a wave; at most 64 parts a tile
-  // and 16384 in all, which bounds the workspace (136 MB at D = 128) where a long
-  // prompt's tiles fill the chip many times over by themselves.
-  long long chunk = groups * steps / 1024;
-  if (chunk > 64) chunk = 64;
-  if (chunk < 2 * kWaves) chunk = 2 * kWaves;
-  const long long most = std::min(64ll, std::max(1ll, 16384 / groups));
-  if (chunk < (steps + most - 1) / most) chunk = (steps + most - 1) / most;
-  return {(int)((steps + chunk - 1) / chunk), (int)chunk};
+  Split sp;
+  sp.want = (int)((1024 + groups - 1) / groups);
+  sp.most = (int)std::min(64ll, std::max(1ll, 8192 / groups));
+  sp.most = (int)parts_of_steps(sp, len / 32 + 2);
+  return sp;
 }
 
 template <int D, int TY>
 hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
-  const auto [most, chunk] = split_of(a.c, a.b, a.type, a.q_heads, a.window);
+  const Split sp = split_of(a.c, a.b, a.type, a.q_heads, a.window);
   const unsigned tiles = (unsigned)tiles_bound(a.c, a.b, a.type, a.q_heads);
-  kv_attend_kernel<D, TY><<<dim3(tiles, (unsigned)(a.c.kv_heads * most)), kWaves * 64, 0, s>>>(
-      a, most, chunk);
-  if (most > 1)
+  kv_attend_kernel<D, TY><<<dim3(tiles, (unsigned)(a.c.kv_heads * sp.most)), kWaves * 64, 0, s>>>(a, sp);
+  if (sp.most > 1)
     kv_join_kernel<D, TY>
-        <<<dim3(tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, most, chunk);
+        <<<dim3(tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, sp);
   return hipGetLastError();
 }
 
