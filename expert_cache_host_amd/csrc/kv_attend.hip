@@ -429,10 +429,13 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   const long long cap = position_cap(a);
   const int hi = live ? (int)min(past + tok + 1, cap) : 0;
   const int lo_key = a.window > 0 ? (int)min(max(past + tok + 1 - a.window, 0ll), cap) : 0;
-  // keys that every row sees, and the end of the keys that some row sees
+  // keys that every row sees, and the range of the keys that some row of the
+  // batch sees (its tokens may end inside the tile)
   const int tok0 = tile.first / G, tok1 = (min(tile.first + RT, tile.rows) - 1) / G;
-  const int hi_max = (int)min(past + tok1 + 1, cap), hi_min = (int)min(past + tok0 + 1, cap);
+  const long long last = min((long long)tok1, (long long)a.b.T - 1 - tile.t0);
+  const int hi_max = (int)min(past + last + 1, cap), hi_min = (int)min(past + tok0 + 1, cap);
   const int lo_max = a.window > 0 ? (int)min(max(past + tok1 + 1 - a.window, 0ll), cap) : 0;
+  const int lo_min = a.window > 0 ? (int)min(max(past + tok0 + 1 - a.window, 0ll), cap) : 0;
   const int per = (c1 - c0 + kWaves - 1) / kWaves;
   const int i0 = min(c0 + wave * per, c1), i1 = min(i0 + per, c1);
 
@@ -491,9 +494,9 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       w.next(at, ok);  // past the last step: loaded from a valid place and not used
 
       if (!whole) {
-        // places that hold no key of the sequence, whose scales may be anything
+        // places that no row sees, whose scales may be anything
         const int key = key0 + (w.lane >> 1);
-        if (!((w.lane < 32 ? ok_now[0] : ok_now[1]) && key < hi_max)) {
+        if (!((w.lane < 32 ? ok_now[0] : ok_now[1]) && key >= lo_min && key < hi_max)) {
           w.sv.w[0] = 0;
           if constexpr (NB == 8) w.sv.w[1] = 0;
         }

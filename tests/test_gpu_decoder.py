@@ -603,6 +603,32 @@ def test_rows_past_the_tensors_are_not_touched():
     check_attend(c, q, pages, torch.tensor([0, 10], dtype=torch.int32), past, 0.1, 0, full, "f32")
 
 
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("ty", list(TYPES))
+def test_attend_garbage_beside_the_window_and_past_the_rows(D, G, ty):
+    """Keys on valid pages that no row sees (left of every row's window, or of tokens that the tensors do not
+    hold) may carry NaN and infinite scales: the result is the same bit for bit."""
+    P, Hkv = 32, 2
+    g = gen(D + 5)
+    new, past, window = [3, 1, 2, 40], [70, 45, 5, 90], 20
+    pages, start, pst, n = make_batch(new, past, P, 5)
+    c = fill_cache(g, n, P, Hkv, D)
+    T = sum(new) - 33  # of the last sequence's tokens the tensors hold 7
+    q = rnd(g, T, Hkv * G * D, dtype=TYPES[ty])
+    for w in (window, 0):
+        want = c.attend(q, pages, start, pst, D ** -0.5, window=w)
+        bad = m.KVCache(*(t.clone() for t in c.tensors))
+        pg = pages.cpu().numpy()
+        for s, (a, b) in enumerate(zip(new, past)):
+            b_live = b + (a if s < 3 else 7)
+            unseen = list(range(max(0, b + 1 - w))) if w else []
+            for p in unseen + list(range(b_live, b + a)):
+                bad.tensors[1][int(pg[s, p // P]), :, p % P] = float("nan")
+                bad.tensors[3][int(pg[s, p // P]), :, p % P] = float("inf" if p % 3 else "nan")
+        got = bad.attend(q, pages, start, pst, D ** -0.5, window=w)
+        assert bool(got.isfinite().all()) and torch.equal(got, want), w
+
+
 def test_workspace_stays_bounded():
     """A long prompt over a long table asks for no workspace that grows with both."""
     from expert_cache_host_amd.decoder import _KvBatch, _library
