@@ -10,6 +10,8 @@
 // before its rounding to the residual's type.  Bound by memory traffic (4.6 TB/s
 // at 4093 x 2045 f16 with a gate per element, 3.7 TB/s at 512 x 6144); a single
 // row is bound by the launch and two workgroup sums (3.8 us at d = 2816).
+#include <algorithm>
+
 #include "device_types.hpp"
 
 namespace moe {
@@ -38,7 +40,8 @@ __device__ __forceinline__ float wg_sum(float v, float *slot) {
 template <int K>
 __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs a) {
   __shared__ float slots[2][16];
-  const long long t = blockIdx.x;
+  const long long t = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+  if (t >= a.T) return;
   const int chunks = (a.d + 3) / 4;
   auto load = [&](const void *p, int type, long long row, int c) {
     return 4 * c + 4 <= a.d ? load4(p, type, row + 4 * c) : load_few(p, type, row + 4 * c, a.d & 3);
@@ -118,7 +121,9 @@ __global__ __launch_bounds__(1024) void block_norm_kernel(NormArgs a) {
 
 hipError_t launch_block_norm(const NormArgs &a, hipStream_t s) {
   const int chunks = (a.d + 3) / 4;
-  const dim3 grid((unsigned)a.T);
+  // a grid dimension holds fewer than 2^32 threads: 2^21 rows of up to 1024
+  const int gx = std::min(a.T, 1 << 21);
+  const dim3 grid((unsigned)gx, (unsigned)((a.T - 1) / gx + 1));
   auto threads = [&](int k) { return dim3(((chunks + k - 1) / k + 63) / 64 * 64); };
   // Accesses per thread: as many (up to 4) as leave the chip 2^18 threads, else
   // what a workgroup of 1024 needs.  More loads in flight per thread and fewer

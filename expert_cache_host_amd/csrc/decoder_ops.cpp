@@ -50,7 +50,7 @@ const char *batch_fault(const moe_kv_batch *b) {
   if (!b->pages || !b->start || !b->past) return "batch pointer is NULL";
   if (b->n_seqs < 1) return "n_seqs must be >= 1";
   if (b->max_pages < 1) return "max_pages must be >= 1";
-  if (b->n_rows < 0) return "n_rows must be >= 0";
+  if (b->n_rows < 0 || b->n_rows > MOE_KV_MAX_ROWS) return "n_rows must be in [0, 2^23]";
   for (const void *p : {(const void *)b->pages, (const void *)b->start, (const void *)b->past})
     if ((uintptr_t)p % 4) return "batch pointers must be 4-byte aligned";
   return nullptr;
@@ -63,6 +63,14 @@ moe::KvCache to_cache(const moe_kv_cache *c) {
 
 moe::KvBatch to_batch(const moe_kv_batch *b) {
   return {b->pages, b->start, b->past, b->n_seqs, b->max_pages, b->n_rows};
+}
+
+// A grid dimension holds fewer than 2^32 threads, 2^24 workgroups of attention; a
+// tile holds at least 8 of a KV head's rows.
+const char *tiles_fault(const moe_kv_cache *c, const moe_kv_batch *b, int32_t q_heads) {
+  if ((int64_t)b->n_rows * (q_heads / c->kv_heads) / 8 + b->n_seqs >= 1 << 24)
+    return "n_rows * q_heads / kv_heads / 8 + n_seqs must stay below 2^24";
+  return nullptr;
 }
 
 const char *heads_fault(const moe_kv_cache *c, int32_t q_heads) {
@@ -189,8 +197,7 @@ int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *b
   if (!f && bad_type(type)) f = "element type must be MOE_F32, MOE_BF16 or MOE_F16";
   if (!f) f = heads_fault(cache, q_heads);
   if (!f && window < 0) f = "window must be >= 0";
-  if (!f && (int64_t)batch->n_rows * q_heads > INT32_MAX - batch->n_seqs)
-    f = "n_rows * q_heads must stay below 2^31";
+  if (!f) f = tiles_fault(cache, batch, q_heads);
   if (f) return einval(f);
   return (int64_t)moe::kv_attend_ws_bytes(to_cache(cache), to_batch(batch), type, q_heads, window);
 }
@@ -209,8 +216,7 @@ moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, i
   if (q_stride < 0) return einval("input strides must be >= 0");
   if (batch->n_rows > 1 && out_stride < (int64_t)q_heads * cache->head_dim)
     return einval("out_stride must be >= q_heads * head_dim");
-  if ((int64_t)batch->n_rows * q_heads > INT32_MAX - batch->n_seqs)
-    return einval("n_rows * q_heads must stay below 2^31");
+  if (const char *f = tiles_fault(cache, batch, q_heads)) return einval(f);
   if (batch->n_rows == 0) return MOE_OK;
   if (!q || !out) return einval("q or out is NULL");
   if (misaligned(q, type) || misaligned(out, type))

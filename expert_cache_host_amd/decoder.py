@@ -3,7 +3,7 @@
 block_norm, q4_matvec over a Q4Matrix, and KVCache.append / attend / read: what a
 decoder layer needs around the routed MoE layer.  The formulas and layouts are
 set out in include/moe_cache.h.  Tensors are torch tensors on one GPU; calls go
-to the given stream, or to the current stream of that GPU.
+to the given stream, or to the current stream of that GPU; they record no gradients.
 """
 from __future__ import annotations
 
@@ -299,7 +299,7 @@ class KVCache:
         n, m = pages.shape if pages.dim() == 2 else (0, 0)
         if pages.get_device() != dev or start.get_device() != dev or past.get_device() != dev or \
                 pages.dtype != i32 or start.dtype != i32 or past.dtype != i32 or \
-                n < 1 or m < 1 or start.shape != (n + 1,) or past.shape != (n,) or \
+                not 1 <= n <= _I32 or not 1 <= m <= _I32 or start.shape != (n + 1,) or past.shape != (n,) or \
                 not (pages.is_contiguous() and start.is_contiguous() and past.is_contiguous()):
             raise ValueError("pages must be [n_seqs, max_pages], start [n_seqs + 1] and past [n_seqs], "
                              f"contiguous int32 on cuda:{dev}")

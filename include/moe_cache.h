@@ -448,6 +448,7 @@ moe_status moe_host_expert_forward(const void *expert_q4, int32_t d_model, int32
 #define MOE_Q4_MAX_ROWS (1 << 30)
 #define MOE_KV_MAX_PAGE_TOKENS 65536
 #define MOE_KV_MAX_HEADS 1024
+#define MOE_KV_MAX_ROWS (1 << 23)
 
 /* moe_block_norm -- a block's residual update and the norm before the next one:
  *
@@ -516,7 +517,7 @@ typedef struct moe_kv_batch {
   const int32_t *start; /* [n_seqs + 1] */
   const int32_t *past;  /* [n_seqs] */
   int32_t n_seqs, max_pages;
-  int32_t n_rows; /* rows of the tensors given with the batch */
+  int32_t n_rows; /* rows of the tensors given with the batch, <= MOE_KV_MAX_ROWS */
 } moe_kv_batch;
 
 /* moe_kv_append -- writes the new tokens' keys and values into the cache, keys
@@ -559,7 +560,8 @@ moe_status moe_kv_read(const moe_kv_cache *cache, const moe_kv_batch *batch, flo
  *   workspace  device memory of moe_kv_attend_workspace bytes (same arguments),
  *            16-byte aligned, for this call alone until its work is done
  *
- * Scores, softmax statistics and sums are float32. */
+ * Scores, softmax statistics and sums are float32.  n_rows * q_heads / kv_heads / 8
+ * + n_seqs must stay below 2^24. */
 int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
                                 int32_t q_heads, int32_t window);
 moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,

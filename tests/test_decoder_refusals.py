@@ -103,6 +103,19 @@ def test_cache(fn, kw, msg):
 
 
 @pytest.mark.parametrize("fn", [append, attend, read, need])
+def test_too_many_rows(fn):
+    assert fn(b=batch(n_rows=(1 << 23) + 1)) == EINVAL and "n_rows" in _err()
+
+
+@pytest.mark.parametrize("fn", [attend, need])
+@pytest.mark.parametrize("b,heads", [(dict(n_rows=1 << 23), 32), (dict(n_seqs=1 << 24), 4),
+                                     (dict(n_rows=1 << 23, n_seqs=(1 << 24) - (1 << 21)), 4)])
+def test_more_tiles_than_a_grid(fn, b, heads):
+    assert fn(b=batch(**b), heads=heads, **(dict(ldo=heads * 64) if fn is attend else {})) == EINVAL
+    assert "2^24" in _err()
+
+
+@pytest.mark.parametrize("fn", [append, attend, read, need])
 @pytest.mark.parametrize("kw,msg", BATCHES)
 def test_batch(fn, kw, msg):
     assert fn(b=batch(**kw)) == EINVAL and msg in _err()

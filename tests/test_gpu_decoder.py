@@ -99,6 +99,17 @@ def test_norm_parts_and_strides(parts, extra, shift):
         assert bool((base[:, :shift] == 7.5).all()) and bool((base[:, shift + d:] == 7.5).all())
 
 
+def test_norm_more_rows_than_a_grid_dimension():
+    """Small rows by the million (a norm per head, say): the rows on both sides of 2^21 and the last ones."""
+    T, d = (1 << 22) + 5, 8
+    g = gen(3)
+    h, y = rnd(g, T, d, dtype=torch.bfloat16), rnd(g, T, d, dtype=torch.bfloat16)
+    w = rnd(g, d)
+    gh, gx = m.block_norm(h, y, w, None, w)
+    at = torch.tensor([0, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, (1 << 22) - 1, 1 << 22, T - 1], device="cuda")
+    check_norm(h[at], y[at], w, None, w, "bf16", "bf16", gh[at], gx[at])
+
+
 def test_norm_in_place():
     g = gen(3)
     h, y, w1, w2 = rnd(g, 9, 2816), rnd(g, 9, 2816), 1 + rnd(g, 2816), 1 + rnd(g, 2816)
