@@ -29,8 +29,8 @@ __device__ __forceinline__ float finite_of(float v) {
 
 // A new token: its sequence, position and place in the cache.
 struct Place {
-  int s;
-  long long pos;  // -1: a row of no sequence, or a negative past
+  int s;          // -1: a row of no sequence
+  long long pos;  // -1: none (no sequence, or a negative past)
   // page * kv_heads * page_tokens + offset in the page, or -1 when the sequence
   // has no valid page there; head h's row is at this + h * page_tokens
   long long row;
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_any_kernel(KvAppendArgs a)
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
   const int t = blockIdx.x;
   const Place p = place_of(a.c, a.b, t);
-  if (p.pos < 0) return;
+  if (p.s < 0) return;
   const int D = a.c.head_dim, nb = D / 32, per = D / 8, n = a.c.kv_heads * per;
   for (int i = blockIdx.y * kThreads + threadIdx.x; i < 2 * n; i += gridDim.y * kThreads) {
     const bool is_v = i >= n;

@@ -309,8 +309,8 @@ class KVCache:
                q_out=None, stream=None):
         """Writes k, v [T, kv_heads * head_dim] into the cache, the keys rotated by their
         positions (inv_freq float32 [rot_dim / 2] or None); returns q [T, q_heads * head_dim]
-        rotated likewise, or None.  Rows of no sequence are left as they are in `q_out`
-        (undefined in a new one)."""
+        rotated likewise, or None.  Rows of no sequence, or of a negative past, are left as
+        they are in `q_out` (undefined in a new one)."""
         dev, D, dt = self._index, self.head_dim, k.dtype
         if _elsewhere(dev, stream):
             with _At(dev, stream):

@@ -528,7 +528,8 @@ typedef struct moe_kv_batch {
  *              inv_freq[j].  rot_dim 0: no rotation; below head_dim: the rest of the
  *              head is left as it is
  *   interleaved  0: pair j is elements (j, j + rot_dim / 2); 1: (2j, 2j + 1)
- *   q, q_out   [n_rows][q_heads][head_dim] of `type`, or both NULL
+ *   q, q_out   [n_rows][q_heads][head_dim] of `type`, or both NULL; rows of a negative
+ *              past, which have no position, are left as they are in q_out
  *
  * Angles, sines, cosines and the rotation are computed in binary64 and the result
  * rounded to float32 before it is coded.  Per block of 32: m = the first element

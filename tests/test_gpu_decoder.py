@@ -420,6 +420,28 @@ def test_append_holes():
     assert bool((gk[16:32] == 0).all()) and bool((gk[44:] == 0).all()) and bool((gk[:16] != 0).any())
 
 
+def test_read_and_append_with_a_negative_past():
+    """Rows of a negative past read 0, whatever stood in the output; their queries have no position and stay."""
+    from expert_cache_host_amd.decoder import _library
+    D, P, Hkv = 64, 16, 2
+    g = gen(6)
+    t = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    pages, start, past = t([[0, 1], [2, 3], [4, 5]]), t([0, 3, 8, 10]), t([4, -2, 0])
+    c = m.KVCache.create(6, P, Hkv, D)
+    k = rnd(g, 12, Hkv * D)
+    for freq in (None, torch.ones(32, device="cuda"), torch.ones(3, device="cuda")):
+        q_out = torch.full((12, Hkv * D), 7.5, device="cuda")
+        c.append(k, k, pages, start, past, q=k, inv_freq=freq, q_out=q_out)
+        kept = (q_out == 7.5).all(1)
+        assert kept.tolist() == [False] * 3 + [True] * 5 + [False] * 2 + [True] * 2
+        out = torch.full((2, 12, Hkv * D), 7.5, device="cuda")
+        b = c._batch(pages, start, past, 12)
+        assert _library().moe_kv_read(c._cp, b, out[0].data_ptr(), out[1].data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream) == 0
+        assert bool((out[:, 3:8] == 0).all()) and bool((out[:, 10:] == 7.5).all())
+        assert bool((out[:, :3] != 7.5).all()) and bool((out[:, 8:10] != 7.5).all())
+
+
 # ------------------------------------------------------------------ attention
 
 def fill_cache(g, n, P, Hkv, D, garbage=True, size=0.3):
