@@ -71,10 +71,22 @@ struct Matvec {
   // The wave's K slice of every token into X and xs; `first` is its first block.
   // Many parts: every lane converts the units of its own row of A.  The slice is
   // read twice (its largest element, then the parts), which holds no more
-  // registers than X.
+  // registers than X.  Binary16 tokens are taken as they are.
   __device__ __forceinline__ void stage_many(int first) {
     const int u = part_of_row(n), t = t0 + u / PL, p = u % PL;
     const bool mine = u < parts;
+    if constexpr (TY == kF16) {
+#pragma unroll
+      for (int b = 0; b < KT * 4; ++b) {
+        float v[8];
+        load_unit(mine, t, first + b, g, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) X[b][j] = (_Float16)v[j];
+      }
+#pragma unroll
+      for (int i = 0; i < FI; ++i) xs[i] = 1.f;
+      return;
+    }
     uint32_t top = 0;
 #pragma unroll
     for (int b = 0; b < KT * 4; ++b) {
@@ -120,7 +132,7 @@ struct Matvec {
       uint32_t top = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = max(top, __builtin_bit_cast(uint32_t, v[j]) & 0x7fffffffu);
-      const int e = scale_exp(wave_max_u32(top));
+      const int e = TY == kF16 ? 0 : scale_exp(wave_max_u32(top));
       const float f = exp2_int(-e);
       half8_t hi, lo;
 #pragma unroll
