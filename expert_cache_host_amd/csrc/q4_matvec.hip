@@ -214,6 +214,7 @@ __global__ __launch_bounds__(KT == 4 ? 768 : 1024) void q4_matvec_kernel(Q4Matve
     for (int j = threadIdx.x; j < 16 * tokens; j += blockDim.x) {
       const int t = j >> 4, row = tile * 16 + (j & 15);
       float v = 0.f;
+#pragma unroll 4
       for (int x = 0; x < m.waves; ++x)
 #pragma unroll
         for (int p = 0; p < PL; ++p) {
