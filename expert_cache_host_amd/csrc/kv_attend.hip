@@ -32,7 +32,7 @@
 // workgroup to a tile.
 //
 // Measured (GPU time): 32 sequences of 6000 to 16000 keys, 64 heads on 8 KV heads
-// of 128, bfloat16: 97 us and 7 us of joining, 3.75 TB/s (a large copy reaches
+// of 128, bfloat16: 95 us and 7 us of joining, 3.75 TB/s (a large copy reaches
 // 4.85; the vector units are busy half of the time, loads are waited for 40% of
 // it); 3 chunks of 490 tokens, 16 heads on 8 of 256, window 1024, binary16: 77 us;
 // 4 sequences of up to 500 keys: 7.1 us.
@@ -125,8 +125,8 @@ struct Split {
 // Equal parts of a tile of `steps` steps, by its own length and not the page
 // table's: as many as are wanted, if they leave every wave two steps, and none of
 // more than 64 steps.  (A part's start and end cost about two steps, the last one
-// to end sets the time: 32 sequences of 6000 to 16000 keys take 125 us with parts
-// of 48, 123 with 64, 128 with 96.)
+// to end sets the time: 32 sequences of 6000 to 16000 keys take 106 us with parts
+// of 48, 105 with 64, 110 with 96.)
 __host__ __device__ __forceinline__ long long parts_of_steps(const Split &sp, long long steps) {
   const long long by_size = (steps + 63) / 64, by_waves = (steps + 2 * kWaves - 1) / (2 * kWaves);
   const long long few = by_waves < sp.want ? by_waves : sp.want;

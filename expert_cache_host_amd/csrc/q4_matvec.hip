@@ -19,8 +19,8 @@
 // columns takes passes, the tokens laid out again for each.
 //
 // Measured (GPU time): one float32 token, 131072 x 2048: 36-38 us, 4.1 TB/s (a large
-// copy reaches 4.85); 8192 x 2816: 6.3 us, of which the weights need 2.7; four
-// bfloat16 tokens, 10240 x 6144: 14.6 us, where twelve waves a CU wait for loads
+// copy reaches 4.85); 8192 x 2816: 6.1 us, of which the weights need 2.7; four
+// bfloat16 tokens, 10240 x 6144: 14.5 us, where twelve waves a CU wait for loads
 // half of their time.
 #include <algorithm>
 
@@ -288,7 +288,7 @@ hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   const int gy = (a.T + tokens - 1) / tokens;
   // as many workgroups as the chip holds at a time, each with the same number of
   // visits, so that the tokens are laid out no more often than that (45 x 2144 x
-  // 5003 f16: 12.3 us; with a workgroup per tile 25.7)
+  // 5003 f16: 11.2 us; with a workgroup per tile 24.5)
   auto grid = [&](int waves, int visits) {
     const int fit = std::max(1, (KT == 4 ? 12 : KT == 2 ? 16 : 32) / waves);
     const int most = std::max(1, 256 * fit / gy), each = (visits + most - 1) / most;
@@ -330,8 +330,8 @@ hipError_t launch_parts(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   return launch_group<TY, KT, 4>(a, chunks, s);
 }
 
-// Chunks of K per wave: 2 up to 32 chunks (one float32 token, 131072 x 2048: 38 us
-// with 2, 40 with 1, 42 with 4), 4 above.
+// Chunks of K per wave: 2 up to 32 chunks (one float32 token, 131072 x 2048: 36 us
+// with 2, 39 with 1, 48 with 4), 4 above.
 template <int TY>
 hipError_t launch_cols(const Q4MatvecArgs &a, hipStream_t s) {
   const int chunks = (a.cols / 32 + 3) / 4;
