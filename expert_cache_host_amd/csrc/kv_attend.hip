@@ -298,9 +298,9 @@ struct Attend {
     }
   }
 
-  // Scores of the step's keys in units of `unit`, as the matrix cores leave them:
-  // s[x][i] is key 4 g + i of tile x against the lane's column.
-  __device__ __forceinline__ void scores(const half8_t (&Q)[NB], float (&s)[2][4]) const {
+  // Scores of the step's keys less `base`, in units of `unit`, as the matrix cores
+  // leave them: s[x][i] is key 4 g + i of tile x against the lane's column.
+  __device__ __forceinline__ void scores(const half8_t (&Q)[NB], float base, float (&s)[2][4]) const {
     const floatx4 z = {0.f, 0.f, 0.f, 0.f};
     uint4 both = make_uint4(0, 0, 0, 0);
     if constexpr (NB == 2) both = transpose_rows(kc[0]);  // both tiles' two blocks
@@ -309,7 +309,7 @@ struct Attend {
       Scales<NB> ks;
       ks.read(lds + (16 * x + 4 * g) * NB * 2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[x][i] = 0.f;
+      for (int i = 0; i < 4; ++i) s[x][i] = PL == 2 ? -0.5f * base : -base;
 #pragma unroll
       for (int h = 0; h < (NB + 3) / 4; ++h) {
         uint4 t = both;
@@ -443,8 +443,11 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
 #pragma unroll
   for (int b = 0; b < 2 * NB; ++b) O[b] = floatx4{0.f, 0.f, 0.f, 0.f};
   float off[NB] = {};
-  // running maximum (in units of `unit`) and sum
-  float top = -INFINITY, sum = 0.f;
+  // The probabilities' reference score (in units of `unit`), what a score may pass
+  // it by before it is raised (-inf before the first key), and the running sum.
+  // Scores come with the reference taken off, so that an exponent is as exact as
+  // their difference however large they are.
+  float base = 0.f, room = -INFINITY, sum = 0.f;
   float unit = 1.f;
   int vexp = -14;                    // value scales met so far lie below 2^(vexp + 1)
 
@@ -483,9 +486,12 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
         Q[b][j] = PL == 2 && n >= 8 ? y : x;
       }
     // a score's unit in log2: positive (a negative scale is q's sign), the raw
-    // codes' 2^24 in it.  (Beyond 2^116 in q the unit saturates: such rows' scores differ
-    // by far more than an exponential tells apart.)
-    unit = fmaxf(exp2_int(min(e + Attend<D, PL>::kUnitBits, 126)) * fabsf(a.scale * kLog2e), 1e-37f);
+    // codes' 2^24 in it.  At the bounds: scores that all differ by nothing, and
+    // scores of which any two that differ do so by more than an exponential tells
+    // apart, with none beyond float32 (15 * 32 codes, q below 2^14, scales below
+    // 2^16, NB blocks: below 2^42 units).
+    unit = ldexpf(fabsf(a.scale) * kLog2e, e + Attend<D, PL>::kUnitBits);
+    unit = fminf(fmaxf(unit, 1e-37f), Attend<D, PL>::kRaw ? 0x1p108f : 0x1p84f);
 
     for (int i = i0; i < i1; ++i) {
       const int key0 = (tile.step0 + i) * 32;
@@ -505,7 +511,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       w.sv.write(w.lds + 64 * NB, w.lane);
       const uint32_t sb = w.sv.top();
       float s[2][4];
-      w.scores(Q, s);
+      w.scores(Q, base, s);
       w.load_k(at);
       if (!whole) {
         // keys the row does not see
@@ -519,10 +525,25 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       }
       float m = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      if (__any((m - top) * unit > kSlack)) {
-        const float to = fmaxf(top, rows_max(m));
-        const float f = to == -INFINITY ? 1.f : exp2f((top - to) * unit);
-        top = to;
+      if (__any(m > room)) {
+        const float up = rows_max(m);
+        const bool first = room == -INFINITY;
+        // rounded down, so that the largest score does not end below its reference
+        float to = up == -INFINITY ? base : base + (first ? up : fmaxf(up, 0.f));
+        if (to - base > up && to != base) to = nextafterf(to, -INFINITY);
+        const float d = to - base;
+        const float f = first ? 1.f : exp2f(-d * unit);
+        base = to;
+        if (up != -INFINITY) room = kSlack / unit;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[x][j] -= d;
+            // where even the sum's rounding is more than the room, scores that
+            // float32 does not tell apart count the same
+            s[x][j] = s[x][j] > room ? room : s[x][j];
+          }
         sum *= f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) off[b] *= f;
@@ -543,11 +564,11 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
 #pragma unroll
           for (int j = 0; j < 4; ++j) O[b][j] *= f;
       }
-      const float ref = fmaf(top == -INFINITY ? 0.f : top, unit, (float)(vexp - kHead));
+      const float head = (float)(kHead - vexp);
       float p[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(fmaf(s[j >> 2][j & 3], unit, -ref));
+        p[j] = __builtin_amdgcn_exp2f(fmaf(s[j >> 2][j & 3], unit, head));
         sum += p[j];
       }
       w.weigh(p, O, off);
@@ -557,8 +578,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
 
   // join the waves: reference of the column's sums, -inf when it saw no key
   sum = rows_sum(sum);
-  const float ref =
-      sum == 0.f ? -INFINITY : fmaf(top == -INFINITY ? 0.f : top, unit, (float)(vexp - kHead));
+  const float ref = sum == 0.f ? -INFINITY : fmaf(base, unit, (float)(vexp - kHead));
   __syncthreads();  // an earlier part's sums have been read
   if (g == 0 && n < RT) sh.ref[wave][n] = ref, sh.sum[wave][n] = sum;
 #pragma unroll

@@ -593,6 +593,42 @@ def test_attend_magnitudes(ty, ksize, vsize, qsize):
     check_attend(c, q, pages, start, pst, D ** -0.5, 0, got, ty)
 
 
+@pytest.mark.parametrize("ty,qsize,ksize,scale", [
+    (ty, *a) for a in [(1e3, 30.0, 0.1), (6e4, 500.0, 0.1), (6e4, 500.0, -0.1), (1e12, 0.3, 0.1), (1e30, 0.3, 0.1),
+                       (3e38, 0.3, 0.1), (3e38, 0.3, -1e-30), (1e-30, 500.0, 1e38)]
+    for ty in TYPES if ty != "f16" or a[0] < 65504 and a[0] > 1e-7])
+def test_attend_scores_beyond_an_exponential(ty, qsize, ksize, scale):
+    """Scores so far apart that the softmax is the largest one's key alone, up to where float32 cannot hold them."""
+    for D, Hkv, G in ((64, 1, 2), (128, 1, 4), (256, 2, 1)):
+        P, g = 32, gen(D + 1)
+        new, past = [3, 1], [700, 90]
+        pages, start, pst, n = make_batch(new, past, P, 7)
+        c = fill_cache(g, n, P, Hkv, D)
+        c.tensors[1].copy_((torch.rand(c.tensors[1].shape, generator=g, device="cuda") - 0.5) * 2 * ksize)
+        q = ((torch.rand(4, Hkv * G * D, generator=g, device="cuda") - 0.5) * 2 * qsize).to(TYPES[ty])
+        got = f64(c.attend(q, pages, start, pst, scale)).reshape(4, Hkv * G, D)
+        total = torch.tensor([a + b for a, b in zip(new, past)])
+        every = torch.tensor([0, int(total[0]), int(total.sum())], dtype=torch.int32, device="cuda")
+        kk, vv = (f64(x) for x in c.read(pages, every, torch.zeros_like(pst), int(every[-1])))
+        qn, checked = f64(q).reshape(4, Hkv * G, D), 0
+        for t in range(4):
+            s, i = (0, t) if t < 3 else (1, 0)
+            at = slice(int(every[s]), int(every[s]) + past[s] + i + 1)
+            for h in range(Hkv * G):
+                k, v = kk[at, h // G], vv[at, h // G]
+                z, mag = k @ qn[t, h] * scale, np.abs(k) @ np.abs(qn[t, h]) * abs(scale)
+                top = int(z.argmax())
+                # float32 sums: see check_attend, 8 times the magnitudes stands for codes as stored; 100 apart
+                # leaves e^-100
+                if not (np.delete(z, top) + 100 + 64 * U * 8 * (mag.max() + np.abs(z).max()) < z[top]).all():
+                    continue
+                checked += 1
+                part = 2.0 ** -11 if ty != "f32" else 2.0 ** -21
+                assert np.all(np.abs(got[t, h] - v[top]) <= (part + 40 * U + HALF[ty]) * 1.01 * np.abs(v[top])
+                              + 8 * U * 23 * 0.3), (D, t, h)
+        assert checked >= 2 * Hkv * G
+
+
 def test_attend_shared_prefix_and_many_sequences():
     """300 sequences in one call (more than one probe of the search), many of them on the same prefix pages."""
     D, P, Hkv, G, S = 64, 16, 2, 2, 300
