@@ -406,13 +406,13 @@ template <int D, int TY>
 struct Shared {
   static constexpr int RT = rows_of(TY);
   float o[kWaves][RT][D + 4];
-  float ref[kWaves][RT], sum[kWaves][RT];
+  float ref[kWaves][RT], sum[kWaves][RT], unit[RT];
   __attribute__((aligned(16))) char scales[kWaves][128 * (D / 32)];
 };
 
 // Steps c0 .. c1 - 1 of a tile and KV head by one workgroup: to `out` when they
-// are all of its steps, else as a part: RT rows of D sums in part_o, their
-// references and sums of probabilities in part_l.
+// are all of its steps, else as a part: RT rows of D sums in part_o; their
+// references, sums of probabilities and units in part_l.
 template <int D, int TY>
 __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kvh, const Tile &tile,
                                             int c0, int c1, float *part_o,
@@ -576,23 +576,32 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
     }
   }
 
-  // join the waves: reference of the column's sums, -inf when it saw no key
-  sum = rows_sum(sum);
-  const float ref = sum == 0.f ? -INFINITY : fmaf(base, unit, (float)(vexp - kHead));
+  // Join the waves.  Their sums go there without the value scales' power of two, so
+  // that they differ by their references alone, and those stay what they are: a
+  // score beside the unit it counts in (-inf where no key was seen).  The
+  // difference of two references is taken before it is multiplied by the unit: as
+  // one number in log2 a reference past 2^24 would hold neither the power of two
+  // nor the difference of two close scores.
+  const float back = exp2_int(vexp);
+  sum = rows_sum(sum) * back;
   __syncthreads();  // an earlier part's sums have been read
-  if (g == 0 && n < RT) sh.ref[wave][n] = ref, sh.sum[wave][n] = sum;
+  if (g == 0 && n < RT) {
+    sh.ref[wave][n] = sum == 0.f ? -INFINITY : base;
+    sh.sum[wave][n] = sum;
+    if (wave == 0) sh.unit[n] = unit;  // the same for every wave with a step, and wave 0 has one
+  }
 #pragma unroll
   for (int b = 0; b < 2 * NB; ++b) {
     // the sums of the raw codes (units of 2^-24, of 2^-20 for the second nibbles)
     // without their offset of 8
     if constexpr (Attend<D, PL>::kRaw) {
-      const float eight = 8.f * rows_sum(off[b / 2]);
+      const float eight = 8.f * back * rows_sum(off[b / 2]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) O[b][j] = fmaf(O[b][j], b & 1 ? 0x1p20f : 0x1p24f, -eight);
+      for (int j = 0; j < 4; ++j) O[b][j] = fmaf(O[b][j], (b & 1 ? 0x1p20f : 0x1p24f) * back, -eight);
     }
     if constexpr (PL == 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) O[b][j] += other_half(O[b][j]);
+      for (int j = 0; j < 4; ++j) O[b][j] = (O[b][j] + other_half(O[b][j])) * back;
     }
     if (n < RT) *(floatx4 *)&sh.o[wave][n][b * 16 + 4 * g] = O[b];
   }
@@ -603,6 +612,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
     const int rr = tile.first + r, tk = rr / G;
     const long long tt = (long long)tile.t0 + tk;
     if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    const float unit_r = sh.unit[r];
     float best = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kWaves; ++x) best = fmaxf(best, sh.ref[x][r]);
@@ -610,7 +620,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int x = 0; x < kWaves; ++x) {
-      const float f = sh.ref[x][r] == -INFINITY ? 0.f : exp2f(sh.ref[x][r] - best);
+      const float f = sh.ref[x][r] == -INFINITY ? 0.f : exp2f((sh.ref[x][r] - best) * unit_r);
       l = fmaf(f, sh.sum[x][r], l);
       const floatx4 v = *(const floatx4 *)&sh.o[x][r][d];
 #pragma unroll
@@ -622,7 +632,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       for (int k = 0; k < 4; ++k) store1(a.out, TY, to + k, l == 0.f ? 0.f : o[k] / l);
     } else {
       *(floatx4 *)(part_o + r * D + d) = o;
-      if (d == 0) part_l[r] = best, part_l[RT + r] = l;
+      if (d == 0) part_l[r] = best, part_l[RT + r] = l, part_l[2 * RT + r] = unit_r;
     }
   }
 }
@@ -633,7 +643,7 @@ template <int D>
 constexpr int waves_per_simd() { return D == 64 ? 4 : D == 128 ? 3 : 2; }
 
 // A workgroup per tile, KV head and part.  The workspace holds RT rows of D sums
-// per part, then the parts' references and sums of probabilities.
+// per part, then the parts' references, sums of probabilities and units.
 template <int D, int TY>
 __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_kernel(
     KvAttendArgs a, Split sp) {
@@ -650,7 +660,7 @@ __global__ __launch_bounds__(kWaves * 64, waves_per_simd<D>()) void kv_attend_ke
   const size_t slots = (size_t)gridDim.x * a.c.kv_heads * sp.most;
   float *ws = (float *)a.ws;
   attend_part<D, TY>(a, G, kvh, tile, c0, c1, ws + slot * RT * D,
-                     ws + slots * RT * D + slot * RT * 2, sh);
+                     ws + slots * RT * D + slot * RT * 3, sh);
 }
 
 // Joins a tile's parts where there are several.
@@ -665,22 +675,23 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, Split sp) 
   const size_t slot = ((size_t)blockIdx.x * a.c.kv_heads + kvh) * sp.most;
   const size_t slots = (size_t)gridDim.x * a.c.kv_heads * sp.most;
   const float *o_parts = (const float *)a.ws + slot * RT * D;
-  const float *l_parts = (const float *)a.ws + slots * RT * D + slot * RT * 2;
+  const float *l_parts = (const float *)a.ws + slots * RT * D + slot * RT * 3;
   for (int j = threadIdx.x; j < RT * D / 4; j += 256) {
     const int r = j / (D / 4), d = j % (D / 4) * 4;
     const int rr = tile.first + r;
     const long long tt = (long long)tile.t0 + rr / G;
     if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    const float unit = l_parts[2 * RT + r];  // the same in every part
     float best = -INFINITY;
 #pragma unroll 8
-    for (int x = 0; x < parts; ++x) best = fmaxf(best, l_parts[x * RT * 2 + r]);
+    for (int x = 0; x < parts; ++x) best = fmaxf(best, l_parts[x * RT * 3 + r]);
     float l = 0.f;
     floatx4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int x = 0; x < parts; ++x) {
-      const float ref = l_parts[x * RT * 2 + r];
-      const float f = ref == -INFINITY ? 0.f : exp2f(ref - best);
-      l = fmaf(f, l_parts[x * RT * 2 + RT + r], l);
+      const float ref = l_parts[x * RT * 3 + r];
+      const float f = ref == -INFINITY ? 0.f : exp2f((ref - best) * unit);
+      l = fmaf(f, l_parts[x * RT * 3 + RT + r], l);
       const floatx4 v = *(const floatx4 *)(o_parts + ((size_t)x * RT + r) * D + d);
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] = fmaf(f, v[k], o[k]);
@@ -736,7 +747,7 @@ size_t kv_attend_ws_bytes(const KvCache &c, const KvBatch &b, int type, int q_he
   const int most = split_of(c, b, type, q_heads, window).most;
   if (most == 1) return 0;
   return (size_t)tiles_bound(c, b, type, q_heads) * c.kv_heads * most * rows_of(type) *
-         (c.head_dim + 2) * sizeof(float);
+         (c.head_dim + 3) * sizeof(float);
 }
 
 hipError_t launch_kv_attend(const KvAttendArgs &a, hipStream_t s) {
