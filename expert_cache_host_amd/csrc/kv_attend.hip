@@ -507,8 +507,10 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
           if constexpr (NB == 8) w.sv.w[1] = 0;
         }
       }
+      wave_lds_order();  // the last step's scales have been read
       w.sk.write(w.lds, w.lane);
       w.sv.write(w.lds + 64 * NB, w.lane);
+      wave_lds_order();  // and these are read by other lanes
       const uint32_t sb = w.sv.top();
       float s[2][4];
       w.scores(Q, base, s);

@@ -147,17 +147,14 @@ struct Matvec {
       }
       if (g / PL == t) xs[0] = exp2_int(e);  // C's one register in row g: part g
     }
-    // the units are read by the wave that wrote them: order the LDS accesses
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_order();  // the units are read by the wave that wrote them
 #pragma unroll
     for (int k = 0; k < KT * 4; ++k) {
       uint4 r = make_uint4(0, 0, 0, 0);
       if (u < parts) r = buf[u][4 * k + g];
       X[k] = __builtin_bit_cast(half8_t, r);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();  // the next pass's are written over them
   }
 };
 

@@ -114,6 +114,15 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return rows_max_u32(v);
 }
 
+// Between LDS writes of a wave's lanes and its other lanes' reads of them, or such
+// reads and the next writes over them: LDS serves a wave's accesses in order, and
+// this holds the compiler to their order, whatever types they are made through.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Exponent e for which |v| * 2^-e lies below 2^14 for every v whose magnitude
 // bits are at most `bits` (the bits of the largest, as an integer), kept where
 // 2^e and 2^-e are normal floats.  Infinities and NaN clamp at the top.
