@@ -22,10 +22,17 @@
 //    is rounded to binary16.
 //
 // A float32 row takes two columns of 16 (hi and lo binary16 parts of q and of
-// the scaled probabilities, 22 bits), a half-width row one.  The columns' power
-// of two for q, and for the probabilities the largest value scale met so far,
-// keep binary16 in range whatever the magnitudes are; the running maximum is
-// raised only when a score passes it by 2^4 (the sums' common factor cancels).
+// the scaled probabilities, 22 bits), a half-width row one (11 bits).  Powers of
+// two keep binary16 in range whatever the magnitudes are: the columns' for q, and
+// for the scaled probabilities that of the largest value scale a wave has met so
+// far, of any block.  So a product of probability and value scale is held to 2^-35
+// of the largest value scale, beside its relative rounding: values whose scales
+// lie more than 2^13 (float32; half-width types 2^24) below the largest of their
+// KV head lose digits, which no cache of real values comes near.  (A power per
+// block of 32, applied on the scales' way through LDS, was built: its registers
+// spill, and it took 135 us for 104 at decode and 161 for 77 for chunks.)  The
+// running maximum is raised only when a score passes it by 2^4 (the sums' common
+// factor cancels).
 //
 // Keys are split over the waves of a workgroup and over workgroups; the parts
 // are joined in LDS, and by a second kernel when there is more than one

@@ -561,8 +561,10 @@ moe_status moe_kv_read(const moe_kv_cache *cache, const moe_kv_batch *batch, flo
  *   workspace  device memory of moe_kv_attend_workspace bytes (same arguments),
  *            16-byte aligned, for this call alone until its work is done
  *
- * Scores, softmax statistics and sums are float32.  n_rows * q_heads / kv_heads / 8
- * + n_seqs must stay below 2^24. */
+ * Scores, softmax statistics and sums are float32.  A product of probability and
+ * value scale is held to 2^-35 of the largest value scale of its KV head (or of
+ * 2^-14, if that is larger) at least.
+ * n_rows * q_heads / kv_heads / 8 + n_seqs must stay below 2^24. */
 int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
                                 int32_t q_heads, int32_t window);
 moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,

@@ -66,3 +66,68 @@ def test_attend_close_scores_far_from_zero(D, ty, q0, scale, steps, n, at):
     tol = (PART[ty] + (4 * 32 + 24) * U) * mag + len(at) * 2.0 ** -35 * 8 * float(vs.max())
     tol = tol + HALF[ty] * (np.abs(ref) + tol)
     assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
+
+
+def one_sequence(g, n, P, D, ks, vs, Hkv=1):
+    """A cache of one sequence of n keys with random codes and the given scales [n, Hkv, D / 32]; what it holds."""
+    pages, start, past, n_pages = make_batch([1], [n - 1], P, 1)
+    c = fill_cache(g, n_pages, P, Hkv, D)
+    pg = pages.cpu().numpy()[0, np.arange(n) // P].astype(np.int64)
+    at = (torch.from_numpy(pg).cuda(), slice(None), torch.arange(n, device="cuda") % P)
+    c.tensors[1][at] = torch.from_numpy(np.ascontiguousarray(ks.astype(np.float16))).cuda()
+    c.tensors[3][at] = torch.from_numpy(np.ascontiguousarray(vs.astype(np.float16))).cuda()
+    kq, kf, vq, vf = (t[at].cpu().numpy() for t in c.tensors)
+    vq = vq.transpose(0, 1, 3, 2)
+    k = o.q4_decode(np.concatenate([kq & 15, kq >> 4], -1), kf)
+    v = o.q4_decode(np.concatenate([vq & 15, vq >> 4], -1), vf)
+    return c, pages, start, past, k, v
+
+
+@pytest.mark.parametrize("n", [40, 300, 5000])
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("D,spread", [(64, 13), (64, 20), (128, 13), (128, 20), (256, 20), (128, 26)])
+def test_attend_value_blocks_of_very_different_size(D, spread, ty, n):
+    """Blocks of 32 value elements up to 2^spread apart: each keeps its relative precision down to 2^-35 of the
+    largest value scale per key."""
+    g, nb = gen(n + D), D // 32
+    rng = np.random.default_rng(n)
+    size = 2.0 ** (spread - 17 - (np.arange(nb) * spread // (nb - 1))[::-1 if n == 300 else 1])
+    vs = rng.uniform(0.5, 1, (n, 1, nb)) * size
+    c, pages, start, past, k, v = one_sequence(g, n, 32, D, np.zeros((n, 1, nb)), vs)  # all scores are 0
+    q = torch.randn(1, 3 * D, generator=g, device="cuda").to(TYPES[ty])
+    got = f64(c.attend(q, pages, start, past, D ** -0.5)).reshape(3, D)
+    ref, mag, per = v[:, 0].mean(0), np.abs(v[:, 0]).mean(0), np.repeat(size, 32)
+    # equal probabilities: the parts' rounding, sums of n terms of codes 0..15 as stored and of their offset of 8
+    # (23 value scales a term), and the stated bound
+    tol = PART[ty] * mag + 2 * (n + 40) * U * 23 * per + 23 * 2.0 ** -35 * size.max()
+    tol = tol + HALF[ty] * (np.abs(ref) + tol) + (2.0 ** -25 if ty == "f16" else 0)
+    for h in range(3):
+        assert np.all(np.abs(got[h] - ref) <= tol), (h, (np.abs(got[h] - ref) / tol).reshape(nb, 32).max(1))
+
+
+@pytest.mark.parametrize("ratio", [12, 20, 28])
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_a_large_value_without_weight(D, ty, ratio):
+    """A visible key whose value scales are 2^ratio times the others' but whose probability is nothing: the others
+    keep what 2^-35 of that scale per key leaves them."""
+    n, nb, g = 200, D // 32, gen(D + ratio)
+    rng = np.random.default_rng(ratio)
+    ks, vs = np.zeros((n, 1, nb)), rng.uniform(0.5, 1, (n, 1, nb)) * 2.0 ** -13
+    c, pages, start, past, k, v = one_sequence(g, n, 32, D, ks, vs)
+    for p in (3, 90, 150):
+        # the first element's key code 0 (value -8) at scale 8: score -64 * 60 against 0
+        pg = int(pages[0, p // 32])
+        c.tensors[0][pg, 0, p % 32, 0, 0] &= 0xf0
+        c.tensors[1][pg, 0, p % 32, 0] = 8.0
+        c.tensors[3][pg, 0, p % 32] = 2.0 ** (ratio - 13)
+    q = torch.zeros(1, D, device="cuda")
+    q[0, 0] = 60
+    got = f64(c.attend(q.to(TYPES[ty]), pages, start, past, 1.0)).reshape(D)
+    rest = np.setdiff1d(np.arange(n), [3, 90, 150])
+    ref = v[rest, 0].mean(0)
+    # equal probabilities, exact scores: the parts' rounding, sums of n terms of raw codes, the stated bound
+    mag = np.abs(v[rest, 0]).mean(0)
+    tol = PART[ty] * mag + 2 * (n + 40) * U * 23 * 2.0 ** -13 + 23 * 2.0 ** (ratio - 13) * 2.0 ** -35
+    tol = tol + HALF[ty] * (np.abs(ref) + tol) + (2.0 ** -25 if ty == "f16" else 0)
+    assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
