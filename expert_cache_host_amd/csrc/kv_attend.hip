@@ -359,6 +359,11 @@ struct Attend {
 
   // O += V^T P^T for the step's probabilities p (key j of K slot j); with raw codes
   // off[b] sums what their offset of 8 multiplies.
+  // Half-width types take one binary16 part of p times the scale.  Relative error
+  // against binary64 (root mean square), where float32 products rounded at the end
+  // have 1.66e-3 (bfloat16, 32 sequences of ~12000 keys) and 2.08e-4 (binary16, 3
+  // chunks of 490): 1.67e-3 and 2.55e-4, less than the output's own half step.  A
+  // pair of parts was measured: as float32 products, but 118 us for 104 and 92 for 77.
   __device__ __forceinline__ void weigh(const float (&p)[8], floatx4 (&O)[2 * NB],
                                         float (&off)[NB]) const {
     const uint32_t lo_part = PL == 2 && n >= 8 ? 0xffffffffu : 0u;

@@ -487,7 +487,9 @@ moe_status moe_block_norm(const void *h, int32_t h_type, int64_t h_stride, const
  *
  * Meant for the few tokens of decode (weights are read once for up to 8 float32
  * or 16 half-width tokens); n_tokens <= MOE_Q4_MAX_TOKENS, rows <=
- * MOE_Q4_MAX_ROWS.  Sums are float32.  cols must be a multiple of group. */
+ * MOE_Q4_MAX_ROWS.  Sums are float32; x enters the matrix cores as binary16, MOE_F32
+ * as a pair of parts (22 bits), held to 2^-38 of the token's largest element at
+ * least.  cols must be a multiple of group. */
 moe_status moe_q4_matvec(const void *codes, const void *scales, int32_t rows, int32_t cols,
                          int32_t group, const void *x, int32_t type, int64_t x_stride,
                          int32_t n_tokens, void *out, int64_t out_stride, moe_stream_t stream);
@@ -561,9 +563,11 @@ moe_status moe_kv_read(const moe_kv_cache *cache, const moe_kv_batch *batch, flo
  *   workspace  device memory of moe_kv_attend_workspace bytes (same arguments),
  *            16-byte aligned, for this call alone until its work is done
  *
- * Scores, softmax statistics and sums are float32.  A product of probability and
- * value scale is held to 2^-35 of the largest value scale of its KV head (or of
- * 2^-14, if that is larger) at least.
+ * Scores, softmax statistics and sums are float32.  Queries, and the products of
+ * probabilities and value scales, enter the matrix cores as binary16: as a pair of
+ * parts (22 bits) for MOE_F32, as one part (11 bits) for the half-width types.
+ * Elements of q are held to 2^-34 of the row's largest at least, such a product to
+ * 2^-35 of the largest value scale of its KV head (or of 2^-14, if that is larger).
  * n_rows * q_heads / kv_heads / 8 + n_seqs must stay below 2^24. */
 int64_t moe_kv_attend_workspace(const moe_kv_cache *cache, const moe_kv_batch *batch, int32_t type,
                                 int32_t q_heads, int32_t window);
