@@ -66,13 +66,20 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 constexpr int parts_of(int type) { return type == kF32 ? 2 : 1; }
 constexpr int rows_of(int type) { return 16 / parts_of(type); }
 
-// Rows of a tile of sequence s, and the 32-key steps that some row of it sees.
+// Rows of a tile of sequence s, and the 32-key steps that some row of it sees.  Of
+// a sequence that begins before the tensors' first row or ends past their last,
+// the rows in them are the ones counted.
 struct Tile {
   int s, first, rows;  // sequence, first row of the tile in it, rows of the sequence
-  int t0;              // packed row of the sequence's first token
-  int past;
+  int t0;              // packed row of the sequence's first token in the tensors
+  long long past;      // that token's position, -1 in a hole
   int step0, steps;
 };
+
+// First packed row of sequence s in the tensors.
+__device__ __forceinline__ int row_start(const KvBatch &b, int s) {
+  return min(max(b.start[s], 0), b.T);
+}
 
 // First tile of sequence s when tiles of RT rows never span sequences: an upper
 // bound of the tiles before it that needs no running count.
@@ -84,13 +91,12 @@ __device__ __forceinline__ long long position_cap(const KvAttendArgs &a) {
   return min((long long)a.b.max_pages * a.c.page_tokens, (long long)kMaxPos);
 }
 
-// Fills in a tile of sequence o.s from the sequence's rows start .. end; false
-// when the tile has no row.
+// Fills in a tile of sequence o.s from the sequence's rows start .. end in the
+// tensors; false when the tile has no row.
 __device__ __forceinline__ bool fill_tile(const KvAttendArgs &a, int G, int RT, long long tile,
                                           int start_0, int start, int end, Tile &o) {
   o.t0 = start;
-  // at most the batch's rows, whatever stands in `start`
-  o.rows = (int)min(max((long long)end - start, 0ll), (long long)a.b.T) * G;
+  o.rows = max(end - start, 0) * G;
   o.steps = 0;
   const long long first = (tile - tile_base(start, start_0, o.s, G, RT)) * RT;
   if (first < 0 || first >= o.rows) return false;
@@ -98,9 +104,8 @@ __device__ __forceinline__ bool fill_tile(const KvAttendArgs &a, int G, int RT, 
   if (o.past < 0) return true;
   const int tok0 = o.first / G, tok1 = (min(o.first + RT, o.rows) - 1) / G;
   const long long cap = position_cap(a);
-  const int hi = (int)min((long long)o.past + tok1 + 1, cap);
-  const int lo =
-      a.window > 0 ? (int)min(max((long long)o.past + tok0 + 1 - a.window, 0ll), cap) : 0;
+  const int hi = (int)min(o.past + tok1 + 1, cap);
+  const int lo = a.window > 0 ? (int)min(max(o.past + tok0 + 1 - a.window, 0ll), cap) : 0;
   o.step0 = lo / 32;
   o.steps = max(0, (hi + 31) / 32 - o.step0);
   return true;
@@ -110,18 +115,18 @@ __device__ __forceinline__ bool fill_tile(const KvAttendArgs &a, int G, int RT, 
 // probe (one load's latency for up to 64 sequences, two up to 4096).
 __device__ __forceinline__ bool find_tile(const KvAttendArgs &a, int G, int RT, long long tile,
                                           Tile &o) {
-  const int lane = threadIdx.x & 63, start_0 = a.b.start[0];
+  const int lane = threadIdx.x & 63, start_0 = row_start(a.b, 0);
   int lo = 0, hi = a.b.n_seqs;  // the last s in [lo, hi) whose first tile is at most `tile`
   while (hi - lo > 1) {
     const int each = (hi - lo + 63) / 64, s = lo + lane * each;
-    const bool before = s < hi && tile_base(a.b.start[min(s, hi - 1)], start_0, s, G, RT) <= tile;
+    const bool before = s < hi && tile_base(row_start(a.b, min(s, hi - 1)), start_0, s, G, RT) <= tile;
     lo += (max(__popcll(__ballot(before)), 1) - 1) * each;
     hi = min(hi, lo + each);
   }
   o.s = uniform(lo);
-  o.past = uniform(a.b.past[o.s]);
-  return fill_tile(a, G, RT, tile, uniform(start_0), uniform(a.b.start[o.s]),
-                   uniform(a.b.start[o.s + 1]), o);
+  const int past = uniform(a.b.past[o.s]), start = uniform(row_start(a.b, o.s));
+  o.past = past < 0 ? -1 : (long long)past + start - uniform(a.b.start[o.s]);
+  return fill_tile(a, G, RT, tile, uniform(start_0), start, uniform(row_start(a.b, o.s + 1)), o);
 }
 
 // How tiles are cut into parts, a workgroup each.
@@ -437,15 +442,13 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
   // the lane's column: row n % RT of the tile, part n / RT of it
   const int row = tile.first + n % RT, tok = row / G, head = kvh * G + row % G;
   const long long t = (long long)tile.t0 + tok, past = tile.past;
-  const bool live = row < tile.rows && t >= 0 && t < a.b.T;
+  const bool live = row < tile.rows;
   const long long cap = position_cap(a);
   const int hi = live ? (int)min(past + tok + 1, cap) : 0;
   const int lo_key = a.window > 0 ? (int)min(max(past + tok + 1 - a.window, 0ll), cap) : 0;
-  // keys that every row sees, and the range of the keys that some row of the
-  // batch sees (its tokens may end inside the tile)
+  // keys that every row sees, and the range of the keys that some row sees
   const int tok0 = tile.first / G, tok1 = (min(tile.first + RT, tile.rows) - 1) / G;
-  const long long last = min((long long)tok1, (long long)a.b.T - 1 - tile.t0);
-  const int hi_max = (int)min(past + last + 1, cap), hi_min = (int)min(past + tok0 + 1, cap);
+  const int hi_max = (int)min(past + tok1 + 1, cap), hi_min = (int)min(past + tok0 + 1, cap);
   const int lo_max = a.window > 0 ? (int)min(max(past + tok1 + 1 - a.window, 0ll), cap) : 0;
   const int lo_min = a.window > 0 ? (int)min(max(past + tok0 + 1 - a.window, 0ll), cap) : 0;
   const int per = (c1 - c0 + kWaves - 1) / kWaves;
@@ -625,7 +628,7 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
     const int r = j / (D / 4), d = j % (D / 4) * 4;
     const int rr = tile.first + r, tk = rr / G;
     const long long tt = (long long)tile.t0 + tk;
-    if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    if (rr >= tile.rows) continue;
     const float unit_r = sh.unit[r];
     float best = -INFINITY;
 #pragma unroll
@@ -694,7 +697,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttendArgs a, Split sp) 
     const int r = j / (D / 4), d = j % (D / 4) * 4;
     const int rr = tile.first + r;
     const long long tt = (long long)tile.t0 + rr / G;
-    if (rr >= tile.rows || tt < 0 || tt >= a.b.T) continue;
+    if (rr >= tile.rows) continue;
     const float unit = l_parts[2 * RT + r];  // the same in every part
     float best = -INFINITY;
 #pragma unroll 8

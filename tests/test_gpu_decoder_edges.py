@@ -8,7 +8,7 @@ import torch
 
 import expert_cache_host_amd as m
 from oracle import decoder as o
-from test_gpu_decoder import HALF, TYPES, U, f64, fill_cache, gen, make_batch
+from test_gpu_decoder import HALF, TYPES, U, check_attend, f64, fill_cache, gen, make_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,38 @@ def test_attend_a_large_value_without_weight(D, ty, ratio):
     tol = PART[ty] * mag + 2 * (n + 40) * U * 23 * 2.0 ** -13 + 23 * 2.0 ** (ratio - 13) * 2.0 ** -35
     tol = tol + HALF[ty] * (np.abs(ref) + tol) + (2.0 ** -25 if ty == "f16" else 0)
     assert np.all(np.abs(got - ref) <= tol), (np.abs(got - ref) / tol).max()
+
+
+# ------------------------------------------------------------------ batches that pass the tensors' ends
+
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("D,G,window", [(64, 1, 0), (128, 4, 0), (128, 5, 9), (256, 2, 40)])
+def test_sequences_that_begin_before_the_tensors(D, G, window, ty):
+    """start may begin below 0: append, read and attention take the rows that the tensors hold, each at its
+    position, as the same rows in a longer batch."""
+    P, Hkv, g, before = 16, 2, gen(D + G), 150
+    start = torch.tensor([-150, -141, -30, 40, 41, 43], dtype=torch.int32, device="cuda")
+    past = torch.tensor([4, 9, 33, 70, -3], dtype=torch.int32, device="cuda")
+    pages = torch.arange(5 * 16, dtype=torch.int32, device="cuda").view(5, 16)
+    T = 47  # four rows of no sequence at the end
+    k, v = (torch.randn(before + T, Hkv * D, generator=g, device="cuda").to(TYPES[ty]) for _ in range(2))
+    q = torch.randn(before + T, Hkv * G * D, generator=g, device="cuda").to(TYPES[ty])
+    f = torch.full((D // 2,), 0.01, device="cuda")
+    whole = fill_cache(g, 80, P, Hkv, D)
+    held = m.KVCache(*(t.clone() for t in whole.tensors))
+    want_q = torch.full_like(q, 7.5)
+    whole.append(k, v, pages, start + before, past, q=q, inv_freq=f, q_out=want_q)
+    got_q = torch.full_like(q[before:], 7.5)
+    held.append(k[before:], v[before:], pages, start, past, q=q[before:], inv_freq=f, q_out=got_q)
+    assert torch.equal(got_q, want_q[before:])
+    for a, b in zip(whole.read(pages, start + before, past, before + T), held.read(pages, start, past, T)):
+        assert torch.equal(a[before:before + 43], b[:43])
+    # attention over the whole batch's cache: the same rows in both calls
+    want, got = torch.full_like(q, 7.5), torch.full_like(q[before:], 7.5)
+    whole.attend(q, pages, start + before, past, 0.1, window=window, out=want)
+    whole.attend(q[before:], pages, start, past, 0.1, window=window, out=got)
+    assert bool((got[43:] == 7.5).all()) and bool((got[41:43] == 0).all())
+    # tiles are cut at other rows, so sums may be joined in another order: see check_attend for the parts
+    check_attend(whole, q, pages, start + before, past, 0.1, window, want, ty, rows=range(before, before + 43))
+    shifted = torch.cat([want[:before], got])
+    check_attend(whole, q, pages, start + before, past, 0.1, window, shifted, ty, rows=range(before, before + 43))
