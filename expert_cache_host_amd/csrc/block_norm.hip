@@ -133,15 +133,10 @@ hipError_t launch_block_norm(const NormArgs &a, hipStream_t s) {
   int k = 4;
   while (k > 1 && (long long)a.T * chunks / k < 1 << 18) k /= 2;
   while (chunks > 1024 * k) k *= 2;
-  if (k <= 1)
-    block_norm_kernel<1><<<grid, threads(1), 0, s>>>(a);
-  else if (k <= 2)
-    block_norm_kernel<2><<<grid, threads(2), 0, s>>>(a);
-  else if (k <= 4)
-    block_norm_kernel<4><<<grid, threads(4), 0, s>>>(a);
-  else
-    block_norm_kernel<8><<<grid, threads(8), 0, s>>>(a);
-  return hipGetLastError();
+  if (k <= 1) return launch(block_norm_kernel<1>, grid, threads(1), s, a);
+  if (k <= 2) return launch(block_norm_kernel<2>, grid, threads(2), s, a);
+  if (k <= 4) return launch(block_norm_kernel<4>, grid, threads(4), s, a);
+  return launch(block_norm_kernel<8>, grid, threads(8), s, a);
 }
 
 }  // namespace moe

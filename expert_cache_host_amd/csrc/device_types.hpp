@@ -3,9 +3,22 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "decoder_ops.hpp"
 
 namespace moe {
+
+// Launches a kernel and returns this launch's own status.  (The thread's last HIP
+// error, all that the launch syntax leaves, may be that of an earlier call of the
+// caller's, which would then fail a call whose kernel runs.)
+template <class... P>
+hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, std::common_type_t<P>... args) {
+  void *p[] = {(void *)&args...};
+  const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, p, 0, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t b) {
   return __builtin_bit_cast(float, b << 16);

@@ -744,11 +744,10 @@ template <int D, int TY>
 hipError_t launch_one(const KvAttendArgs &a, hipStream_t s) {
   const Split sp = split_of(a.c, a.b, a.type, a.q_heads, a.window);
   const unsigned tiles = (unsigned)tiles_bound(a.c, a.b, a.type, a.q_heads);
-  kv_attend_kernel<D, TY><<<dim3(tiles, (unsigned)(a.c.kv_heads * sp.most)), kWaves * 64, 0, s>>>(a, sp);
-  if (sp.most > 1)
-    kv_join_kernel<D, TY>
-        <<<dim3(tiles, (unsigned)a.c.kv_heads), 256, 0, s>>>(a, sp);
-  return hipGetLastError();
+  const hipError_t e = launch(kv_attend_kernel<D, TY>, dim3(tiles, (unsigned)(a.c.kv_heads * sp.most)),
+                              kWaves * 64, s, a, sp);
+  if (e != hipSuccess || sp.most == 1) return e;
+  return launch(kv_join_kernel<D, TY>, dim3(tiles, (unsigned)a.c.kv_heads), 256, s, a, sp);
 }
 
 template <int TY>

@@ -318,10 +318,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
 
 hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s) {
   if (a.b.T == 0) return hipSuccess;
-  if (a.rot_dim % 8) {
-    kv_append_any_kernel<<<dim3((unsigned)a.b.T), kThreads, 0, s>>>(a);
-    return hipGetLastError();
-  }
+  if (a.rot_dim % 8) return launch(kv_append_any_kernel, dim3((unsigned)a.b.T), kThreads, s, a);
   const int per = a.c.head_dim / 8, fit = kThreads / per;
   const int heads = fit < a.c.kv_heads ? fit : a.c.kv_heads;
   const int kv_groups = (a.c.kv_heads + heads - 1) / heads;
@@ -330,21 +327,16 @@ hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t s) {
   int q_groups = (a.q_heads * per + kThreads - 1) / kThreads;
   if (a.b.T > 512) q_groups = (q_groups + 3) / 4;
   const dim3 grid((unsigned)a.b.T, (unsigned)(kv_groups + q_groups));
-  if (a.type == kF32)
-    kv_append_kernel<kF32><<<grid, kThreads, 0, s>>>(a, kv_groups, heads);
-  else if (a.type == kBf16)
-    kv_append_kernel<kBf16><<<grid, kThreads, 0, s>>>(a, kv_groups, heads);
-  else
-    kv_append_kernel<kF16><<<grid, kThreads, 0, s>>>(a, kv_groups, heads);
-  return hipGetLastError();
+  if (a.type == kF32) return launch(kv_append_kernel<kF32>, grid, kThreads, s, a, kv_groups, heads);
+  if (a.type == kBf16) return launch(kv_append_kernel<kBf16>, grid, kThreads, s, a, kv_groups, heads);
+  return launch(kv_append_kernel<kF16>, grid, kThreads, s, a, kv_groups, heads);
 }
 
 hipError_t launch_kv_read(const KvReadArgs &a, hipStream_t s) {
   if (a.b.T == 0) return hipSuccess;
   int groups = (2 * a.c.kv_heads * (a.c.head_dim / 8) + kThreads - 1) / kThreads;
   if (a.b.T > 512) groups = (groups + 3) / 4;
-  kv_read_kernel<<<dim3((unsigned)a.b.T, (unsigned)groups), kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  return launch(kv_read_kernel, dim3((unsigned)a.b.T, (unsigned)groups), kThreads, s, a);
 }
 
 }  // namespace moe

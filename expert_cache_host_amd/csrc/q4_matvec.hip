@@ -293,7 +293,7 @@ hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   };
   if (KT < 4 || chunks <= kPassChunks) {
     const int waves = (chunks + KT - 1) / KT;
-    q4_matvec_kernel<TY, KT, FI, GB, 0><<<grid(waves, tiles), waves * 64, 0, s>>>(a, 1);
+    return launch(q4_matvec_kernel<TY, KT, FI, GB, 0>, grid(waves, tiles), waves * 64, s, a, 1);
   } else if constexpr (KT == 4) {
     const int passes = (chunks + kPassChunks - 1) / kPassChunks;
     const int waves = (chunks + 4 * passes - 1) / (4 * passes);
@@ -301,15 +301,12 @@ hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
     // over the chip (one token, 8192 x 12288: 31 us with four, 23 with one; 16
     // float32 tokens, 8192 x 8192: 54 with four, 105 with one); below 128 visits of
     // four the chip stands too empty for it.
-    if (FI > 1 && (long long)(tiles / 4) * gy >= 128) {
-      if constexpr (FI > 1)
-        q4_matvec_kernel<TY, 4, FI, GB, 4>
-            <<<grid(waves, (tiles + 3) / 4), waves * 64, 0, s>>>(a, passes);
-    } else {
-      q4_matvec_kernel<TY, 4, FI, GB, 1><<<grid(waves, tiles), waves * 64, 0, s>>>(a, passes);
-    }
+    if constexpr (FI > 1)
+      if ((long long)(tiles / 4) * gy >= 128)
+        return launch(q4_matvec_kernel<TY, 4, FI, GB, 4>, grid(waves, (tiles + 3) / 4), waves * 64, s, a, passes);
+    return launch(q4_matvec_kernel<TY, 4, FI, GB, 1>, grid(waves, tiles), waves * 64, s, a, passes);
   }
-  return hipGetLastError();
+  return hipErrorInvalidValue;  // not reached: fewer chunks per wave hold all of K
 }
 
 template <int TY, int KT, int FI>

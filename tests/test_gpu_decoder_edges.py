@@ -166,3 +166,37 @@ def test_sequences_that_begin_before_the_tensors(D, G, window, ty):
     check_attend(whole, q, pages, start + before, past, 0.1, window, want, ty, rows=range(before, before + 43))
     shifted = torch.cat([want[:before], got])
     check_attend(whole, q, pages, start + before, past, 0.1, window, shifted, ty, rows=range(before, before + 43))
+
+
+# ------------------------------------------------------------------ the caller's surroundings
+
+def test_an_earlier_error_of_the_caller_fails_no_call():
+    """A HIP error that the caller has not fetched yet is neither a call's result nor taken away by it."""
+    import ctypes
+    hip = ctypes.CDLL(m.lib_path())  # the runtime the library is linked to
+    D, P, g = 64, 16, gen(91)
+    x, w, out = torch.randn(2, D, generator=g, device="cuda"), torch.ones(D, device="cuda"), torch.empty(2, D, device="cuda")
+    c = m.KVCache.create(2, P, 1, D)
+    mat = m.Q4Matrix(torch.full((D, D // 32, 16), 0x99, dtype=torch.uint8, device="cuda"),
+                     torch.ones(D, D // 32, dtype=torch.float16, device="cuda"))
+    pages, start, past = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([[1]], [0, 2], [0]))
+    k, f = x.clone(), torch.ones(3, device="cuda")
+    read = c.read(pages, start, past, 2)  # allocations are cached from here on
+    att = c.attend(x, pages, start, past, 1.0, out=out).clone()
+    torch.cuda.synchronize()
+    del read, att
+    calls = [lambda: m.block_norm(x, pre_w=w, x_out=out), lambda: m.q4_matvec(x, mat, out=out),
+             lambda: c.append(k, k, pages, start, past, q=x, q_out=out), lambda: c.read(pages, start, past, 2),
+             lambda: c.append(k, k, pages, start, past, inv_freq=f),
+             lambda: c.attend(x, pages, start, past, 1.0, out=out)]
+    try:
+        for call in calls:
+            hip.hipGetLastError()
+            assert hip.hipSetDevice(4096) != 0
+            call()
+            assert hip.hipGetLastError() != 0
+    finally:
+        hip.hipGetLastError()
+        torch.cuda.synchronize()
+    want = x.double().sum(1, keepdim=True)  # 64 weights of 1: see check_matvec's 160 roundings
+    assert bool(((m.q4_matvec(x, mat) - want).abs() <= 160 * U * x.abs().sum(1, keepdim=True)).all())
