@@ -4,6 +4,9 @@ block_norm, q4_matvec over a Q4Matrix, and KVCache.append / attend / read: what 
 decoder layer needs around the routed MoE layer.  The formulas and layouts are
 set out in include/moe_cache.h.  Tensors are torch tensors on one GPU; calls go
 to the given stream, or to the current stream of that GPU; they record no gradients.
+A given stream is not made to wait for the current one: the caller orders it behind
+the work that fills the inputs.  Tensors given to such a call may be dropped at once;
+what it allocates belongs to the given stream.
 """
 from __future__ import annotations
 
@@ -62,10 +65,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 class _At:
     """Makes a device and a stream current, so that the launch and what the call allocates
-    belong to them."""
+    belong to them; the stream's use of `tensors` is recorded, so that their memory is not
+    given out again before the call has run."""
 
-    def __init__(self, index, stream):
+    def __init__(self, index, stream, *tensors):
         self.guards = [torch.cuda.device(index)]
+        self.stream, self.tensors = stream, tensors
         if stream is not None:
             if stream.device.index != index:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
@@ -76,6 +81,10 @@ class _At:
             g.__enter__()
 
     def __exit__(self, *exc):
+        if self.stream is not None and exc[0] is None:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
         for g in reversed(self.guards):
             g.__exit__(*exc)
         return False
@@ -140,7 +149,7 @@ def block_norm(h, y=None, post_w=None, gate=None, pre_w=None, *, res_scale: floa
     """
     dev = _cuda(h, "h")
     if _elsewhere(dev, stream):
-        with _At(dev, stream):
+        with _At(dev, stream, h, y, post_w, gate, pre_w, h_out, x_out):
             return block_norm(h, y, post_w, gate, pre_w, res_scale=res_scale, block_scale=block_scale, eps=eps,
                               h_out=h_out, x_out=x_out, x_dtype=x_dtype)
     ldh = _rows(h, "h", dev)
@@ -234,7 +243,7 @@ def q4_matvec(x, w: Q4Matrix, out=None, stream=None):
     """out [T, rows] = x [T, cols] times w transposed, in x's type (float32 sums)."""
     dev = w._index
     if _elsewhere(dev, stream):
-        with _At(dev, stream):
+        with _At(dev, stream, x, w.codes, w.scales, out):
             return q4_matvec(x, w, out)
     ldx = _rows(x, "x", dev, None, w.cols)
     T, dt = x.shape[0], x.dtype
@@ -313,7 +322,7 @@ class KVCache:
         they are in `q_out` (undefined in a new one)."""
         dev, D, dt = self._index, self.head_dim, k.dtype
         if _elsewhere(dev, stream):
-            with _At(dev, stream):
+            with _At(dev, stream, k, v, pages, start, past, q, inv_freq, q_out, *self.tensors):
                 return self.append(k, v, pages, start, past, q, inv_freq, interleaved, q_out)
         ldk = _rows(k, "k", dev, None, self.kv_heads * D)
         T = k.shape[0]
@@ -359,7 +368,7 @@ class KVCache:
         if not 0 <= rows <= _I32:
             raise ValueError("rows must be in [0, 2^31)")
         if _elsewhere(self._index, stream):
-            with _At(self._index, stream):
+            with _At(self._index, stream, pages, start, past, *self.tensors):
                 return self.read(pages, start, past, rows)
         b = self._batch(pages, start, past, rows)
         k = torch.empty((rows, self.kv_heads, self.head_dim), dtype=torch.float32, device=self.device)
@@ -375,7 +384,7 @@ class KVCache:
         are left as they are in `out` (undefined in a new one)."""
         dev, dt = self._index, q.dtype
         if _elsewhere(dev, stream):
-            with _At(dev, stream):
+            with _At(dev, stream, q, pages, start, past, out, *self.tensors):
                 return self.attend(q, pages, start, past, scale, window, out)
         ldq = _rows(q, "q", dev)
         T, n = q.shape

@@ -200,3 +200,47 @@ def test_an_earlier_error_of_the_caller_fails_no_call():
         torch.cuda.synchronize()
     want = x.double().sum(1, keepdim=True)  # 64 weights of 1: see check_matvec's 160 roundings
     assert bool(((m.q4_matvec(x, mat) - want).abs() <= 160 * U * x.abs().sum(1, keepdim=True)).all())
+
+
+@pytest.mark.parametrize("op", ["norm", "matvec", "append", "read", "attend"])
+def test_tensors_dropped_while_another_stream_reads_them(op):
+    """Inputs of a call on another stream may be dropped at once: their memory is not given out before it has run."""
+    s, g = torch.cuda.Stream(), gen(92)
+    D, T = 64, 513
+    new = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    busy = torch.zeros(8192, 8192, device="cuda")
+    c = m.KVCache.create(40, 16, 1, D)
+    start, past = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([0, T], [0]))
+    pages = torch.arange(40, dtype=torch.int32, device="cuda").view(1, 40)
+    ops = {"norm": lambda t: m.block_norm(t[0], t[1], pre_w=t[2], gate=t[3], post_w=t[4], h_out=t[5], x_out=t[6], stream=s),
+           "matvec": lambda t: m.q4_matvec(t[0], m.Q4Matrix(t[1], t[2]), out=t[3], stream=s),
+           "append": lambda t: c.append(t[0], t[1], t[2], t[3], t[4], q=t[5], inv_freq=t[6], q_out=t[7], stream=s),
+           "read": lambda t: m.KVCache(*t[:4]).read(t[4], t[5], t[6], T, stream=s),
+           "attend": lambda t: c.attend(t[0], t[1], t[2], t[3], 1.0, out=t[4], stream=s)}
+    make = {"norm": lambda: [new(T, D), new(T, D), new(D), new(T, D), new(D), new(T, D), new(T, D)],
+            "matvec": lambda: [new(3, 1024), torch.zeros(512, 32, 16, dtype=torch.uint8, device="cuda"),
+                               torch.ones(512, 32, dtype=torch.float16, device="cuda"), new(3, 512)],
+            "append": lambda: [new(T, D), new(T, D), pages.clone(), start.clone(), past.clone(), new(T, D),
+                               new(D // 2), new(T, D)],
+            "read": lambda: [t.clone() for t in c.tensors] + [pages.clone(), start.clone(), past.clone()],
+            "attend": lambda: [new(T, D), pages.clone(), start.clone(), past.clone(), new(T, D)]}
+    ops[op](make[op]())  # what is loaded at first use
+    torch.cuda.synchronize()
+    inputs = make[op]()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(30):  # some 10 ms each
+            torch.mm(busy, busy)
+        done = torch.cuda.Event()
+        done.record()
+    held = {t.data_ptr(): (t.shape, t.dtype) for t in inputs}
+    kept = ops[op](inputs)
+    del inputs
+    # the same sizes again from the same pool, never written
+    again = [torch.empty(shape, dtype=dtype, device="cuda") for shape, dtype in held.values()]
+    early = not done.query()
+    taken = {t.data_ptr() for t in again} & set(held)
+    torch.cuda.synchronize()
+    del kept
+    assert early, "the stream was not kept busy long enough"
+    assert not taken
