@@ -8,7 +8,8 @@ import torch
 
 import expert_cache_host_amd as m
 from oracle import decoder as o
-from test_gpu_decoder import HALF, TYPES, U, check_attend, f64, fill_cache, gen, make_batch
+from test_gpu_decoder import (HALF, TYPES, U, check_attend, check_matvec, f64, fill_cache, gen, make_batch, make_q4,
+                              rnd, spoil)
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +245,71 @@ def test_tensors_dropped_while_another_stream_reads_them(op):
     del kept
     assert early, "the stream was not kept busy long enough"
     assert not taken
+
+
+# ------------------------------------------------------------------ launch shapes of large calls
+
+@pytest.mark.parametrize("rows,cols,group", [(70001, 512, 32), (9001, 4096, 64), (9001, 6144, 128), (6017, 2144, 32),
+                                             (9001, 8192, 32), (9001, 8256, 64), (8200, 12288, 128)])
+@pytest.mark.parametrize("ty", list(TYPES))
+def test_matvec_several_tiles_a_workgroup(rows, cols, group, ty):
+    """More tiles of rows than workgroups fit the chip: each takes several in turn, with the next one's loads in
+    flight; above 6144 columns one or four tiles a visit (from 5 parts of tokens on), the last visit not full."""
+    g = gen(rows + cols)
+    codes, scales = make_q4(g, rows, cols, group)
+    w = m.Q4Matrix(codes, scales)
+    for T in (1, 4, 8, 16, 37):
+        x = rnd(g, T, cols, scale=2, dtype=TYPES[ty])
+        out = torch.full((T, rows + 3), 7.5, device="cuda", dtype=TYPES[ty])
+        m.q4_matvec(x, w, out=out[:, :rows])
+        check_matvec(x, codes, scales, out[:, :rows], ty)
+        assert bool((out[:, rows:] == 7.5).all())
+
+
+@pytest.mark.parametrize("D,Hkv,G", [(256, 32, 2), (128, 8, 4), (64, 1, 3)])
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (6, False)])
+def test_append_and_read_of_long_prompts(D, Hkv, G, ty, rot, inter):
+    """More than 512 tokens in a call: fewer workgroups a token, each with several chunks of heads."""
+    g, P = gen(D + rot), 48
+    new, past = [300, 1, 291], [7, 100, 0]
+    pages, start, pst, n = make_batch(new, past, P, D)
+    T = sum(new)
+    c = m.KVCache.create(n, P, Hkv, D)
+    q, k, v = (rnd(g, T, h * D, scale=2, dtype=TYPES[ty]) for h in (G * Hkv, Hkv, Hkv))
+    f = torch.from_numpy((1000.0 ** (-np.arange(rot // 2) * 2 / rot)).astype(np.float32)).cuda()
+    got = c.append(k, v, pages, start, pst, q=q, inv_freq=f, interleaved=inter).float().cpu().numpy()
+    pos = np.concatenate([np.arange(p, p + w) for p, w in zip(past, new)])
+    turn = lambda t, h: o.rotate(f64(t).reshape(T, h, D), pos, f.cpu().numpy(), inter)  # noqa: E731
+    ref = turn(q, G * Hkv).reshape(T, -1)
+    # as in test_append_and_read: binary64 rounded to float32, then to the type
+    assert np.all(np.abs(got - ref) <= (HALF[ty] + 2 * U) * np.abs(ref) + 2e-7 * (ty == "f16"))
+    gk, gv = c.read(pages, start, pst, T)
+    assert np.array_equal(gk.double().cpu().numpy(), o.q4_decode(*o.q4_encode(turn(k, Hkv))))
+    assert np.array_equal(gv.double().cpu().numpy(),
+                          o.q4_decode(*o.q4_encode(f64(v).reshape(T, Hkv, D).astype(np.float32))))
+
+
+@pytest.mark.parametrize("ty", list(TYPES))
+def test_attend_garbage_around_many_sequences(ty):
+    """Shared prefixes, hundreds of sequences and a long one: scales that are NaN or infinite wherever no key of the
+    batch lies stay out of every result."""
+    D, P, Hkv, G, S = 64, 16, 2, 2, 300
+    g, rng = gen(93), np.random.default_rng(4)
+    past = rng.integers(0, 90, S)
+    past[17] = 9000
+    pages = np.full((S, 564), -1, np.int32)
+    for s in range(S):
+        k = (past[s] + P) // P
+        pages[s, :k] = [(s % 7) * 6 + j if j + 1 < k else 42 + s for j in range(k)] if s != 17 else 342 + np.arange(k)
+    start = np.arange(S + 1)
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    pages, start, past_d = t(pages), t(start), t(past)
+    c = fill_cache(g, 342 + 563, P, Hkv, D)
+    q = rnd(g, S, Hkv * G * D, dtype=TYPES[ty])
+    want = c.attend(q, pages, start, past_d, D ** -0.5)
+    # pages 0 .. 41 are shared by sequences of different lengths: those are full up to their last shared page
+    spoil(c, pages, [int(p) + 1 for p in past], P)
+    got = c.attend(q, pages, start, past_d, D ** -0.5)
+    assert torch.equal(got, want)
+    check_attend(c, q, pages, start, past_d, D ** -0.5, 0, got, ty, rows=[0, 5, 17, 100, 299])
