@@ -490,8 +490,14 @@ __device__ __forceinline__ void attend_part(const KvAttendArgs &a, int G, int kv
       for (int j = 0; j < 8; ++j)
         big = max(big, __builtin_bit_cast(uint32_t, v[b][j]) & 0x7fffffffu);
     }
-    const int e = scale_exp(rows_max_u32(big));
-    const float f = a.scale == 0.f ? 0.f : a.scale < 0.f ? -exp2_int(-e) : exp2_int(-e);
+    big = rows_max_u32(big);
+    const int e = scale_exp(big);
+    // a row with an infinity or a NaN has no finite score: NaN, and not the -inf that
+    // stands for unseen keys
+    const float f = big >= 0x7f800000u ? __builtin_nanf("")
+                    : a.scale == 0.f   ? 0.f
+                    : a.scale < 0.f    ? -exp2_int(-e)
+                                       : exp2_int(-e);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll

@@ -313,3 +313,29 @@ def test_attend_garbage_around_many_sequences(ty):
     got = c.attend(q, pages, start, past_d, D ** -0.5)
     assert torch.equal(got, want)
     check_attend(c, q, pages, start, past_d, D ** -0.5, 0, got, ty, rows=[0, 5, 17, 100, 299])
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+@pytest.mark.parametrize("ty", list(TYPES))
+def test_attend_non_finite_queries(D, G, ty):
+    """An infinite or NaN element of a query makes that row's head NaN (every visible key's score is infinite or NaN,
+    all minus infinity among them) and no other's; a row that sees no key is 0 all the same."""
+    P, Hkv, g = 16, 2, gen(94)
+    new, past = [1, 1, 4, 1, 1], [0, 3, 60, 2500, -7]
+    pages, start, pst, n = make_batch(new, [max(p, 0) for p in past], P, 5)
+    pst = torch.tensor(past, dtype=torch.int32, device="cuda")
+    c = fill_cache(g, n, P, Hkv, D)
+    q = rnd(g, 8, Hkv * G * D, dtype=TYPES[ty])
+    sound = q.clone()
+    bad = [(t, h, e) for t, h, e in ((0, 0, 3), (1, 0, 0), (3, Hkv * G - 1, D - 1), (4, 0, 17), (6, Hkv * G - 1, 40), (7, 0, 1))]
+    for i, (t, h, e) in enumerate(bad):
+        for value in (float("inf"), float("-inf"), float("nan")):
+            q.copy_(sound)
+            q[t, h * D + e] = value
+            for scale in (0.1, -0.1):
+                got = c.attend(q, pages, start, pst, scale)
+                own = got.view(8, Hkv * G, D)[t, h]
+                assert bool((own == 0).all() if t == 7 else own.isnan().all()), (t, h, value, scale)
+                if i % 2 == 0 and scale > 0:
+                    got.view(8, Hkv * G, D)[t, h] = c.attend(sound, pages, start, pst, scale).view(8, Hkv * G, D)[t, h]
+                    check_attend(c, sound, pages, start, pst, scale, 0, got, ty, rows=[0, 1, 2, 3, 4, 5])
