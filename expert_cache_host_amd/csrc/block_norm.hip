@@ -7,9 +7,10 @@
 //
 // One workgroup per row; the row stays in registers between the two sums, so
 // every input is read once and every output written once.  x is formed from h'
-// before its rounding to the residual's type.  Bound by memory traffic (4.6 TB/s
-// at 4093 x 2045 f16 with a gate per element, 3.7 TB/s at 512 x 6144); a single
-// row is bound by the launch and two workgroup sums (3.9 us at d = 2816).
+// before its rounding to the residual's type.  Bound by memory traffic (3.9 TB/s
+// at 4093 x 2045 f16 with a gate per element, 3.4 TB/s at 512 x 6144, where a large
+// copy reaches 5.1; 4.8 and 3.7 on inputs in the last-level cache); a single row is
+// bound by the launch and two workgroup sums (3.8 us at d = 2816).
 #include <algorithm>
 
 #include "device_types.hpp"

@@ -39,10 +39,10 @@
 // workgroup to a tile.
 //
 // Measured (GPU time): 32 sequences of 6000 to 16000 keys, 64 heads on 8 KV heads
-// of 128, bfloat16: 95 us and 7 us of joining, 3.75 TB/s (a large copy reaches
-// 4.85; the vector units are busy half of the time, loads are waited for 40% of
-// it); 3 chunks of 490 tokens, 16 heads on 8 of 256, window 1024, binary16: 77 us;
-// 4 sequences of up to 500 keys: 7.1 us.
+// of 128, bfloat16: 94 us and 7 us of joining, 3.9 TB/s (a large copy reaches 5.1;
+// the vector units are busy half of the time, loads are waited for a third of it);
+// 3 chunks of 490 tokens, 16 heads on 8 of 256, window 1024, binary16: 77 us (80 on
+// inputs past the last-level cache); 4 sequences of up to 500 keys: 7.2 us.
 #include <algorithm>
 
 #include "device_types.hpp"

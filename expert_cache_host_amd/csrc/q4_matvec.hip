@@ -18,10 +18,10 @@
 // multiplied; the waves' sums meet in LDS, a barrier per tile.  K beyond 6144
 // columns takes passes, the tokens laid out again for each.
 //
-// Measured (GPU time): one float32 token, 131072 x 2048: 36-38 us, 4.1 TB/s (a large
-// copy reaches 4.85); 8192 x 2816: 6.1 us, of which the weights need 2.7; four
-// bfloat16 tokens, 10240 x 6144: 14.5 us, where twelve waves a CU wait for loads
-// half of their time.
+// Measured (GPU time, inputs past the last-level cache): one float32 token, 131072 x
+// 2048: 34 us, 4.45 TB/s (a large copy reaches 5.1); 8192 x 2816: 6.5 us, of which
+// the weights need 2.6; four bfloat16 tokens, 10240 x 6144: 15.5 us, where twelve
+// waves a CU wait for loads half of their time.
 #include <algorithm>
 
 #include "device_types.hpp"
@@ -283,9 +283,10 @@ template <int TY, int KT, int FI, int GB>
 hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
   const int tiles = (a.rows + 15) / 16, tokens = 4 * FI / parts_of(TY);
   const int gy = (a.T + tokens - 1) / tokens;
-  // as many workgroups as the chip holds at a time, each with the same number of
-  // visits, so that the tokens are laid out no more often than that (45 x 2144 x
-  // 5003 f16: 11.2 us; with a workgroup per tile 24.5)
+  // Each workgroup with the same number of visits, and no more of them than 12, 16
+  // or 32 waves a CU make (by the chunks a wave holds; the instantiations of few
+  // tokens would fit more), so that the tokens are laid out no more often than that
+  // (45 x 2144 x 5003 f16: 10.8 us; with a workgroup per tile 24.5)
   auto grid = [&](int waves, int visits) {
     const int fit = std::max(1, (KT == 4 ? 12 : KT == 2 ? 16 : 32) / waves);
     const int most = std::max(1, 256 * fit / gy), each = (visits + most - 1) / most;
@@ -299,8 +300,9 @@ hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
     const int waves = (chunks + 4 * passes - 1) / (4 * passes);
     // Four tiles a visit share the laying out of many tokens, one spreads the tiles
     // over the chip (one token, 8192 x 12288: 31 us with four, 23 with one; 16
-    // float32 tokens, 8192 x 8192: 54 with four, 105 with one); below 128 visits of
-    // four the chip stands too empty for it.
+    // float32 tokens, 8192 x 8192: 54 with four, 105 with one, though the four tiles'
+    // kernels spill 22 to 40 registers); below 128 visits of four the chip stands too
+    // empty for it.
     if constexpr (FI > 1)
       if ((long long)(tiles / 4) * gy >= 128)
         return launch(q4_matvec_kernel<TY, 4, FI, GB, 4>, grid(waves, (tiles + 3) / 4), waves * 64, s, a, passes);
