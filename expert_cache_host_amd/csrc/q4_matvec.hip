@@ -292,23 +292,22 @@ hipError_t launch_one(const Q4MatvecArgs &a, int chunks, hipStream_t s) {
     const int most = std::max(1, 256 * fit / gy), each = (visits + most - 1) / most;
     return dim3((unsigned)((visits + each - 1) / each), (unsigned)gy);
   };
-  if (KT < 4 || chunks <= kPassChunks) {
-    const int waves = (chunks + KT - 1) / KT;
-    return launch(q4_matvec_kernel<TY, KT, FI, GB, 0>, grid(waves, tiles), waves * 64, s, a, 1);
-  } else if constexpr (KT == 4) {
-    const int passes = (chunks + kPassChunks - 1) / kPassChunks;
-    const int waves = (chunks + 4 * passes - 1) / (4 * passes);
-    // Four tiles a visit share the laying out of many tokens, one spreads the tiles
-    // over the chip (one token, 8192 x 12288: 31 us with four, 23 with one; 16
-    // float32 tokens, 8192 x 8192: 54 with four, 105 with one, though the four tiles'
-    // kernels spill 22 to 40 registers); below 128 visits of four the chip stands too
-    // empty for it.
-    if constexpr (FI > 1)
-      if ((long long)(tiles / 4) * gy >= 128)
-        return launch(q4_matvec_kernel<TY, 4, FI, GB, 4>, grid(waves, (tiles + 3) / 4), waves * 64, s, a, passes);
-    return launch(q4_matvec_kernel<TY, 4, FI, GB, 1>, grid(waves, tiles), waves * 64, s, a, passes);
-  }
-  return hipErrorInvalidValue;  // not reached: fewer chunks per wave hold all of K
+  if constexpr (KT == 4)
+    if (chunks > kPassChunks) {
+      const int passes = (chunks + kPassChunks - 1) / kPassChunks;
+      const int waves = (chunks + 4 * passes - 1) / (4 * passes);
+      // Four tiles a visit share the laying out of many tokens, one spreads the tiles
+      // over the chip (one token, 8192 x 12288: 31 us with four, 23 with one; 16
+      // float32 tokens, 8192 x 8192: 54 with four, 105 with one, though the four
+      // tiles' kernels spill 22 to 40 registers); below 128 visits of four the chip
+      // stands too empty for it.
+      if constexpr (FI > 1)
+        if ((long long)(tiles / 4) * gy >= 128)
+          return launch(q4_matvec_kernel<TY, 4, FI, GB, 4>, grid(waves, (tiles + 3) / 4), waves * 64, s, a, passes);
+      return launch(q4_matvec_kernel<TY, 4, FI, GB, 1>, grid(waves, tiles), waves * 64, s, a, passes);
+    }
+  const int waves = (chunks + KT - 1) / KT;
+  return launch(q4_matvec_kernel<TY, KT, FI, GB, 0>, grid(waves, tiles), waves * 64, s, a, 1);
 }
 
 template <int TY, int KT, int FI>

@@ -511,10 +511,10 @@ typedef struct moe_kv_cache {
  * sequence s's new tokens, at positions past[s], past[s] + 1, ...; position p lies
  * on page pages[s][p / page_tokens].  start holds n_seqs + 1 ascending entries;
  * rows outside [start[0], start[n_seqs]) belong to no sequence: they are neither
- * read nor written.  Entries below 0 or past n_rows are allowed: the tokens of the
- * rows that the tensors do not hold are left out, the others keep their positions.  A page outside [0, n_pages), a position past the table (or
- * past 2^31 - 257) and a negative past are holes: nothing is written there and no
- * key is seen there. */
+ * read nor written.  Entries below 0 or past n_rows are allowed: the tokens of rows
+ * that the tensors do not hold are left out, the others keep their positions.  A
+ * page outside [0, n_pages), a position past the table (or past 2^31 - 257) and a
+ * negative past are holes: nothing is written there and no key is seen there. */
 typedef struct moe_kv_batch {
   const int32_t *pages; /* [n_seqs][max_pages] */
   const int32_t *start; /* [n_seqs + 1] */

@@ -339,3 +339,34 @@ def test_attend_non_finite_queries(D, G, ty):
                 if i % 2 == 0 and scale > 0:
                     got.view(8, Hkv * G, D)[t, h] = c.attend(sound, pages, start, pst, scale).view(8, Hkv * G, D)[t, h]
                     check_attend(c, sound, pages, start, pst, scale, 0, got, ty, rows=[0, 1, 2, 3, 4, 5])
+
+
+def test_captured_calls_on_a_given_stream():
+    """Calls with a stream argument inside a capture, on the capturing stream and with inputs dropped meanwhile."""
+    D, P, g = 64, 16, gen(95)
+    codes, scales = make_q4(g, D, D, 32)
+    c = m.KVCache.create(4, P, 1, D)
+    pages, start, past = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([[1, 2], [0, 3]], [0, 2, 3], [0, 17]))
+    x, w = rnd(g, 3, D), torch.ones(D, device="cuda")
+
+    def chain(x, w, s):
+        _, y = m.block_norm(x, pre_w=w, stream=s)
+        y = m.q4_matvec(y, m.Q4Matrix(codes.clone() if s is None else kept[0], scales if s is None else kept[1]), stream=s)
+        q = c.append(y, y, pages, start, past, q=y, stream=s)
+        return c.attend(q, pages, start, past, 0.1, stream=s), *c.read(pages, start, past, 3, stream=s)
+
+    kept = [codes.clone(), scales.clone()]
+    chain(x, w, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(x, w, torch.cuda.current_stream())
+    for _ in range(4):
+        x.copy_(rnd(g, 3, D))
+        want = chain(x, w, None)
+        torch.cuda.synchronize()
+        for t in c.tensors:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
