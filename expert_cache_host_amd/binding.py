@@ -26,6 +26,11 @@ class MoeError(RuntimeError):
         self.status = status
 
 
+class RouteRule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("top_k", "score", "groups", "keep_groups", "group_best", "renorm")] + \
+               [("scale", ctypes.c_float)]
+
+
 class Opts(ctypes.Structure):
     _fields_ = [("top_k", ctypes.c_int32), ("miss_mode", ctypes.c_int32),
                 ("n_shared", ctypes.c_int32), ("norm_topk", ctypes.c_int32),
@@ -68,6 +73,7 @@ def load_library():
         "moe_cache_default_opts": (None, [ctypes.POINTER(Opts)]),
         "moe_cache_create": (I32, [I32, I32, I32, I32, I32, P, ctypes.POINTER(Opts), ctypes.POINTER(P)]),
         "moe_layer_forward": (I32, [P, I32, P, I32, P, P, P, P]),
+        "moe_layer_forward_ruled": (I32, [P, I32, P, I32, P, P, ctypes.POINTER(RouteRule), P, P, P]),
         "moe_layer_forward_noalloc": (I32, [P, I32, P, I32, P, P, P, P]),
         "moe_cache_stats": (I32, [P, I32, ctypes.POINTER(Stats)]),
         "moe_cache_reset_stats": (I32, [P]),
@@ -184,8 +190,11 @@ class MoECache:
 
     # -- compute ---------------------------------------------------------------
     def forward(self, layer: int, x, router_w, router_bias=None, out=None, stream=None,
-                noalloc: bool = False):
+                noalloc: bool = False, rule=None, select_bias=None):
         """out [T, d] = layer(x) for torch float32 CUDA tensors (contiguous).
+        rule: a RoutingRule that selects the experts and their weights from the router's
+        logits in place of softmax and top-k; select_bias [n_experts] takes part in its
+        selection alone.
         noalloc: through moe_layer_forward_noalloc (the library's fixed scratch;
         `out` must then be given, since creating it would allocate)."""
         import torch
@@ -193,7 +202,11 @@ class MoECache:
             raise ValueError("noalloc calls need a preallocated out")
         if out is None:
             out = torch.empty_like(x)
-        for t in (x, router_w, out) + ((router_bias,) if router_bias is not None else ()):
+        if noalloc and rule is not None:
+            raise ValueError("noalloc calls take no rule")
+        if select_bias is not None and (rule is None or tuple(select_bias.shape) != (self.n_experts,)):
+            raise ValueError("select_bias must be [n_experts], with a rule")
+        for t in (x, router_w, out) + tuple(b for b in (router_bias, select_bias) if b is not None):
             if not (t.is_cuda and t.dtype == torch.float32 and t.is_contiguous()):
                 raise ValueError("tensors must be contiguous float32 on the GPU")
         if x.dim() != 2 or x.shape[1] != self.d_model or out.shape != x.shape:
@@ -201,6 +214,12 @@ class MoECache:
         if tuple(router_w.shape) != (self.n_experts, self.d_model):
             raise ValueError("router_w must be [n_experts, d_model]")
         s = torch.cuda.current_stream() if stream is None else stream
+        if rule is not None:
+            _check(load_library().moe_layer_forward_ruled(
+                self._h, layer, x.data_ptr(), x.shape[0], router_w.data_ptr(),
+                router_bias.data_ptr() if router_bias is not None else None, rule._cp,
+                select_bias.data_ptr() if select_bias is not None else None, out.data_ptr(), s.cuda_stream))
+            return out
         fn = load_library().moe_layer_forward_noalloc if noalloc else load_library().moe_layer_forward
         rc = fn(
             self._h, layer, x.data_ptr(), x.shape[0], router_w.data_ptr(),

@@ -21,8 +21,9 @@ HIPCC = os.path.join(ROCM, "bin", "hipcc")
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 CXX_FLAGS = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-ffp-contract=off"]
-# kernels of the decoder-layer operators, a file each
+# kernels of the decoder-layer operators, and of those between a prompt and its next token, a file each
 DECODER_OPS = ("block_norm", "q4_matvec", "kv_cache", "kv_attend")
+STEP_OPS = ("q8_rows", "q8_matmul", "route", "sample")
 
 
 def _jobs():
@@ -31,11 +32,13 @@ def _jobs():
         ([HIPCC] + HIP_FLAGS + ["-c", os.path.join(CSRC, "kernels.hip"), "-o",
                                 os.path.join(BUILD, "kernels.o")]),
         *([HIPCC] + HIP_FLAGS + ["-c", os.path.join(CSRC, n + ".hip"), "-o",
-                                 os.path.join(BUILD, n + ".o")] for n in DECODER_OPS),
+                                 os.path.join(BUILD, n + ".o")] for n in DECODER_OPS + STEP_OPS),
         (["g++"] + CXX_FLAGS + inc + ["-c", os.path.join(CSRC, "api.cpp"), "-o",
                                       os.path.join(BUILD, "api.o")]),
         (["g++"] + CXX_FLAGS + inc + ["-c", os.path.join(CSRC, "decoder_ops.cpp"), "-o",
                                       os.path.join(BUILD, "decoder_ops.o")]),
+        (["g++"] + CXX_FLAGS + inc + ["-c", os.path.join(CSRC, "step_ops.cpp"), "-o",
+                                      os.path.join(BUILD, "step_ops.o")]),
         (["g++"] + CXX_FLAGS + ["-c", os.path.join(CSRC, "planner.cpp"), "-o",
                                 os.path.join(BUILD, "planner.o")]),
         (["g++"] + CXX_FLAGS + ["-c", os.path.join(CSRC, "host_expert.cpp"), "-o",
@@ -70,8 +73,8 @@ def build(verbose: bool = False) -> str:
         msg = "\n".join(" ".join(c) + "\n" + t for c, t in failed)
         raise RuntimeError("libmoecache build failed:\n" + msg)
     objs = [os.path.join(BUILD, n) for n in ("kernels.o", "api.o", "planner.o", "host_expert.o",
-                                             "workspace.o", "host_routing.o", "decoder_ops.o",
-                                             *(n + ".o" for n in DECODER_OPS))]
+                                             "workspace.o", "host_routing.o", "decoder_ops.o", "step_ops.o",
+                                             *(n + ".o" for n in DECODER_OPS + STEP_OPS))]
     tmp = OUT + f".tmp{os.getpid()}"
     link = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs + [
         "-L" + os.path.join(ROCM, "lib"), "-lrocprofiler-sdk-roctx", "-pthread"]

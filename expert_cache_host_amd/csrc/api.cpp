@@ -33,6 +33,7 @@
 #include "kernels.hpp"
 #include "layout.hpp"
 #include "planner.hpp"
+#include "route_rule.hpp"
 #include "workspace.hpp"
 
 // The header's stream type is HIP's own (no HIP header needed there).
@@ -620,10 +621,12 @@ void run_experts(moe_cache *c, int32_t layer, int32_t T, const moe::SlotView &vi
 
 // One layer call.  noalloc: the workspace is the fixed scratch array and
 // nothing is allocated (the caller checked that the call fits); else the
-// cache's arena and page-locked buffers grow as needed.
+// cache's arena and page-locked buffers grow as needed.  rule: the routing rule
+// that selects in place of the top-k kernels and the host's own selection.
 moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
                         const float *router_w, const float *router_bias, float *out,
-                        hipStream_t st, bool noalloc = false) {
+                        hipStream_t st, bool noalloc = false, const moe_route_rule *rule = nullptr,
+                        const float *select_bias = nullptr) {
   LayerState &ly = c->layers[layer];
   const int32_t k = c->o.top_k, E = c->E, d = c->d;
   const bool host_mode = c->o.miss_mode == MOE_MISS_HOST;
@@ -673,6 +676,16 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
   const bool router_x = host_mode && dec && moe::router_decode_fits(T, d, E);
   if (host_mode && !router_x)
     HIPCHK(hipMemcpyAsync(c->h_x.p, x, (size_t)T * d * 4, hipMemcpyDeviceToHost, st));
+  // a rule's kernel writes the routing to the device and to page-locked memory;
+  // the host waits for it as for a prompt batch's
+  const auto route_by_rule = [&]() {
+    moe::RouteArgs a = moe::route_args(*rule);
+    a.z = ws.z, a.bias = select_bias, a.idx = (int32_t *)ws.idx, a.w = (float *)ws.w;
+    a.idx2 = (int32_t *)c->h_idx.p, a.w2 = (float *)c->h_w.p;
+    a.ldz = E, a.type = moe::kF32, a.T = T, a.E = E;
+    HIPCHK(moe::launch_route(a, st));
+  };
+  const bool publish = dec && !rule;  // decode calls select on the host from published logits
   if (dec) {
     // router with the digit planes of the decode GEMV, then the decode top-k
     KTime kt(c, MOE_K_ROUTER, st);
@@ -690,10 +703,12 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
     HIPCHK(moe::launch_router(x, T, d, router_w, router_bias, E, (float *)ws.z, nullptr,
                               nullptr, (uint4 *)ws.xq, (float *)ws.xs, st,
                               router_x ? (float *)c->h_x.p : nullptr,
-                              (unsigned long long *)c->h_z, c->z_seq));
+                              publish ? (unsigned long long *)c->h_z : nullptr, c->z_seq));
     kt.end(4.0 * ((double)E * d + (double)T * d * 2 + (double)T * E + (router_bias ? E : 0)));
+    if (rule) route_by_rule();
     KTime kt2(c, MOE_K_TOPK, st);
-    HIPCHK(moe::launch_topk_decode((const float *)ws.z, T, E, a, st));
+    HIPCHK(rule ? moe::launch_decode_buckets(T, a, st)
+                : moe::launch_topk_decode((const float *)ws.z, T, E, a, st));
     kt2.end(4.0 * ((double)T * E + 4.0 * T * k));
   } else {
     {
@@ -704,12 +719,16 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
                                 (float *)ws.xs, st));
       kt.end(4.0 * ((double)E * d + (double)T * d * 2 + (double)T * E + (router_bias ? E : 0)));
     }
-    KTime kt(c, MOE_K_TOPK, st);
-    HIPCHK(moe::launch_topk((const float *)ws.z, T, E, k, c->o.norm_topk, (int32_t *)ws.idx,
-                            (float *)ws.w, (int32_t *)c->h_idx.p, (float *)c->h_w.p, st));
-    kt.end(4.0 * ((double)T * E + 4.0 * T * k));
+    if (rule) {
+      route_by_rule();
+    } else {
+      KTime kt(c, MOE_K_TOPK, st);
+      HIPCHK(moe::launch_topk((const float *)ws.z, T, E, k, c->o.norm_topk, (int32_t *)ws.idx,
+                              (float *)ws.w, (int32_t *)c->h_idx.p, (float *)c->h_w.p, st));
+      kt.end(4.0 * ((double)T * E + 4.0 * T * k));
+    }
   }
-  if (!dec) HIPCHK(hipEventRecord(c->ev_idx, st));
+  if (!publish) HIPCHK(hipEventRecord(c->ev_idx, st));
   if (c->o.keep_debug) {
     ly.dbg_z.ensure((size_t)T * E * 4);
     HIPCHK(hipMemcpyAsync(ly.dbg_z.p, ws.z, (size_t)T * E * 4, hipMemcpyDeviceToDevice, st));
@@ -728,7 +747,7 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
   }
   {
     TraceRange tr("moe.wait_routing");
-    if (dec)
+    if (publish)
       wait_routing(c, st, T);
     else
       HIPCHK(hipEventSynchronize(c->ev_idx));
@@ -1095,6 +1114,25 @@ moe_status moe_layer_forward(moe_cache *c, int32_t layer, const float *x, int32_
   return guarded(c, [&]() {
     TraceRange tr("moe.layer_forward");
     return forward_impl(c, layer, x, n_tokens, router_w, router_bias, out, stream);
+  });
+}
+
+moe_status moe_layer_forward_ruled(moe_cache *c, int32_t layer, const float *x, int32_t n_tokens,
+                                   const float *router_w, const float *router_bias,
+                                   const moe_route_rule *rule, const float *select_bias, float *out,
+                                   moe_stream_t stream) {
+  g_err.clear();
+  if (!c) return fail(MOE_EINVAL, "cache is NULL");
+  if (layer < 0 || layer >= c->L) return fail(MOE_EINVAL, "layer out of range");
+  if (n_tokens < 1) return fail(MOE_EINVAL, "n_tokens must be >= 1");
+  if (n_tokens > (1 << 20)) return fail(MOE_EINVAL, "n_tokens too large");
+  if (!x || !router_w || !out) return fail(MOE_EINVAL, "x, router_w and out must be non-NULL");
+  if (const char *f = moe::rule_fault(rule, c->E)) return fail(MOE_EINVAL, f);
+  if (rule->top_k != c->o.top_k) return fail(MOE_EINVAL, "the rule's top_k is not the cache's");
+  return guarded(c, [&]() {
+    TraceRange tr("moe.layer_forward");
+    return forward_impl(c, layer, x, n_tokens, router_w, router_bias, out, stream, false, rule,
+                        select_bias);
   });
 }
 

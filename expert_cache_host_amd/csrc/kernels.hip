@@ -549,30 +549,10 @@ __global__ __launch_bounds__(64) void topk_kernel(const float *__restrict__ z, i
   }
 }
 
-// Decode calls (T <= 4 tokens, T*k + shared pairs <= 64): one workgroup, wave t
-// selects token t's experts; then wave 0 maps every pair to its slot through
-// `view` (shared pairs to shared_slot) and lists the buckets (pairs grouped by
-// slot, a bucket per slot in order of its first pair, pairs ascending).  The
-// host makes the same selection from the published logits, so nothing here
-// goes to host memory.  Every thread of the workgroup (at least 64 * T) calls it.
-__device__ void topk_decode_block(const float *z, int T, int E, const DecodeTopk &a) {
-  __shared__ int sidx[kDecodeMaxPairs];
-  const int t = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int k = a.k;
-  if (t < T) {
-    int my_e;
-    float my_w;
-    topk_token(z, t, E, k, a.norm_topk, my_e, my_w);
-    if (lane < k) {
-      const int o = t * k + lane;
-      a.idx[o] = my_e;
-      a.w[o] = my_w;
-      sidx[o] = my_e;
-    }
-  }
-  __syncthreads();
-  if (t != 0) return;
-  const int Pr = T * k;
+// Wave 0's part: the pairs' experts in sidx (shared memory).
+__device__ void decode_buckets(const int *sidx, int T, const DecodeTopk &a) {
+  const int lane = threadIdx.x & 63;
+  const int Pr = T * a.k;
   const int P = Pr + (a.shared_slot >= 0 ? T : 0);
   int s = -1;
   if (lane < P) s = lane < Pr ? (int)a.view.slot[sidx[lane]] : a.shared_slot;
@@ -604,9 +584,42 @@ __device__ void topk_decode_block(const float *z, int T, int E, const DecodeTopk
   if (lane == 0) a.buckets[0] = nbk;
 }
 
+// Decode calls (T <= 4 tokens, T*k + shared pairs <= 64): one workgroup, wave t
+// selects token t's experts; then wave 0 maps every pair to its slot through
+// `view` (shared pairs to shared_slot) and lists the buckets (pairs grouped by
+// slot, a bucket per slot in order of its first pair, pairs ascending).  The
+// host makes the same selection from the published logits, so nothing here
+// goes to host memory.  Every thread of the workgroup (at least 64 * T) calls it.
+__device__ void topk_decode_block(const float *z, int T, int E, const DecodeTopk &a) {
+  __shared__ int sidx[kDecodeMaxPairs];
+  const int t = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int k = a.k;
+  if (t < T) {
+    int my_e;
+    float my_w;
+    topk_token(z, t, E, k, a.norm_topk, my_e, my_w);
+    if (lane < k) {
+      const int o = t * k + lane;
+      a.idx[o] = my_e;
+      a.w[o] = my_w;
+      sidx[o] = my_e;
+    }
+  }
+  __syncthreads();
+  if (t == 0) decode_buckets(sidx, T, a);
+}
+
 __global__ __launch_bounds__(256) void topk_decode_kernel(const float *z, int T, int E,
                                                           DecodeTopk a) {
   topk_decode_block(z, T, E, a);
+}
+
+// The buckets of experts selected before (a.idx, by a routing rule's kernel).
+__global__ __launch_bounds__(64) void decode_buckets_kernel(int T, DecodeTopk a) {
+  __shared__ int sidx[kDecodeMaxPairs];
+  if ((int)threadIdx.x < T * a.k) sidx[threadIdx.x] = a.idx[threadIdx.x];
+  __syncthreads();
+  decode_buckets(sidx, T, a);
 }
 
 hipError_t launch_topk(const float *z, int T, int E, int k, int norm_topk, int32_t *idx, float *w,
@@ -624,6 +637,12 @@ static bool decode_args_ok(int T, const DecodeTopk &a) {
 hipError_t launch_topk_decode(const float *z, int T, int E, const DecodeTopk &a, hipStream_t s) {
   if (!decode_args_ok(T, a)) return hipErrorInvalidValue;
   launch_k(topk_decode_kernel, dim3(1), dim3(64 * T), 0, s, z, T, E, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_decode_buckets(int T, const DecodeTopk &a, hipStream_t s) {
+  if (!decode_args_ok(T, a)) return hipErrorInvalidValue;
+  launch_k(decode_buckets_kernel, dim3(1), dim3(64), 0, s, T, a);
   return hipGetLastError();
 }
 

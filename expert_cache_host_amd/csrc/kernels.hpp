@@ -67,6 +67,8 @@ struct DecodeTopk {
   int32_t *buckets, *pair_slot;
 };
 hipError_t launch_topk_decode(const float *z, int T, int E, const DecodeTopk &a, hipStream_t s);
+// The same tables for experts selected before (idx holds them; idx and w stay).
+hipError_t launch_decode_buckets(int T, const DecodeTopk &a, hipStream_t s);
 
 // Expert -> slot remap of the routed pairs (plus one shared pair per token when
 // shared_slot >= 0) and stable bucketing per slot, for batches beyond the

@@ -577,6 +577,143 @@ moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, i
                          int32_t window, void *out, int64_t out_stride, void *workspace,
                          int64_t workspace_bytes, moe_stream_t stream);
 
+/* ---- operators between a prompt and its next token ----
+ *
+ * Products with 8-bit matrices for prompts and batches, the routing rules that the
+ * MoE layer's own softmax and top-k do not cover, and the choice of the next token.
+ * They keep to what is said of the decoder layer's operators above: no state, no
+ * allocation, no waiting; capturable; strides in elements. */
+
+#define MOE_Q8_MAX_COLS 131072
+#define MOE_Q8_MAX_ROWS (1 << 24)
+#define MOE_Q8_MAX_TOKENS (1 << 20)
+#define MOE_ROUTE_MAX_TOKENS (1 << 24)
+#define MOE_SAMPLE_MAX_ROWS 65535
+#define MOE_SAMPLE_MAX_VOCAB (1 << 20)
+
+/* Rows held in 8 bits are padded with zero codes to a multiple of this. */
+#define MOE_Q8_PAD 128
+
+/* moe_q8_rows -- rows in 8-bit integers with a scale each:
+ *
+ *     scales[i] = max_c |x[i][c]| / 127   (float32)
+ *     codes[i][c] = rint(x[i][c] / scales[i]), halves to the even integer, decided exactly
+ *
+ *   x       [n_rows][cols] of `type`
+ *   codes   int8, 16-byte aligned; a row holds cols codes and zeros up to the next
+ *           multiple of MOE_Q8_PAD; codes_stride is a multiple of 16 and holds such a row
+ *   scales  float32 [n_rows]
+ *
+ * A row of zeros (or of numbers so small that its scale is 0) has scale 0 and codes 0;
+ * a row with an infinity or a NaN has scale NaN and codes 0, which makes the results of
+ * its products NaN.  For tokens and for a matrix's rows (its output channels) alike. */
+moe_status moe_q8_rows(const void *x, int32_t type, int64_t x_stride, int32_t n_rows, int32_t cols, void *codes,
+                       int64_t codes_stride, float *scales, moe_stream_t stream);
+
+/* moe_q8_matmul -- out[t][r] = x_scales[t] w_scales[r] sum_c x[t][c] w[r][c].
+ *
+ *   x       int8 [n_tokens][cols], 16-byte aligned, rows zeroed up to a multiple of
+ *           MOE_Q8_PAD as moe_q8_rows writes them; x_stride a multiple of 16
+ *   w       int8 [rows][cols], 16-byte aligned; w_stride a multiple of 16 that holds a
+ *           row; the bytes of a row from cols to the next multiple of 16 are read, with
+ *           no effect
+ *   out     [n_tokens][rows] of `type`
+ *
+ * The sum is an exact 32-bit integer (codes of x in [-127, 127]); it is rounded to
+ * float32, multiplied by x_scales[t], then by w_scales[r], and rounded to `type`. */
+moe_status moe_q8_matmul(const void *x, int64_t x_stride, const float *x_scales, int32_t n_tokens, const void *w,
+                         int64_t w_stride, const float *w_scales, int32_t rows, int32_t cols, void *out, int32_t type,
+                         int64_t out_stride, moe_stream_t stream);
+
+/* moe_q8_linear -- both: x [n_tokens][cols] of `type` in 8 bits as moe_q8_rows gives
+ * it, then moe_q8_matmul into out of `out_type`; the same results.
+ *   workspace  device memory of moe_q8_linear_workspace bytes, 16-byte aligned, for this
+ *              call alone until its work is done */
+int64_t moe_q8_linear_workspace(int32_t n_tokens, int32_t rows, int32_t cols);
+moe_status moe_q8_linear(const void *x, int32_t type, int64_t x_stride, int32_t n_tokens, const void *w,
+                         int64_t w_stride, const float *w_scales, int32_t rows, int32_t cols, void *out,
+                         int32_t out_type, int64_t out_stride, void *workspace, int64_t workspace_bytes,
+                         moe_stream_t stream);
+
+/* A rule of routing.  Expert e of logit z has the score
+ *     s_e = exp(z_e) / sum_j exp(z_j)   (MOE_SCORE_SOFTMAX)
+ *     s_e = 1 / (1 + exp(-z_e))         (MOE_SCORE_SIGMOID)
+ * and the selection value c_e = s_e + bias[e]; without a bias the experts' order is
+ * that of their logits.  Groups of n_experts / groups consecutive experts are worth
+ * their largest c (group_best 1) or the sum of their two largest (group_best 2; without
+ * a bias the sum of their two largest scores); the keep_groups best groups are kept, of
+ * their experts the top_k best are selected, in falling order; equal values go to the
+ * lower group or expert.  Expert j's weight is scale * s_j, with renorm scale * s_j over
+ * the sum of the selected scores (0 where that is 0).
+ * Scores and selection values are binary64, weights rounded to float32 at the end.
+ * A logit of minus infinity or NaN, or a bias of either, excludes an expert: it is
+ * selected only where fewer than top_k others are left in the kept groups, the lowest
+ * ids first, with weight 0; a group with fewer than group_best others comes after all
+ * that have them.  A logit of plus infinity counts as the largest float32. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct moe_route_rule {
+  int32_t top_k;       /* 1..min(64, n_experts) */
+  int32_t score;       /* MOE_SCORE_* */
+  int32_t groups;      /* 1..64, divides n_experts */
+  int32_t keep_groups; /* 1..groups */
+  int32_t group_best;  /* 1 or 2 */
+  int32_t renorm;      /* 0 or 1 */
+  float scale;         /* finite */
+} moe_route_rule;
+
+/* moe_route -- the experts of each token and their weights.
+ *   logits  [n_tokens][n_experts] of `type`; n_experts <= MOE_MAX_EXPERTS
+ *   bias    float32 [n_experts] or NULL; takes part in the selection alone
+ *   idx, w  int32 and float32 [n_tokens][top_k] */
+moe_status moe_route(const void *logits, int32_t type, int64_t stride, const float *bias, int32_t n_tokens,
+                     int32_t n_experts, const moe_route_rule *rule, int32_t *idx, float *w, moe_stream_t stream);
+
+/* moe_layer_forward_ruled -- moe_layer_forward with the experts and gating weights that
+ * `rule` selects from the router's logits (router_bias is part of the logits, select_bias,
+ * device float32 [n_experts] or NULL, of the selection alone).  rule->top_k must be the
+ * cache's top_k; the cache's norm_topk is not looked at.  Everything else is as there. */
+moe_status moe_layer_forward_ruled(moe_cache *c, int32_t layer, const float *x, int32_t n_tokens,
+                                   const float *router_w, const float *router_bias, const moe_route_rule *rule,
+                                   const float *select_bias, float *out, moe_stream_t stream);
+
+/* Settings of moe_sample: each either one for the call, or, where the pointer is given,
+ * one per row (device memory). */
+typedef struct moe_sample_opts {
+  double temperature;        /* >= 0, finite; 0 takes the likeliest token */
+  double top_p;              /* in [0, 1]; 1 keeps all */
+  double min_p;              /* in [0, 1]; 0 keeps all */
+  int32_t top_k;             /* 0 keeps all */
+  const float *temperatures; /* [n_rows]; 0, a negative number or NaN takes the likeliest */
+  const float *top_ps;       /* [n_rows]; 1 or more, or NaN, keeps all; below 0 counts as 0 */
+  const float *min_ps;       /* [n_rows]; 0 or less, or NaN, keeps all; above 1 counts as 1 */
+  const int32_t *top_ks;     /* [n_rows]; 0 or less keeps all */
+} moe_sample_opts;
+
+/* moe_sample -- the next token of each row of logits, from given random numbers:
+ *
+ *   Tokens stand in the order of falling logits, equal ones by their ids, with weights
+ *   p_i = exp((z_i - z_0) / temperature).  Kept are the first n = min(n_k, n_p, n_m): n_k =
+ *   top_k; n_p the least number whose weights sum to top_p of the first n_k's sum; n_m
+ *   the number with p_i >= min_p.  token is the first whose running sum passes u times
+ *   the kept sum, prob its weight over the kept sum (1 at temperature 0).
+ *
+ *   logits  [n_rows][vocab] of `type`; a NaN counts as minus infinity, which bans a token;
+ *           plus infinity as the largest float32
+ *   u       float32 [n_rows] in [0, 1) (above counts as the last kept, NaN or below as 0)
+ *   token   int32 [n_rows]; -1 (prob 0) where every token is banned
+ *   prob    float32 [n_rows] or NULL
+ *   workspace  device memory of moe_sample_workspace bytes, 16-byte aligned, for this
+ *           call alone until its work is done
+ *
+ * Weights are binary64, rounded to multiples of 2^-42, and summed exactly: results do
+ * not depend on the order of additions.  Tokens 29.8 temperatures below the first and
+ * further have weight 0. */
+int64_t moe_sample_workspace(int32_t n_rows, int32_t vocab);
+moe_status moe_sample(const void *logits, int32_t type, int64_t stride, int32_t n_rows, int32_t vocab, const float *u,
+                      const moe_sample_opts *opts, int32_t *token, float *prob, void *workspace,
+                      int64_t workspace_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
