@@ -22,10 +22,58 @@ __device__ __forceinline__ float scaled(int sum, float sx, float sw) {
 using i32x16 = __attribute__((ext_vector_type(16))) int;
 
 // Rows of codes as a buffer that starts at row r0: what lies behind the last row reads 0.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const int8_t *p, long long ld, int r0, int rows, int most,
-                                                            int bytes) {
-  const int n = min(rows - r0, most);
-  return __builtin_amdgcn_make_buffer_rsrc((void *)(p + (long long)r0 * ld), 0, (n - 1) * (int)ld + bytes, 0x00027000);
+__device__ __forceinline__ i32x4 rows_from(const int8_t *p, long long ld, int r0, int rows, int most, int bytes) {
+  const uint64_t base = (uint64_t)(p + (long long)r0 * ld);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff);
+  r[2] = __builtin_amdgcn_readfirstlane((min(rows - r0, most) - 1) * (int)ld + bytes);
+  r[3] = 0x00027000;
+  return r;
+}
+
+// 16 bytes a lane from the buffer's byte lane_at + at into LDS, the wave's kilobyte
+// at place `l`.  Written as assembly (it returns nothing in registers) because the
+// compiler waits for every such load before any read of LDS (nothing else here uses
+// m0); wait_loads says which
+// of them a wave waits for.
+__device__ __forceinline__ void load_lds(i32x4 rows, uint32_t l, int lane_at, int at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(l), "v"(lane_at), "s"(rows), "s"(at)
+               : "memory");
+}
+
+// The first n of eight elements of a row.
+__device__ __forceinline__ void store8(void *p, int type, long long i, float4 x, float4 y, int n) {
+  if (n >= 8) {
+    if (type == kF32) {
+      store4(p, type, i, x), store4(p, type, i + 4, y);
+      return;
+    }
+    uint32_t b[4];
+    store4(b, type, 0, x), store4(b, type, 4, y);
+    __builtin_memcpy((uint16_t *)p + i, b, 16);
+  } else if (n >= 4) {
+    store4(p, type, i, x);
+    if (n > 4) store_few(p, type, i + 4, y, n - 4);
+  } else {
+    store_few(p, type, i, x, n);
+  }
+}
+
+// This wave's loads into LDS have landed but for the last N; then the workgroup's.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Every wave's reads of LDS so far have returned.
+__device__ __forceinline__ void reads_done() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // A tile of RT rows of w by TT tokens, WR x WT waves.
@@ -44,69 +92,113 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   // groups of 8 row tiles, the token tiles of a group in turn
   const int group = at / (8 * t_tiles), in = at % (8 * t_tiles), high = min(8, r_tiles - 8 * group);
   const int r0 = (8 * group + in % high) * RT, t0 = in / high * TT;
+  __shared__ __attribute__((aligned(16))) float sws[RT], sxs[TT];
+  for (int i = threadIdx.x; i < RT; i += 64 * NW) sws[i] = r0 + i < a.rows ? a.w_scales[r0 + i] : 0.f;
+  for (int i = threadIdx.x; i < TT; i += 64 * NW) sxs[i] = t0 + i < a.T ? a.x_scales[t0 + i] : 0.f;
   const auto wr = rows_from(a.w, a.ldw, r0, a.rows, RT, (a.cols + 15) & ~15);
   const auto xr = rows_from(a.x, a.ldx, t0, a.T, TT, (a.cols + 127) & ~127);
-  // a wave's load takes 8 rows of 128 bytes; the 16-byte pieces of row r lie at place (piece ^ r % 8)
-  const int piece = ((lane & 7) ^ (lane >> 3)) * 16, row = (lane >> 3) + 8 * wave;
+  // a wave's load takes 8 rows of 128 bytes; the 16-byte pieces of row r lie at place
+  // piece ^ r / 2 % 8: sixteen lanes that read the same piece of sixteen rows then
+  // touch each of the 64 banks once (with r % 8 half of the LDS time was conflicts)
+  static_assert(NW % 2 == 0, "a wave's loads all start at rows of the same r / 8 % 2");
+  const int piece = ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16, row = (lane >> 3) + 8 * wave;
   const int wo = row * (int)a.ldw + piece, xo = row * (int)a.ldx + piece;
   const int ldw8 = 8 * NW * (int)a.ldw, ldx8 = 8 * NW * (int)a.ldx;
-  using lds_ptr = __attribute__((address_space(3))) void *;
-  const auto load = [&](int8_t *l, int k) {
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds + wave * 1024;
+  const auto load = [&](int to, int k) {
 #pragma unroll
-    for (int j = 0; j < LA; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (lds_ptr)(l + (j * NW + wave) * 1024), 16, wo, j * ldw8 + k, 0, 0);
+    for (int j = 0; j < LA; ++j) load_lds(wr, lds_at + to + j * NW * 1024, wo, j * ldw8 + k);
 #pragma unroll
-    for (int j = 0; j < LB; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_ptr)(l + RT * 128 + (j * NW + wave) * 1024), 16, xo,
-                                               j * ldx8 + k, 0, 0);
+    for (int j = 0; j < LB; ++j) load_lds(xr, lds_at + to + RT * 128 + j * NW * 1024, xo, j * ldx8 + k);
   };
   const int wi = wave % WR, ti = wave / WR;
   const int ra = (wi * (RT / WR) + (lane & 31)) * 128, rb = (RT + ti * (TT / WT) + (lane & 31)) * 128;
   i32x16 acc[RI][TI] = {};
-  const auto multiply = [&](const int8_t *l) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int c = ((2 * s + (lane >> 5)) ^ (lane & 7)) * 16;
-      i32x4 wf[RI], xf[TI];
-#pragma unroll
-      for (int j = 0; j < TI; ++j) xf[j] = *(const i32x4 *)(l + rb + c + j * 4096);
-#pragma unroll
-      for (int i = 0; i < RI; ++i) wf[i] = *(const i32x4 *)(l + ra + c + i * 4096);
-#pragma unroll
-      for (int i = 0; i < RI; ++i)
-#pragma unroll
-        for (int j = 0; j < TI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], xf[j], acc[i][j], 0, 0, 0);
-    }
+  struct Frag {
+    i32x4 w[RI], x[TI];
   };
-  const int end = (a.cols + 127) & ~127;
-  load(lds, 0);
-  int cur = 0;
-  for (int k = 128; k < end; k += 128, cur = kStep - cur) {
-    __syncthreads();
-    load(lds + kStep - cur, k);
-    multiply(lds + cur);
-  }
-  __syncthreads();
-  multiply(lds + cur);
+  const auto read = [&](const int8_t *l, int s, Frag &f) {
+    const int c = ((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16;
 #pragma unroll
-  for (int j = 0; j < TI; ++j) {
-    const int t = t0 + ti * (TT / WT) + j * 32 + (lane & 31);
-    if (t >= a.T) continue;
-    const float sx = a.x_scales[t];
+    for (int j = 0; j < TI; ++j) f.x[j] = *(const i32x4 *)(l + rb + c + j * 4096);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) f.w[i] = *(const i32x4 *)(l + ra + c + i * 4096);
+  };
+  const auto multiply = [&](const Frag &f) {
 #pragma unroll
     for (int i = 0; i < RI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = r0 + wi * (RT / WR) + i * 32 + 8 * q + 4 * (lane >> 5);
-        const long long o = t * a.ldo + r;
-        float v[4];
+      for (int j = 0; j < TI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
+  };
+  // `reads` reads of fragments to a product, the rest of the products after them
+  const auto mix = [&](auto reads) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i][j][4 * q + e], sx, r + e < a.rows ? a.w_scales[r + e] : 0.f);
-        if (r + 4 <= a.rows)
-          store4(a.out, TY, o, make_float4(v[0], v[1], v[2], v[3]));
-        else if (r < a.rows)
-          store_few(a.out, TY, o, make_float4(v[0], v[1], v[2], v[3]), a.rows - r);
+    for (int i = 0; i < RI * TI; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < RI + TI) __builtin_amdgcn_sched_group_barrier(0x100, decltype(reads)::value, 0);
+    }
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  Frag f0, f1, f2, f3;
+  int cur = 0;
+  const auto first_half = [&]() {
+    read(lds + cur, 1, f1), multiply(f0), mix(One{});
+    read(lds + cur, 2, f2), read(lds + cur, 3, f3), multiply(f1), mix(Two{});
+  };
+  const auto turn = [&]() {
+    read(lds + kStep - cur, 0, f0), multiply(f3), mix(One{});
+    cur = kStep - cur;
+  };
+  // at least two steps of 128 columns (launch_type's rule)
+  const int steps = (a.cols + 127) / 128;
+  load(0, 0);
+  load(kStep, 128);
+  wait_loads<LA + LB>();
+  read(lds, 0, f0);
+  for (int i = 2; i < steps; ++i) {
+    first_half();
+    // every wave has this step's fragments: its place takes the step after the next
+    reads_done();
+    load(cur, 128 * i);
+    multiply(f2);
+    wait_loads<LA + LB>();
+    turn();
+  }
+  first_half();
+  multiply(f2);
+  wait_loads<0>();
+  turn();
+  first_half();
+  multiply(f2);
+  multiply(f3);
+  // a lane holds, of token lane % 32, four rows in eight; the wave's halves swap, so
+  // that it has eight in sixteen
+  const int half = lane >> 5;
+#pragma unroll
+  for (int j = 0; j < TI; ++j) {
+    const int tl = ti * (TT / WT) + j * 32 + (lane & 31), t = t0 + tl;
+    const float sx = sxs[tl];
+#pragma unroll
+    for (int i = 0; i < RI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        const int rl = wi * (RT / WR) + i * 32 + 8 * q;
+        i32x4 lo, hi;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto p = __builtin_amdgcn_permlane32_swap(acc[i][j][4 * q + e], acc[i][j][4 * q + 4 + e], false, false);
+          lo[e] = (int)p[0], hi[e] = (int)p[1];
+        }
+        const int rr = rl + 8 * half, r = r0 + rr;
+        if (t >= a.T || r >= a.rows) continue;
+        const float4 s0 = *(const float4 *)(sws + rr), s1 = *(const float4 *)(sws + rr + 4);
+        const float4 v0 = make_float4(scaled(lo[0], sx, s0.x), scaled(lo[1], sx, s0.y), scaled(lo[2], sx, s0.z),
+                                      scaled(lo[3], sx, s0.w));
+        const float4 v1 = make_float4(scaled(hi[0], sx, s1.x), scaled(hi[1], sx, s1.y), scaled(hi[2], sx, s1.z),
+                                      scaled(hi[3], sx, s1.w));
+        store8(a.out, TY, t * a.ldo + r, v0, v1, a.rows - r);
       }
   }
 }
@@ -136,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void q8_matmul_kernel(Q8MatmulArgs a) {
 
 template <int TY>
 hipError_t launch_type(const Q8MatmulArgs &a, hipStream_t s) {
-  if (a.T > 64) {
+  if (a.T > 64 && a.cols > 128) {
     const int r = (a.rows + 255) / 256, t = (a.T + 255) / 256;
     return launch(q8_tile_kernel<TY, 256, 256, 2, 4>, dim3(r * t), dim3(512), s, a, r, t);
   }
