@@ -20,6 +20,16 @@ hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, st
   return e;
 }
 
+// The same with `lds` bytes of the workgroup's memory given at the launch.
+template <class... P>
+hipError_t launch_lds(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t s,
+                      std::common_type_t<P>... args) {
+  void *p[] = {(void *)&args...};
+  const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, p, lds, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
 __device__ __forceinline__ float bf16_to_f32(uint32_t b) {
   return __builtin_bit_cast(float, b << 16);
 }

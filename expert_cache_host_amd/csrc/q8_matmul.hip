@@ -1,5 +1,20 @@
-// out[t][r] = sx[t] sw[r] sum_c x[t][c] w[r][c] over 8-bit integers.
-#include "device_types.hpp"
+// out[t][r] = sx[t] sw[r] sum_c x[t][c] w[r][c] over 8-bit integers, the sums in 32
+// bits on the matrix cores (v_mfma_i32_32x32x32_i8; 16x16x64 for few tokens).
+//
+// Many tokens (q8_tile_kernel): a workgroup takes a tile of rows by tokens, 128
+// columns a step, both operands loaded straight into LDS, S steps under way.  Large
+// products are bound by the card's power (the clock falls to about 1.5 GHz while the
+// matrix cores are busy): 4096 x 6144 x 16384 in 345 us, 2390 TOP/s (a library's
+// product of these sizes without the scales: 395 us); 8192^3 in 440 us, 2500 TOP/s.  Small ones are bound
+// by what a CU can load, about 50 GB/s next to the reads: 512 x 6144 x 10240 in 43 us.
+// What mattered: fragments read a step ahead of their products and loads a step and a
+// quarter ahead of their fragments (8192^3: 567 -> 472 us); pieces laid out so that
+// reads meet no bank conflict; a step's loads spread over it, since LDS takes their
+// writes between the reads (491 -> 441 us, and 84 -> 67 us for 80 tiles of 6144
+// columns, one each on 80 CUs).
+// Few tokens: memory.  16 x 6144 x 10240 in 15.6 us (4.1 TB/s of weights), one token
+// by 2816 x 8192 in 6.9.
+#include "q8_code.hpp"
 #include "step_ops.hpp"
 
 namespace moe {
@@ -7,8 +22,6 @@ namespace moe {
 namespace {
 
 using i32x4 = __attribute__((ext_vector_type(4))) int;
-
-constexpr int kThreads = 256;
 
 // (sum sx) sw, both products rounded to float32.  The value is settled there:
 // a conversion to binary16 taken together with the product would round once where
@@ -77,13 +90,13 @@ __device__ __forceinline__ void reads_done() {
 }
 
 // A tile of RT rows of w by TT tokens, WR x WT waves.
-template <int TY, int RT, int TT, int WR, int WT>
+template <int TY, int RT, int TT, int WR, int WT, int S>
 __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, int r_tiles, int t_tiles) {
   constexpr int NW = WR * WT, RI = RT / WR / 32, TI = TT / WT / 32;
   constexpr int LA = RT / 8 / NW, LB = TT / 8 / NW;
   static_assert(RT % (8 * NW) == 0 && TT % (8 * NW) == 0, "whole loads");
   constexpr int kStep = (RT + TT) * 128;
-  __shared__ __attribute__((aligned(1024))) int8_t lds[2 * kStep];
+  __shared__ __attribute__((aligned(1024))) int8_t lds[S * kStep];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // workgroups are dealt to the 8 dies in turn: each die takes a run of tiles
   const int n = r_tiles * t_tiles, id = blockIdx.x;
@@ -105,11 +118,15 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   const int wo = row * (int)a.ldw + piece, xo = row * (int)a.ldx + piece;
   const int ldw8 = 8 * NW * (int)a.ldw, ldx8 = 8 * NW * (int)a.ldx;
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds + wave * 1024;
+  const auto load_w = [&](int j, int to, int k) { load_lds(wr, lds_at + to + j * NW * 1024, wo, j * ldw8 + k); };
+  const auto load_x = [&](int j, int to, int k) {
+    load_lds(xr, lds_at + to + RT * 128 + j * NW * 1024, xo, j * ldx8 + k);
+  };
   const auto load = [&](int to, int k) {
 #pragma unroll
-    for (int j = 0; j < LA; ++j) load_lds(wr, lds_at + to + j * NW * 1024, wo, j * ldw8 + k);
+    for (int j = 0; j < LA; ++j) load_w(j, to, k);
 #pragma unroll
-    for (int j = 0; j < LB; ++j) load_lds(xr, lds_at + to + RT * 128 + j * NW * 1024, xo, j * ldx8 + k);
+    for (int j = 0; j < LB; ++j) load_x(j, to, k);
   };
   const int wi = wave % WR, ti = wave / WR;
   const int ra = (wi * (RT / WR) + (lane & 31)) * 128, rb = (RT + ti * (TT / WT) + (lane & 31)) * 128;
@@ -117,62 +134,101 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   struct Frag {
     i32x4 w[RI], x[TI];
   };
-  const auto read = [&](const int8_t *l, int s, Frag &f) {
+  // fragment n of step s: the tokens' first, then the rows'
+  const auto read1 = [&](const int8_t *l, int s, Frag &f, int n) {
     const int c = ((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) * 16;
-#pragma unroll
-    for (int j = 0; j < TI; ++j) f.x[j] = *(const i32x4 *)(l + rb + c + j * 4096);
-#pragma unroll
-    for (int i = 0; i < RI; ++i) f.w[i] = *(const i32x4 *)(l + ra + c + i * 4096);
+    if (n < TI)
+      f.x[n] = *(const i32x4 *)(l + rb + c + n * 4096);
+    else
+      f.w[n - TI] = *(const i32x4 *)(l + ra + c + (n - TI) * 4096);
   };
-  const auto multiply = [&](const Frag &f) {
+  constexpr int kFrags = RI + TI;
+  // products of one step, with what `between(i)` issues after those of row block i
+  const auto multiply = [&](const Frag &f, auto between) {
 #pragma unroll
-    for (int i = 0; i < RI; ++i)
+    for (int i = 0; i < RI; ++i) {
+      between(i);
 #pragma unroll
       for (int j = 0; j < TI; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
-  };
-  // `reads` reads of fragments to a product, the rest of the products after them
-  const auto mix = [&](auto reads) {
-#pragma unroll
-    for (int i = 0; i < RI * TI; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (i < RI + TI) __builtin_amdgcn_sched_group_barrier(0x100, decltype(reads)::value, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  using One = std::integral_constant<int, 1>;
-  using Two = std::integral_constant<int, 2>;
   Frag f0, f1, f2, f3;
   int cur = 0;
-  const auto first_half = [&]() {
-    read(lds + cur, 1, f1), multiply(f0), mix(One{});
-    read(lds + cur, 2, f2), read(lds + cur, 3, f3), multiply(f1), mix(Two{});
+  // S steps of 128 columns are under way; those past the last column are loaded (out
+  // of the rows behind, or as 0) and not used
+  const int steps = (a.cols + 127) / 128;
+#pragma unroll
+  for (int i = 0; i < S; ++i) load(i * kStep, 128 * i);
+  wait_loads<(S - 1) * (LA + LB)>();
+#pragma unroll
+  for (int n = 0; n < kFrags; ++n) read1(lds, 0, f0, n);
+  const auto first_half = [&](auto loads) {
+    multiply(f0, [&](int i) {
+#pragma unroll
+      for (int n = i * 2 * kFrags / RI; n < (i + 1) * 2 * kFrags / RI; ++n)
+        n < kFrags ? read1(lds + cur, 1, f1, n) : read1(lds + cur, 2, f2, n - kFrags);
+      loads(i);
+    });
+    multiply(f1, [&](int i) {
+#pragma unroll
+      for (int n = i * 2 * kFrags / RI; n < (i + 1) * 2 * kFrags / RI && n < kFrags; ++n) read1(lds + cur, 3, f3, n);
+    });
   };
   const auto turn = [&]() {
-    read(lds + kStep - cur, 0, f0), multiply(f3), mix(One{});
-    cur = kStep - cur;
+    cur = cur == (S - 1) * kStep ? 0 : cur + kStep;
+    multiply(f3, [&](int i) {
+#pragma unroll
+      for (int n = i * kFrags / RI; n < (i + 1) * kFrags / RI; ++n) read1(lds + cur, 0, f0, n);
+    });
   };
-  // at least two steps of 128 columns (launch_type's rule)
-  const int steps = (a.cols + 127) / 128;
-  load(0, 0);
-  load(kStep, 128);
-  wait_loads<LA + LB>();
-  read(lds, 0, f0);
-  for (int i = 2; i < steps; ++i) {
-    first_half();
-    // every wave has this step's fragments: its place takes the step after the next
+  const auto nothing = [](int) {};
+  // the loads of a step are spread: the rows' pieces go out in its second half, the
+  // tokens' in the first half of the next
+  int i = 0, back = 0, k = 128 * S;
+  const auto tokens = [&](int i) {
+#pragma unroll
+    for (int j = i * LB / RI; j < (i + 1) * LB / RI; ++j) load_x(j, back, k);
+  };
+  if (S < steps) {
+    first_half(nothing);
     reads_done();
-    load(cur, 128 * i);
-    multiply(f2);
-    wait_loads<LA + LB>();
+    multiply(f2, [&](int i) {
+#pragma unroll
+      for (int j = i * LA / RI; j < (i + 1) * LA / RI; ++j) load_w(j, cur, k);
+    });
+    back = cur;
+    wait_loads<(S - 2) * (LA + LB) + LA>();
+    turn();
+    for (i = 1; i + S < steps; ++i) {
+      first_half(tokens);
+      // every wave has this step's fragments: its place takes the step S further on
+      reads_done();
+      k += 128;
+      multiply(f2, [&](int i) {
+#pragma unroll
+        for (int j = i * LA / RI; j < (i + 1) * LA / RI; ++j) load_w(j, cur, k);
+      });
+      back = cur;
+      wait_loads<(S - 2) * (LA + LB) + LA>();
+      turn();
+    }
+    first_half(tokens);
+    multiply(f2, nothing);
+    wait_loads<0>();
+    turn();
+    ++i;
+  }
+  for (; i < steps - 1; ++i) {
+    first_half(nothing);
+    multiply(f2, nothing);
+    wait_loads<0>();
     turn();
   }
-  first_half();
-  multiply(f2);
-  wait_loads<0>();
-  turn();
-  first_half();
-  multiply(f2);
-  multiply(f3);
+  first_half(nothing);
+  multiply(f2, nothing);
+  multiply(f3, nothing);
   // a lane holds, of token lane % 32, four rows in eight; the wave's halves swap, so
   // that it has eight in sixteen
   const int half = lane >> 5;
@@ -203,42 +259,197 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   }
 }
 
-template <int TY>
-__global__ __launch_bounds__(kThreads) void q8_matmul_kernel(Q8MatmulArgs a) {
-  // a wave takes 16 rows of w and 16 tokens
+// Few tokens: a workgroup takes 16 RB rows of w and up to 16 NT tokens, its 8 waves
+// the pieces of 128 columns in turn; their sums meet in LDS.  The weights go from
+// memory to registers, kAhead pieces of a wave at a time.  TX >= 0: x is of that type
+// and the workgroup makes its codes itself (4 tokens at most), while its first weights
+// are on the way.
+constexpr int kFewWaves = 8, kAhead = 6;
+
+template <int TY, int TX, int NT, int RB>
+__global__ __launch_bounds__(64 * kFewWaves) void q8_few_kernel(Q8MatmulArgs a, const void *x, long long ldx) {
+  extern __shared__ __attribute__((aligned(16))) int8_t lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r0 = (blockIdx.x * 4 + wave) * 16, t0 = blockIdx.y * 16;
-  if (r0 >= a.rows) return;
-  const int r = min(r0 + (lane & 15), a.rows - 1), t = min(t0 + (lane & 15), a.T - 1);
-  const int8_t *wp = a.w + r * a.ldw, *xp = a.x + t * a.ldx;
-  i32x4 acc = {0, 0, 0, 0};
-  for (int k = 0; k < a.cols; k += 64) {
-    const int kk = k + (lane >> 4) * 16;
-    i32x4 wv = {0, 0, 0, 0}, xv = *(const i32x4 *)(xp + kk);
-    if (kk < a.cols) wv = *(const i32x4 *)(wp + kk);
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv, acc, 0, 0, 0);
+  const int r0 = blockIdx.x * 16 * RB, pieces = (a.cols + 127) / 128, padded = pieces * 128;
+  i32x4 *sums = (i32x4 *)lds;                                  // [kFewWaves][NT * RB][64]
+  int8_t *codes = lds + kFewWaves * NT * RB * 64 * 16;         // TX >= 0: [T][padded]
+  const int at = (lane >> 4) * 16, wide = (a.cols + 15) & ~15;
+  const int8_t *wp[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) wp[b] = a.w + (long long)min(r0 + 16 * b + (lane & 15), a.rows - 1) * a.ldw + at;
+  i32x4 wv[kAhead][RB][2];
+  const auto load = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int c = (p0 + u * kFewWaves) * 128 + at;
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          // (columns past the last are multiplied by x's zeros)
+          wv[u][b][h] = c + 64 * h < wide ? *(const i32x4 *)(wp[b] + c - at + 64 * h) : i32x4{0, 0, 0, 0};
+    }
+  };
+  load(wave);
+  __shared__ float scales[TX >= 0 ? 4 : 16 * NT];
+  const int8_t *xp[NT];
+  if constexpr (TX >= 0) {
+    __shared__ uint32_t part[4][kFewWaves];
+    for (int t = 0; t < a.T; ++t) {
+      uint32_t m = 0;
+      for (int c = 8 * threadIdx.x; c < a.cols; c += 8 * 64 * kFewWaves)
+        m = largest(load8<TX>(x, t * ldx, c, a.cols), m);
+      m = wave_largest(m);
+      if (lane == 0) part[t][wave] = m;
+    }
+    __syncthreads();
+    for (int t = 0; t < a.T; ++t) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kFewWaves; ++i) m = max(m, part[t][i]);
+      const float s = q8_scale(m), inv = 1.f / s;
+      if (threadIdx.x == 0) scales[t] = s;
+      for (int c = 8 * threadIdx.x; c < padded; c += 8 * 64 * kFewWaves)
+        *(uint2 *)(codes + t * padded + c) =
+            c < a.cols ? q8_codes(load8<TX>(x, t * ldx, c, a.cols), s, inv) : make_uint2(0u, 0u);
+    }
+    __syncthreads();
+    xp[0] = codes + min(lane & 15, a.T - 1) * padded + at;
+  } else {
+    if ((int)threadIdx.x < min(a.T, 16 * NT)) scales[threadIdx.x] = a.x_scales[threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xp[j] = a.x + (long long)min(16 * j + (lane & 15), a.T - 1) * a.ldx + at;
   }
-  if (t0 + (lane & 15) >= a.T) return;
-  const float sx = a.x_scales[t];
-  for (int i = 0; i < 4; ++i) {
-    const int rr = r0 + (lane >> 4) * 4 + i;
-    if (rr < a.rows) store1(a.out, TY, t * a.ldo + rr, scaled(acc[i], sx, a.w_scales[rr]));
+  i32x4 acc[RB][NT] = {};
+  for (int p0 = wave; p0 < pieces; p0 += kAhead * kFewWaves) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int p = p0 + u * kFewWaves;
+      if (p < pieces) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const i32x4 xv = *(const i32x4 *)(xp[j] + p * 128 + 64 * h);
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+              acc[b][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u][b][h], xv, acc[b][j], 0, 0, 0);
+          }
+      }
+    }
+    if (p0 + kAhead * kFewWaves < pieces) load(p0 + kAhead * kFewWaves);
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sums[(wave * NT * RB + b * NT + j) * 64 + lane] = acc[b][j];
+  __syncthreads();
+  // wave i takes tile i
+  for (int i = wave; i < NT * RB; i += kFewWaves) {
+    i32x4 v = sums[i * 64 + lane];
+#pragma unroll
+    for (int o = 1; o < kFewWaves; ++o) v += sums[(o * NT * RB + i) * 64 + lane];
+    const int t = 16 * (i % NT) + (lane & 15), r = r0 + 16 * (i / NT) + 4 * (lane >> 4);
+    if (t >= a.T || r >= a.rows) continue;
+    const float sx = scales[t];
+    float o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = scaled(v[e], sx, a.w_scales[min(r + e, a.rows - 1)]);
+    const float4 f = make_float4(o[0], o[1], o[2], o[3]);
+    if (r + 4 <= a.rows)
+      store4(a.out, TY, t * a.ldo + r, f);
+    else
+      store_few(a.out, TY, t * a.ldo + r, f, a.rows - r);
   }
 }
 
+// Tiles (rows x tokens, waves, steps under way) and what a step of 128 columns takes
+// on a CU, in microseconds: alone, and with as many workgroups as fit; `tile` is a
+// tile's start and end.  Fitted to 48 products of 65 to 4096 tokens, 200 to 12288
+// columns and 64 to 32768 rows (matrices out of the cache), of which the estimate's
+// choice took 1.03 of the best tile's time in the mean and 1.17 at most; one tile of
+// 256 x 256 for all took 1.9 and 4.8.
+struct Tile {
+  int rows, tokens, fit;
+  float tile, alone, shared;
+};
+constexpr Tile kTiles[] = {
+    {256, 256, 1, 9.6f, 1.11f, 1.11f}, {160, 128, 2, 6.0f, 0.49f, 1.32f}, {128, 128, 2, 5.5f, 0.43f, 1.08f},
+    {96, 128, 1, 4.0f, 0.39f, 0.39f},  {64, 64, 2, 2.0f, 0.21f, 0.44f},   {32, 64, 2, 1.8f, 0.19f, 0.28f},
+    {64, 32, 3, 1.1f, 0.17f, 0.49f},
+};
+
+int best_tile(const Q8MatmulArgs &a) {
+  int best = 0;
+  double least = 1e30;
+  for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
+    const Tile &c = kTiles[i];
+    const int64_t tiles = (int64_t)((a.rows + c.rows - 1) / c.rows) * ((a.T + c.tokens - 1) / c.tokens);
+    if (tiles >= 1 << 22) continue;  // a grid holds fewer than 2^32 threads
+    const int64_t n = (tiles + 255) / 256, steps = (a.cols + 127) / 128;  // tiles a CU
+    const double t = (double)((n + c.fit - 1) / c.fit) * c.tile +
+                     (double)steps * ((double)(n / c.fit) * c.shared + (double)(n % c.fit) * c.alone);
+    if (t < least) least = t, best = i;
+  }
+  return best;
+}
+
+template <int TY, int RT, int TT, int WR, int WT, int S>
+hipError_t launch_tile(const Q8MatmulArgs &a, hipStream_t s) {
+  const int r = (a.rows + RT - 1) / RT, t = (a.T + TT - 1) / TT;
+  return launch(q8_tile_kernel<TY, RT, TT, WR, WT, S>, dim3(r * t), dim3(64 * WR * WT), s, a, r, t);
+}
+
+template <int TY, int TX, int NT, int RB>
+hipError_t launch_few(const Q8MatmulArgs &a, const Q8RowsArgs *q, hipStream_t s) {
+  const size_t codes = q ? (size_t)a.T * q8_padded(a.cols) : 0;
+  return launch_lds(q8_few_kernel<TY, TX, NT, RB>, dim3((a.rows + 16 * RB - 1) / (16 * RB)), dim3(64 * kFewWaves),
+                    kFewWaves * NT * RB * 1024 + codes, s, a, q ? q->x : nullptr, q ? q->ldx : 0ll);
+}
+
+// Few tokens and rows: too few tiles of 64 or 32 rows to keep the CUs' loads under way,
+// so that 8 waves share a tile's columns.  One token, 2816 and 6144 columns, 4096 rows:
+// 6.8 and 8.4 us (tiles of 64 x 32 take 8.5 and 12.8); 8192 rows: 6.9 and 12.1 (8.2 and
+// 13.4); 16384 rows: 11.7 and 22.0 (10.9 and 19.8).
+bool few(const Q8MatmulArgs &a) { return a.T <= (a.rows <= 4096 ? 32 : 16) && a.rows < 10240; }
+
 template <int TY>
 hipError_t launch_type(const Q8MatmulArgs &a, hipStream_t s) {
-  if (a.T > 64 && a.cols > 128) {
-    const int r = (a.rows + 255) / 256, t = (a.T + 255) / 256;
-    return launch(q8_tile_kernel<TY, 256, 256, 2, 4>, dim3(r * t), dim3(512), s, a, r, t);
+  if (few(a)) {
+    if (a.rows > 4096) return launch_few<TY, -1, 1, 2>(a, nullptr, s);
+    return a.T <= 16 ? launch_few<TY, -1, 1, 1>(a, nullptr, s) : launch_few<TY, -1, 2, 1>(a, nullptr, s);
   }
-  return launch(q8_matmul_kernel<TY>, dim3((a.rows + 63) / 64, (a.T + 15) / 16), dim3(kThreads), s, a);
+  switch (best_tile(a)) {
+    case 0: return launch_tile<TY, 256, 256, 2, 4, 2>(a, s);
+    case 1: return launch_tile<TY, 160, 128, 1, 4, 2>(a, s);
+    case 2: return launch_tile<TY, 128, 128, 2, 2, 2>(a, s);
+    case 3: return launch_tile<TY, 96, 128, 1, 4, 4>(a, s);
+    case 4: return launch_tile<TY, 64, 64, 2, 2, 4>(a, s);
+    case 5: return launch_tile<TY, 32, 64, 1, 2, 6>(a, s);
+    default: return launch_tile<TY, 64, 32, 2, 1, 4>(a, s);
+  }
+}
+
+// The tokens' codes made by the product's workgroups: saves a launch.
+template <int TY>
+hipError_t launch_few_linear(const Q8RowsArgs &q, const Q8MatmulArgs &a, hipStream_t s) {
+  return a.rows > 4096 ? launch_few<TY, TY, 1, 2>(a, &q, s) : launch_few<TY, TY, 1, 1>(a, &q, s);
 }
 
 }  // namespace
 
 hipError_t launch_q8_matmul(const Q8MatmulArgs &a, hipStream_t s) {
   return a.type == kF32 ? launch_type<kF32>(a, s) : a.type == kBf16 ? launch_type<kBf16>(a, s) : launch_type<kF16>(a, s);
+}
+
+hipError_t launch_q8_linear(const Q8RowsArgs &q, const Q8MatmulArgs &a, hipStream_t s) {
+  // each workgroup makes all codes: worth it while they are few (and fit the LDS)
+  if (few(a) && a.T <= 4 && a.T * q8_padded(a.cols) <= 32768 && q.type == a.type)
+    return a.type == kF32    ? launch_few_linear<kF32>(q, a, s)
+           : a.type == kBf16 ? launch_few_linear<kBf16>(q, a, s)
+                             : launch_few_linear<kF16>(q, a, s);
+  const hipError_t e = launch_q8_rows(q, s);
+  return e == hipSuccess ? launch_q8_matmul(a, s) : e;
 }
 
 }  // namespace moe

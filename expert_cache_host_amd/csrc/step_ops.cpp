@@ -32,15 +32,18 @@ bool misaligned(const void *p, int32_t type) {
 const char *codes_fault(const void *codes, int64_t stride, int64_t least, int32_t n) {
   if (!codes) return "codes are NULL";
   if ((uintptr_t)codes % 16) return "codes must be 16-byte aligned";
-  if (n > 1 && (stride < least || stride % 16))
-    return "codes' stride must be a multiple of 16 that holds a padded row";
+  if (n > 1 && (stride < least || stride % 16 || stride > (1 << 22)))
+    return "codes' stride must be a multiple of 16 that holds a padded row, at most 2^22";
   return nullptr;
 }
 
 const char *q8_sizes_fault(int32_t n_tokens, int32_t rows, int32_t cols) {
   if (cols < 1 || cols > MOE_Q8_MAX_COLS) return "cols must be in [1, 131072]";
-  if (rows < 1 || rows > MOE_Q8_MAX_ROWS) return "rows must be in [1, 2^24]";
+  if (rows < 1 || rows > MOE_Q8_MAX_ROWS) return "rows must be in [1, 2^24)";
   if (n_tokens < 0 || n_tokens > MOE_Q8_MAX_TOKENS) return "n_tokens must be in [0, 2^20]";
+  // a grid holds fewer than 2^32 threads, 512 a tile of 256 x 256
+  if ((int64_t)((n_tokens + 255) / 256) * ((rows + 255) / 256) >= 1 << 22)
+    return "n_tokens / 256 * rows / 256 must stay below 2^22";
   return nullptr;
 }
 
@@ -53,7 +56,7 @@ moe_status moe_q8_rows(const void *x, int32_t type, int64_t x_stride, int32_t n_
   clear_error();
   if (bad_type(type)) return einval("element type must be MOE_F32, MOE_BF16 or MOE_F16");
   if (cols < 1 || cols > MOE_Q8_MAX_COLS) return einval("cols must be in [1, 131072]");
-  if (n_rows < 0 || n_rows > MOE_Q8_MAX_ROWS) return einval("n_rows must be in [0, 2^24]");
+  if (n_rows < 0 || n_rows > MOE_Q8_MAX_ROWS) return einval("n_rows must be in [0, 2^24)");
   if (x_stride < 0) return einval("x_stride must be >= 0");
   if (n_rows == 0) return MOE_OK;
   if (!x || !scales) return einval("x or scales is NULL");
@@ -116,8 +119,7 @@ moe_status moe_q8_linear(const void *x, int32_t type, int64_t x_stride, int32_t 
   a.x = q.codes, a.w = (const int8_t *)w, a.x_scales = q.scales, a.w_scales = w_scales, a.out = out;
   a.ldx = padded, a.ldw = w_stride, a.ldo = out_stride, a.type = out_type;
   a.T = n_tokens, a.rows = rows, a.cols = cols;
-  const hipError_t e = moe::launch_q8_rows(q, stream);
-  return done(e == hipSuccess ? moe::launch_q8_matmul(a, stream) : e);
+  return done(moe::launch_q8_linear(q, a, stream));
 }
 
 moe_status moe_route(const void *logits, int32_t type, int64_t stride, const float *bias, int32_t n_tokens,

@@ -28,6 +28,8 @@ struct Q8MatmulArgs {
   int type, T, rows, cols;
 };
 hipError_t launch_q8_matmul(const Q8MatmulArgs &a, hipStream_t s);
+// Both: q's codes and scales are a.x and a.x_scales, memory that may stay unwritten.
+hipError_t launch_q8_linear(const Q8RowsArgs &q, const Q8MatmulArgs &a, hipStream_t s);
 
 constexpr int kRouteMaxExperts = 512, kRouteMaxTopk = 64, kRouteMaxGroups = 64;
 

@@ -102,13 +102,13 @@ class Q8Matrix:
                 (codes.shape[1] > 1 and codes.stride(1) != 1):
             raise ValueError("codes must be int8 [rows, cols] with contiguous rows")
         self.rows, self.cols = codes.shape
-        if self.rows > 1 << 24 or self.cols > 131072:
-            raise ValueError("a matrix holds at most 2^24 rows of 131072 columns")
+        if self.rows >= 1 << 24 or self.cols > 131072:
+            raise ValueError("a matrix holds fewer than 2^24 rows, of at most 131072 columns")
         if scales.get_device() != dev or scales.dtype != torch.float32 or scales.shape != (self.rows,) or \
                 not scales.is_contiguous():
             raise ValueError("scales must be contiguous float32 [rows] beside the codes")
-        if codes.data_ptr() % 16 or self.cols % 16 or (self.rows > 1 and codes.stride(0) % 16) or \
-                (self.rows > 1 and codes.stride(0) < self.cols):
+        if codes.data_ptr() % 16 or self.cols % 16 or (
+                self.rows > 1 and (codes.stride(0) % 16 or not self.cols <= codes.stride(0) <= 1 << 22)):
             with torch.cuda.device(dev):
                 laid = torch.zeros((self.rows, -(-self.cols // 16) * 16), dtype=torch.int8, device=codes.device)
                 laid[:, :self.cols] = codes

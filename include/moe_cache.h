@@ -585,7 +585,7 @@ moe_status moe_kv_attend(const moe_kv_cache *cache, const moe_kv_batch *batch, i
  * allocation, no waiting; capturable; strides in elements. */
 
 #define MOE_Q8_MAX_COLS 131072
-#define MOE_Q8_MAX_ROWS (1 << 24)
+#define MOE_Q8_MAX_ROWS ((1 << 24) - 1)
 #define MOE_Q8_MAX_TOKENS (1 << 20)
 #define MOE_ROUTE_MAX_TOKENS (1 << 24)
 #define MOE_SAMPLE_MAX_ROWS 65535
@@ -613,20 +613,21 @@ moe_status moe_q8_rows(const void *x, int32_t type, int64_t x_stride, int32_t n_
 /* moe_q8_matmul -- out[t][r] = x_scales[t] w_scales[r] sum_c x[t][c] w[r][c].
  *
  *   x       int8 [n_tokens][cols], 16-byte aligned, rows zeroed up to a multiple of
- *           MOE_Q8_PAD as moe_q8_rows writes them; x_stride a multiple of 16
+ *           MOE_Q8_PAD as moe_q8_rows writes them; x_stride a multiple of 16, at most 2^22
  *   w       int8 [rows][cols], 16-byte aligned; w_stride a multiple of 16 that holds a
- *           row; the bytes of a row from cols to the next multiple of 16 are read, with
+ *           row, at most 2^22; the bytes of a row from cols to the next multiple of 16 are read, with
  *           no effect
  *   out     [n_tokens][rows] of `type`
  *
  * The sum is an exact 32-bit integer (codes of x in [-127, 127]); it is rounded to
- * float32, multiplied by x_scales[t], then by w_scales[r], and rounded to `type`. */
+ * float32, multiplied by x_scales[t], then by w_scales[r], and rounded to `type`.
+ * n_tokens / 256 * rows / 256 (each rounded up) must stay below 2^22. */
 moe_status moe_q8_matmul(const void *x, int64_t x_stride, const float *x_scales, int32_t n_tokens, const void *w,
                          int64_t w_stride, const float *w_scales, int32_t rows, int32_t cols, void *out, int32_t type,
                          int64_t out_stride, moe_stream_t stream);
 
 /* moe_q8_linear -- both: x [n_tokens][cols] of `type` in 8 bits as moe_q8_rows gives
- * it, then moe_q8_matmul into out of `out_type`; the same results.
+ * it, then moe_q8_matmul into out of `out_type`; the same results, refusals and limits.
  *   workspace  device memory of moe_q8_linear_workspace bytes, 16-byte aligned, for this
  *              call alone until its work is done */
 int64_t moe_q8_linear_workspace(int32_t n_tokens, int32_t rows, int32_t cols);

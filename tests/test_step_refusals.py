@@ -33,6 +33,7 @@ def test_q8_rows(kw, msg):
 SIZES = [
     (dict(t=-1), "element type"), (dict(cols=0), "cols"), (dict(cols=131073, ldw=131088), "cols"), (dict(rows=0), "rows"),
     (dict(rows=(1 << 24) + 1, ldo=1 << 25), "rows"), (dict(T=-1), "n_tokens"), (dict(T=(1 << 20) + 1), "n_tokens"),
+    (dict(T=1 << 20, rows=1 << 18, ldo=1 << 18), "2^22"), (dict(ldw=(1 << 22) + 16), "2^22"),
     (dict(ldo=39), "out_stride"), (dict(w=None), "NULL"), (dict(w=P + 8), "16-byte"), (dict(ldw=96), "multiple of 16"),
     (dict(ldw=120), "multiple of 16"), (dict(ws=None), "NULL"), (dict(out=None), "NULL"), (dict(ws=P + 2), "aligned"),
     (dict(out=P + 2), "aligned"),
