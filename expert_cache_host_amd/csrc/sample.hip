@@ -2,18 +2,17 @@
 //
 // Weights are whole numbers, rint(2^42 exp((z - max) / temperature)), so that sums do
 // not depend on the order of additions and every border is decided alike wherever it
-// is computed.  A row of up to kCap tokens is sorted in LDS.  A longer one takes four
-// launches, the first three over `segments` workgroups a row:
-//   tops      the largest logit (and its first id);
-//   bins      count and weight of the tokens by their distance from it, in kBins bins;
-//   gather    from the bins' running sums: in which bins the borders of top-k, top-p
-//             and min-p and the token itself can lie (each border is known to a bin,
-//             which bounds the next); the tokens of those bins, a few hundred mostly,
-//             are gathered;
-//   resolve   one workgroup a row sorts them, and the running sums settle the borders
-//             and the token exactly.
-// Where they are more than kCap (nearly flat rows), resolve finds the borders digit by
-// digit of the logits' ordered bits over the whole row: right, and slow.
+// is computed.  Count and weight of the tokens are summed by their distance from the
+// largest logit, in kBins bins; from the bins' running sums follows in which of them
+// the borders of top-k, top-p and min-p and the token itself can lie (each border is
+// known to a bin, which bounds the next); the tokens of those bins, a few hundred
+// mostly, are gathered and sorted, and settle borders and token exactly.  Where they
+// are more than kCap (nearly flat rows), the borders are found digit by digit of the
+// logits' ordered bits over the whole row: right, and slow.
+//
+// A row of up to kShortRow tokens takes one workgroup and one launch.  A longer one
+// takes four: its largest logit, its bins and the gathering each over many workgroups,
+// the rest in one.
 #include "device_types.hpp"
 #include "step_ops.hpp"
 
@@ -21,11 +20,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kCap = 2048;       // tokens sorted in LDS
+constexpr int kCap = 2048;        // tokens sorted in LDS
 constexpr int kBins = 2048;
 constexpr int kMaxSegments = 128;
-constexpr int kScan = 512;       // threads of the first three kernels
-constexpr double kOne = 4398046511104.0;  // 2^42: the largest token's weight
+constexpr int kScan = 512;        // threads of a workgroup
+constexpr int kShortRow = 16384;
 
 // A logit as a number of the same order: NaN is minus infinity (0), plus
 // infinity the largest float, -0 is +0.
@@ -38,11 +37,10 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
 }
 
-// exp(-d) for d >= 0 by its series around the nearest multiple of ln 2; the terms left
-// out are below 2^-56 of it.  0 from 40 on, where a weight is 0 anyway.
+// exp(-d) for 0 <= d < 40 by its series around the nearest multiple of ln 2; the terms
+// left out are below 2^-56 of it.
 __device__ __forceinline__ double exp_minus(double d) {
 #pragma clang fp contract(off)
-  if (!(d < 40.0)) return 0.0;
   const double n = rint(d * 1.4426950408889634);
   // ln 2 in two parts, the first with zeros behind so that n times it is exact
   double r = fma(n, 0x1.62e42fefap-1, -d);
@@ -64,17 +62,56 @@ __device__ __forceinline__ double exp_minus(double d) {
   return __builtin_bit_cast(double, __builtin_bit_cast(int64_t, p) - ((int64_t)(int)n << 52));
 }
 
+// 2^42 exp(-i / 64), made by every workgroup: with it a weight takes a polynomial of
+// degree 6 (the terms left out are below 2^-54).
+constexpr int kTable = 1920;     // distances up to 30
+constexpr double kOne = 4398046511104.0;  // 2^42: the largest token's weight
+
+template <int THREADS>
+__device__ __forceinline__ void fill_table(double *table) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < kTable; i += THREADS) table[i] = exp_minus(i * 0.015625) * kOne;
+}
+
+// A distance below 30: its bin, and the two factors of its weight.  Bins are 1/128 of a
+// temperature wide up to 12, then 5/128.
+struct Spot {
+  int bin;
+  double whole, part;
+  __device__ __forceinline__ Spot(double d, const double *table) {
+#pragma clang fp contract(off)
+    const int t = (int)(d * 128.0);
+    bin = t < 1536 ? t : 1536 + (int)(__umul24(t - 1536, 52429) >> 18);  // (t - 1536) / 5
+    const double f = fma((double)(t >> 1), -0.015625, d);
+    double p = 1.0 / 720.0;
+    p = fma(p, f, -1.0 / 120.0);
+    p = fma(p, f, 1.0 / 24.0);
+    p = fma(p, f, -1.0 / 6.0);
+    p = fma(p, f, 0.5);
+    p = fma(p, f, -1.0);
+    part = fma(p, f, 1.0);
+    whole = table[t >> 1];
+  }
+  // rounded to a whole number by the sum with 2^52
+  __device__ __forceinline__ unsigned long long weight() const {
+    return __builtin_bit_cast(unsigned long long, fma(whole, part, 4503599627370496.0)) - 0x4330000000000000ull;
+  }
+  __device__ __forceinline__ double ratio() const { return whole * part * (1.0 / kOne); }
+};
+
+// The first distance of a bin.
+__device__ __forceinline__ double bin_start(int b) { return b < 1536 ? b * 0.0078125 : 12.0 + (b - 1536) * 0.0390625; }
+
 // A row's settings and its largest logit.
 struct Row {
-  double top, inv;           // largest logit, 1 / temperature
+  double top, temp, inv;     // largest logit, temperature and its inverse
   double share, least, u;    // top-p (1: all), min-p (0: all), the random number
   int k;                     // top-k (0: all)
   bool greedy;
-  __device__ __forceinline__ Row(const SampleArgs &a, long long row, uint32_t top_key) {
-    const double t = a.temperatures ? (double)a.temperatures[row] : a.temperature;
-    greedy = !(t > 0.0);
-    inv = greedy ? 1.0 : 1.0 / t;
-    top = top_key ? (double)value_of(top_key) : 0.0;
+  __device__ __forceinline__ Row(const SampleArgs &a, long long row) {
+    temp = a.temperatures ? (double)a.temperatures[row] : a.temperature;
+    greedy = !(temp > 0.0);
+    inv = greedy ? 1.0 : 1.0 / temp;
     const double p = a.top_ps ? (double)a.top_ps[row] : a.top_p;
     share = p < 1.0 ? fmax(p, 0.0) : 1.0;  // NaN keeps all
     const double m = a.min_ps ? (double)a.min_ps[row] : a.min_p;
@@ -83,36 +120,29 @@ struct Row {
     const double v = (double)a.u[row];
     u = v >= 0.0 ? fmin(v, 1.0) : 0.0;
   }
-  // how far below the largest, in temperatures
-  __device__ __forceinline__ double distance(uint32_t key) const {
+  // how far below the largest, in temperatures; weights are 0 from 30 on
+  // (minus infinity and NaN: not below 30)
+  __device__ __forceinline__ double distance(float v) const {
 #pragma clang fp contract(off)
-    return key ? (top - (double)value_of(key)) * inv : __builtin_inf();
+    return (top - (double)v) * inv;
   }
-  __device__ __forceinline__ uint64_t weight(double d) const { return (uint64_t)rint(exp_minus(d) * kOne); }
   // positions (1, 2, ...) in the running sums
-  __device__ __forceinline__ uint64_t share_of(uint64_t sum) const {
-    const uint64_t t = (uint64_t)ceil(share * (double)sum);
+  __device__ __forceinline__ unsigned long long share_of(unsigned long long sum) const {
+    const unsigned long long t = (unsigned long long)ceil(share * (double)sum);
     return t < 1 ? 1 : t < sum ? t : sum;
   }
-  __device__ __forceinline__ uint64_t draw(uint64_t kept) const {
-    const uint64_t t = (uint64_t)(u * (double)kept);
+  __device__ __forceinline__ unsigned long long draw(unsigned long long kept) const {
+    const unsigned long long t = (unsigned long long)(u * (double)kept);
     return (t < kept ? t : kept - 1) + 1;
   }
 };
 
-// Bins: 1/128 of a temperature wide up to 12, then 5/128 up to 32.  Tokens of weight 0
-// (from 29.8 on) lie in none.
-__device__ __forceinline__ int bin_of(double d) {
-#pragma clang fp contract(off)
-  return d < 12.0 ? (int)(d * 128.0) : 1536 + min((int)((d - 12.0) * 25.6), 511);
-}
-
-// What a row has in the workspace.
+// What a long row has in the workspace.
 struct Space {
-  unsigned long long tops[kMaxSegments];  // key << 32 | ~id
+  unsigned long long tops[kMaxSegments];  // of a segment: key << 32 | ~id
   unsigned long long sum[kBins];
-  unsigned long long near[kCap];          // gathered tokens, as tops
   uint32_t count[kBins];
+  unsigned long long near[kCap];          // gathered tokens
   uint32_t gathered, pad[3];
 };
 
@@ -120,17 +150,57 @@ __device__ __forceinline__ unsigned long long token_of(uint32_t key, int id) {
   return (unsigned long long)key << 32 | (uint32_t)~id;
 }
 
-// Calls f(key, id) for a thread's tokens of [lo, hi) of the row, four at a time.
-template <int TY, int THREADS, class F>
-__device__ __forceinline__ void each_token(const SampleArgs &a, long long row, int lo, int hi, F f) {
-  const long long at = row * a.ldz;
-  int i = lo + 4 * threadIdx.x;
-  for (; i + 3 < hi; i += 4 * THREADS) {
-    const float4 v = load4(a.z, TY, at + i);
-    f(order_bits(v.x), i), f(order_bits(v.y), i + 1), f(order_bits(v.z), i + 2), f(order_bits(v.w), i + 3);
+// A thread's tokens of [lo, hi) of the row, four at a time; the first kAhead fours are
+// loaded before they are needed.  One copy of the code for each four, and with `small`
+// for each token: most of what a short call takes is the fetching of its instructions.
+constexpr int kAhead = 2;
+
+template <int TY, int THREADS>
+struct Tokens {
+  float4 first[kAhead];
+  const SampleArgs &a;
+  long long at;
+  int lo, hi;
+  __device__ __forceinline__ float4 load(int i) const {
+    if (i + 3 < hi) return load4(a.z, TY, at + i);
+    const float none = -__builtin_inff();
+    float4 v = make_float4(none, none, none, none);
+    if (i < hi) {
+      v = load_few(a.z, TY, at + i, hi - i);
+      if (hi - i < 2) v.y = none;
+      if (hi - i < 3) v.z = none;
+      v.w = none;
+    }
+    return v;
   }
-  for (; i < hi; ++i) f(order_bits(load1(a.z, TY, at + i)), i);
-}
+  __device__ __forceinline__ Tokens(const SampleArgs &a_, long long row, int lo_, int hi_)
+      : a(a_), at(row * a_.ldz), lo(lo_), hi(hi_) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) first[j] = load(lo + 4 * ((int)threadIdx.x + THREADS * j));
+  }
+  // Calls f(value, id) for each; plus infinity comes as the largest float, places past
+  // the end as minus infinity.
+  template <bool kSmall, class F>
+  __device__ __forceinline__ void each(F f) const {
+    float4 v0 = first[0], v1 = first[1];
+    const auto one = [&](float v, int i) { f(v > 3.40282347e38f ? 3.40282347e38f : v, i); };
+#pragma unroll 1
+    for (int i = lo + 4 * (int)threadIdx.x; i < hi; i += 4 * THREADS) {
+      const float4 v = v0;
+      v0 = v1, v1 = load(i + 4 * THREADS * kAhead);
+      if constexpr (kSmall) {
+        float x = v.x, y = v.y, z = v.z;
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          one(x, i + e);
+          x = y, y = z, z = v.w;
+        }
+      } else {
+        one(v.x, i), one(v.y, i + 1), one(v.z, i + 2), one(v.w, i + 3);
+      }
+    }
+  }
+};
 
 template <class T>
 __device__ __forceinline__ T wave_max(T v) {
@@ -142,8 +212,21 @@ __device__ __forceinline__ T wave_max(T v) {
   return v;
 }
 
-// Sum of v over the threads before this one; `total` gets that of all.  `part` holds a
-// number a wave.
+template <int THREADS>
+__device__ __forceinline__ unsigned long long block_max(unsigned long long v, unsigned long long *part) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = part[threadIdx.x & (THREADS / 64 - 1)];
+#pragma unroll
+  for (int off = THREADS / 128; off >= 1; off >>= 1) {
+    const unsigned long long o = __shfl_xor(v, off, 64);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// Sum of v over the threads before this one; `total` gets that of all.
 template <class T, int THREADS>
 __device__ __forceinline__ T block_before(T v, T *part, T &total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -170,11 +253,51 @@ __device__ __forceinline__ void segment(const SampleArgs &a, int &lo, int &hi) {
   lo = min((int)blockIdx.x * n, a.V), hi = min(lo + n, a.V);
 }
 
-__device__ __forceinline__ unsigned long long top_of(const Space &s, int segments) {
-  unsigned long long t = 0;
-  for (int i = threadIdx.x & 63; i < segments; i += 64) t = max(t, s.tops[i]);
-  return wave_max(t);
+__device__ __forceinline__ void give(const SampleArgs &a, long long row, int token, double prob) {
+  a.token[row] = token;
+  if (a.prob) a.prob[row] = (float)prob;
 }
+
+// The workgroup's memory.
+template <int THREADS>
+struct Lds {
+  unsigned long long sum[kBins];   // of a bin, then of the bins before it
+  unsigned long long token[kCap], sorted[kCap];
+  double table[kTable];
+  uint32_t count[kBins];           // likewise
+  uint32_t wanted[kBins / 32], low, high, gathered;
+  unsigned long long part[THREADS / 64], ends[3], kept;
+  uint32_t part32[THREADS / 64];
+};
+
+// Adds the tokens to the bins.
+template <bool kSmall, int TY, int THREADS>
+__device__ __forceinline__ void add_bins(const Tokens<TY, THREADS> &tokens, const Row &r,
+                                         unsigned long long *sum, uint32_t *count, const double *table) {
+  const bool counts = r.k > 0;  // (looked at for top-k alone)
+  tokens.template each<kSmall>([&](float v, int) {
+    const double d = r.distance(v);
+    if (!(d < 30.0)) return;
+    const Spot at(d, table);
+    const unsigned long long w = at.weight();
+    if (!w) return;
+    atomicAdd(&sum[at.bin], w);
+    if (counts) atomicAdd(&count[at.bin], 1u);
+  });
+}
+
+// The first of a thread's largest tokens.
+struct First {
+  float v = -__builtin_inff();
+  int id = 0;
+  __device__ __forceinline__ void see(float o, int i) {
+    if (o > v) v = o, id = i;
+  }
+  __device__ __forceinline__ unsigned long long token() const {
+    const uint32_t key = order_bits(v);
+    return key ? token_of(key, id) : 0ull;
+  }
+};
 
 template <int TY>
 __global__ __launch_bounds__(kScan) void sample_tops_kernel(SampleArgs a) {
@@ -182,131 +305,112 @@ __global__ __launch_bounds__(kScan) void sample_tops_kernel(SampleArgs a) {
   Space &s = ((Space *)a.ws)[blockIdx.y];
   int lo, hi;
   segment(a, lo, hi);
-  unsigned long long t = 0;
-  each_token<TY, kScan>(a, blockIdx.y, lo, hi, [&](uint32_t key, int id) {
-    if (key) t = max(t, token_of(key, id));
-  });
-  t = wave_max(t);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = t;
+  const Tokens<TY, kScan> tokens(a, blockIdx.y, lo, hi);
   // what the next launches add to
   for (int i = blockIdx.x * kScan + threadIdx.x; i < kBins; i += gridDim.x * kScan) s.sum[i] = 0ull, s.count[i] = 0u;
   if (blockIdx.x == 0 && threadIdx.x == 0) s.gathered = 0u;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kScan / 64; ++i) t = max(t, part[i]);
-    s.tops[blockIdx.x] = t;
-  }
+  First first;
+  tokens.template each<false>([&](float v, int id) { first.see(v, id); });
+  const unsigned long long t = block_max<kScan>(first.token(), part);
+  if (threadIdx.x == 0) s.tops[blockIdx.x] = t;
+}
+
+__device__ __forceinline__ unsigned long long top_of(const Space &s, int segments) {
+  const int lane = threadIdx.x & 63;
+  unsigned long long t = lane < segments ? s.tops[lane] : 0ull;
+  if (lane + 64 < segments) t = max(t, s.tops[lane + 64]);
+  return wave_max(t);
 }
 
 template <int TY>
 __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
   __shared__ unsigned long long sum[kBins];
   __shared__ uint32_t count[kBins];
+  __shared__ double table[kTable];
   Space &s = ((Space *)a.ws)[blockIdx.y];
-  for (int i = threadIdx.x; i < kBins; i += kScan) sum[i] = 0ull, count[i] = 0u;
-  const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
-  const Row r(a, blockIdx.y, top);
-  if (!top || r.greedy) return;
-  __syncthreads();
   int lo, hi;
   segment(a, lo, hi);
-  each_token<TY, kScan>(a, blockIdx.y, lo, hi, [&](uint32_t key, int) {
-    const double d = r.distance(key);
-    const unsigned long long w = r.weight(d);
-    if (w) {
-      const int b = bin_of(d);
-      atomicAdd(&count[b], 1u);
-      atomicAdd(&sum[b], w);
-    }
-  });
+  const Tokens<TY, kScan> tokens(a, blockIdx.y, lo, hi);
+  Row r(a, blockIdx.y);
+  const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
+  for (int i = threadIdx.x; i < kBins; i += kScan) sum[i] = 0ull, count[i] = 0u;
+  fill_table<kScan>(table);
+  if (!top || r.greedy) return;
+  r.top = (double)value_of(top);
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kScan)
-    if (count[i]) {
-      atomicAdd(&s.count[i], count[i]);
-      atomicAdd(&s.sum[i], sum[i]);
-    }
+  add_bins<false>(tokens, r, sum, count, table);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kScan) {
+    if (sum[i]) atomicAdd(&s.sum[i], sum[i]);
+    if (count[i]) atomicAdd(&s.count[i], count[i]);
+  }
 }
 
-template <int TY>
-__global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
-  constexpr int kMine = kBins / kScan;
-  __shared__ unsigned long long part64[kScan / 64], ends[3], found[kCap];
-  __shared__ uint32_t part32[kScan / 64], wanted[kBins / 32], mine, base;
-  Space &s = ((Space *)a.ws)[blockIdx.y];
-  const int tid = threadIdx.x;
-  const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
-  const Row r(a, blockIdx.y, top);
-  if (!top || r.greedy) return;
-  if (tid < kBins / 32) wanted[tid] = 0u;
-  if (tid == 0) mine = 0u;
+// From the bins' counts and sums (in m; they become those of the bins before each):
+// which bins are wanted, and the range of keys that holds them.
+template <int THREADS>
+__device__ void decide(const Row &r, Lds<THREADS> &m, unsigned long long &total, uint32_t &tokens) {
+  constexpr int kMine = kBins / THREADS;
+  const int tid = threadIdx.x, b0 = kMine * tid;
   // running counts and sums at the ends of this thread's bins
-  uint32_t c[kMine + 1], tokens;
-  unsigned long long w[kMine + 1], total;
+  uint32_t c[kMine + 1];
+  unsigned long long w[kMine + 1];
   c[0] = 0u, w[0] = 0ull;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) c[j + 1] = c[j] + s.count[kMine * tid + j], w[j + 1] = w[j] + s.sum[kMine * tid + j];
-  const uint32_t c0 = block_before<uint32_t, kScan>(c[kMine], part32, tokens);
-  const unsigned long long w0 = block_before<unsigned long long, kScan>(w[kMine], part64, total);
+  for (int j = 0; j < kMine; ++j) c[j + 1] = c[j] + m.count[b0 + j], w[j + 1] = w[j] + m.sum[b0 + j];
+  if (tid < kBins / 32) m.wanted[tid] = 0u;
+  if (tid == 0) m.low = kBins, m.high = 0u, m.gathered = 0u;
+  const uint32_t before32 = block_before<uint32_t, THREADS>(c[kMine], m.part32, tokens);
+  const unsigned long long before = block_before<unsigned long long, THREADS>(w[kMine], m.part, total);
 #pragma unroll
-  for (int j = 0; j <= kMine; ++j) c[j] += c0, w[j] += w0;
-  const auto want = [&](int b) { atomicOr(&wanted[b >> 5], 1u << (b & 31)); };
+  for (int j = 0; j <= kMine; ++j) c[j] += before32, w[j] += before;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) m.count[b0 + j] = c[j], m.sum[b0 + j] = w[j];
+  const auto want = [&](int b) {
+    atomicOr(&m.wanted[b >> 5], 1u << (b & 31));
+    atomicMin(&m.low, (uint32_t)b);
+    atomicMax(&m.high, (uint32_t)b);
+  };
   // what is kept lies in [lo, hi]
   unsigned long long lo = total, hi = total;
   if (r.k > 0 && (uint32_t)r.k < tokens) {
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-      if (c[j] < (uint32_t)r.k && (uint32_t)r.k <= c[j + 1]) want(kMine * tid + j), ends[0] = w[j], ends[1] = w[j + 1];
+      if (c[j] < (uint32_t)r.k && (uint32_t)r.k <= c[j + 1]) want(b0 + j), m.ends[0] = w[j], m.ends[1] = w[j + 1];
     __syncthreads();
-    lo = max(ends[0], 1ull), hi = ends[1];
+    lo = max(m.ends[0], 1ull), hi = m.ends[1];
   }
   if (r.share < 1.0) {
     const unsigned long long from = r.share_of(lo), to = r.share_of(hi);
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-      if (w[j] < to && w[j + 1] >= from) want(kMine * tid + j);
-      if (w[j] < to && w[j + 1] >= to) ends[2] = w[j + 1];
+      if (w[j] < to && w[j + 1] >= from) want(b0 + j);
+      if (w[j] < to && w[j + 1] >= to) m.ends[2] = w[j + 1];
     }
     __syncthreads();
-    lo = min(lo, from), hi = min(hi, ends[2]);
+    lo = min(lo, from), hi = min(hi, m.ends[2]);
   }
   if (r.least > 0.0) {
     // the border's distance, and the bins on either side of what rounding may make of it
     const double d = -log(r.least);
-    const int b0 = bin_of(fmin(fmax(d - 1e-9, 0.0), 31.9)), b1 = bin_of(fmin(d + 1e-9, 31.9));
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j) {
-      const int b = kMine * tid + j;
-      if (b >= b0 && b <= b1) want(b);
-      if (b == b0) ends[0] = w[j];
-      if (b == b1) ends[1] = w[j + 1];
+      const double first = bin_start(b0 + j), last = bin_start(b0 + j + 1);
+      if (d > last + 1e-9 || d < first - 1e-9) continue;
+      want(b0 + j);
+      if (d >= first + 1e-9 || b0 + j == 0) m.ends[0] = w[j];
+      if (d < last - 1e-9) m.ends[1] = w[j + 1];
     }
+    if (tid == 0 && d > 29.99) m.ends[0] = m.ends[1] = total;  // past every token
     __syncthreads();
-    lo = min(lo, max(ends[0], 1ull)), hi = min(hi, ends[1]);
+    lo = min(lo, max(m.ends[0], 1ull)), hi = min(hi, m.ends[1]);
   }
   const unsigned long long from = r.draw(lo), to = r.draw(hi);
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
-    if (w[j] < to && w[j + 1] >= from) want(kMine * tid + j);
+    if (w[j] < to && w[j + 1] >= from) want(b0 + j);
   __syncthreads();
-  // (those past kCap are only counted)
-  int first, last;
-  segment(a, first, last);
-  each_token<TY, kScan>(a, blockIdx.y, first, last, [&](uint32_t key, int id) {
-    const double d = r.distance(key);
-    if (!(d < 30.0)) return;
-    const int b = bin_of(d);
-    if (!(wanted[b >> 5] >> (b & 31) & 1u) || !r.weight(d)) return;
-    const uint32_t i = atomicAdd(&mine, 1u);
-    if (i < kCap) found[i] = token_of(key, id);
-  });
-  __syncthreads();
-  const uint32_t n = mine;
-  if (n == 0u) return;
-  if (tid == 0) base = atomicAdd(&s.gathered, n);
-  __syncthreads();
-  if (base + n > kCap) return;
-  for (uint32_t i = tid; i < n; i += kScan) s.near[base + i] = found[i];
 }
 
 // Sorts n (a power of two, at least 128) numbers in LDS, the largest first.  A pair's
@@ -332,92 +436,98 @@ __device__ void sort_falling(unsigned long long *x, int n) {
   __syncthreads();
 }
 
-__device__ __forceinline__ void give(const SampleArgs &a, long long row, int token, double prob) {
-  a.token[row] = token;
-  if (a.prob) a.prob[row] = (float)prob;
-}
-
-// The row's token from sorted tokens x[0..n): all of the row's, or (kBinned) those of
-// some bins, with the row's sums and counts before each bin in before and rank.
-// total and tokens are the row's; least_before the sum before the first bin in which
-// min-p's border can lie.
-template <int THREADS, bool kBinned>
-__device__ void settle(const SampleArgs &a, long long row, const Row &r, const unsigned long long *x, int n,
-                       unsigned long long *before, uint32_t *rank, unsigned long long total, uint32_t tokens,
-                       unsigned long long least_before) {
-  constexpr int kMine = kCap / THREADS;
-  __shared__ unsigned long long part[THREADS / 64], kept;
-  const int tid = threadIdx.x;
-  uint32_t key[kMine];
-  double d[kMine];
-  unsigned long long w[kMine], sum = 0, all;
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const int i = kMine * tid + j;
-    key[j] = i < n ? (uint32_t)(x[i] >> 32) : 0u;
-    d[j] = r.distance(key[j]);
-    w[j] = r.weight(d[j]);
-    sum += w[j];
-  }
-  unsigned long long at = block_before<unsigned long long, THREADS>(sum, part, all);
-  if constexpr (kBinned) {
-    // a bin's first gathered token: what its tokens' places and sums are off by
-    unsigned long long e = at;
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int i = kMine * tid + j;
-      if (w[j]) {
-        const int b = bin_of(d[j]);
-        if (i == 0 || bin_of(r.distance((uint32_t)(x[i - 1] >> 32))) != b) before[b] -= e, rank[b] -= (uint32_t)i;
-      }
-      e += w[j];
+// The gathered tokens, the largest first; where they are.
+template <int THREADS>
+__device__ const unsigned long long *sorted(Lds<THREADS> &m, int n) {
+  if (n <= 256) {
+    // a token's place is the number of larger ones
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      const unsigned long long mine = m.token[i];
+      int place = 0;
+      for (int j = 0; j < n; ++j) place += m.token[j] > mine;
+      m.sorted[place] = mine;
     }
     __syncthreads();
+    return m.sorted;
   }
-  unsigned long long to[kMine];
-  uint32_t place[kMine];
+  int size = 512;
+  while (size < n) size *= 2;
+  for (int i = n + threadIdx.x; i < size; i += THREADS) m.token[i] = 0ull;
+  __syncthreads();
+  sort_falling<THREADS>(m.token, size);
+  return m.token;
+}
+
+// The row's token from its n gathered tokens.  total and tokens are the row's.
+template <int THREADS>
+__device__ void settle(const SampleArgs &a, long long row, const Row &r, Lds<THREADS> &m, int n,
+                       unsigned long long total, uint32_t tokens) {
+  constexpr int kMine = kCap / THREADS;
+  const int tid = threadIdx.x, i0 = kMine * tid;
+  const unsigned long long *x = sorted(m, n);
+  int bin[kMine];
+  double ratio[kMine];
+  unsigned long long w[kMine], to[kMine], sum = 0, all;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    const int b = kBinned && w[j] ? bin_of(d[j]) : 0;
-    at += w[j];
-    to[j] = at + (kBinned ? before[b] : 0ull);
-    place[j] = (uint32_t)(kMine * tid + j) + (kBinned ? rank[b] : 0u);
+    bin[j] = -1, ratio[j] = 0.0, w[j] = 0ull;
+    if (i0 + j < n) {
+      const Spot at(r.distance(value_of((uint32_t)(x[i0 + j] >> 32))), m.table);
+      bin[j] = at.bin, ratio[j] = at.ratio(), w[j] = at.weight();
+    }
+    sum += w[j];
   }
-  if (tid == 0) kept = total;
+  unsigned long long before = block_before<unsigned long long, THREADS>(sum, m.part, all);
+  // a bin's first gathered token: what its tokens' sums and places are off by
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    if (bin[j] >= 0) {
+      const int last = i0 + j == 0 ? -1
+                       : j > 0     ? bin[j - 1]
+                                   : Spot(r.distance(value_of((uint32_t)(x[i0 - 1] >> 32))), m.table).bin;
+      if (last != bin[j]) m.sum[bin[j]] -= before, m.count[bin[j]] -= (uint32_t)(i0 + j);
+    }
+    before += w[j], to[j] = before;
+  }
+  if (tid == 0) m.kept = total;
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (bin[j] >= 0) to[j] += m.sum[bin[j]];
+  unsigned long long keep = total;
   if (r.k > 0 && (uint32_t)r.k < tokens) {
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-      if (w[j] && place[j] == (uint32_t)r.k - 1) kept = to[j];
+      if (bin[j] >= 0 && (uint32_t)(i0 + j) + m.count[bin[j]] == (uint32_t)r.k - 1) m.kept = to[j];
+    __syncthreads();
+    keep = m.kept;
     __syncthreads();
   }
-  unsigned long long keep = kept;
   if (r.share < 1.0) {
     const unsigned long long p = r.share_of(keep);
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-      if (w[j] && to[j] >= p && to[j] - w[j] < p) kept = to[j];
+      if (to[j] >= p && to[j] - w[j] < p) m.kept = to[j];
     __syncthreads();
-    keep = min(keep, kept);
+    keep = min(keep, m.kept);
+    __syncthreads();
   }
   if (r.least > 0.0) {
+    if (tid == 0) m.kept = m.ends[0];  // before the first bin that may hold the border
     __syncthreads();
-    if (tid == 0) kept = least_before;
-    __syncthreads();
-    unsigned long long m = 0;
+    unsigned long long last = 0;
 #pragma unroll
     for (int j = 0; j < kMine; ++j)
-      if (w[j] && exp_minus(d[j]) >= r.least) m = max(m, to[j]);
-    if (m) atomicMax(&kept, m);
+      if (bin[j] >= 0 && ratio[j] >= r.least) last = max(last, to[j]);
+    if (last) atomicMax(&m.kept, last);
     __syncthreads();
-    keep = min(keep, kept);
+    keep = min(keep, m.kept);
   }
   const unsigned long long p = r.draw(keep);
 #pragma unroll
   for (int j = 0; j < kMine; ++j)
-    if (w[j] && to[j] >= p && to[j] - w[j] < p)
-      give(a, row, (int)~(uint32_t)x[kMine * tid + j], exp_minus(d[j]) * kOne / (double)keep);
+    if (to[j] >= p && to[j] - w[j] < p)
+      give(a, row, (int)~(uint32_t)x[i0 + j], ratio[j] * kOne / (double)keep);
 }
 
 // ---- rows whose gathered tokens are too many
@@ -429,30 +539,37 @@ struct Place {
   unsigned long long sum;
 };
 
+// The weight of a value, or 0.
+__device__ __forceinline__ unsigned long long weight_of(const Row &r, float v, const double *table) {
+  const double d = r.distance(v);
+  return d < 30.0 ? Spot(d, table).weight() : 0ull;
+}
+
 template <int TY, int THREADS>
 __device__ Place descend(const SampleArgs &a, long long row, const Row &r, bool by_count, unsigned long long target,
-                         unsigned long long *sum, uint32_t *count, Place *shared) {
+                         Lds<THREADS> &m, Place *shared) {
   Place p{0u, 0u, 0ull};
   int shift = 32;
   for (int level = 0; level < 3; ++level) {
     const int bits = level < 2 ? 11 : 10, above = shift;
     shift -= bits;
-    for (int i = threadIdx.x; i < kBins; i += THREADS) count[i] = 0u, sum[i] = 0ull;
+    for (int i = threadIdx.x; i < kBins; i += THREADS) m.count[i] = 0u, m.sum[i] = 0ull;
     __syncthreads();
-    each_token<TY, THREADS>(a, row, 0, a.V, [&](uint32_t key, int) {
+    Tokens<TY, THREADS>(a, row, 0, a.V).template each<true>([&](float v, int) {
+      const uint32_t key = order_bits(v);
       if (above < 32 && (key >> above) != (p.key >> above)) return;
-      const unsigned long long w = r.weight(r.distance(key));
+      const unsigned long long w = weight_of(r, v, m.table);
       if (!w) return;
       const int b = key >> shift & ((1 << bits) - 1);
-      atomicAdd(&count[b], 1u);
-      atomicAdd(&sum[b], w);
+      atomicAdd(&m.count[b], 1u);
+      atomicAdd(&m.sum[b], w);
     });
     __syncthreads();
     if (threadIdx.x == 0) {
       int b = (1 << bits) - 1;
       for (; b > 0; --b) {
-        if ((by_count ? p.count + count[b] : p.sum + sum[b]) >= target) break;
-        p.count += count[b], p.sum += sum[b];
+        if ((by_count ? p.count + m.count[b] : p.sum + m.sum[b]) >= target) break;
+        p.count += m.count[b], p.sum += m.sum[b];
       }
       p.key |= (uint32_t)b << shift;
       *shared = p;
@@ -465,133 +582,157 @@ __device__ Place descend(const SampleArgs &a, long long row, const Row &r, bool 
 }
 
 template <int TY, int THREADS>
-__device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &r, unsigned long long total,
-                                 uint32_t tokens, unsigned long long *sum, uint32_t *count) {
+__device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &r, Lds<THREADS> &m,
+                                 unsigned long long total, uint32_t tokens) {
   __shared__ Place shared;
-  __shared__ unsigned long long kept;
-  __shared__ uint32_t part[THREADS / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   unsigned long long keep = total;
   if (r.k > 0 && (uint32_t)r.k < tokens) {
-    const Place p = descend<TY, THREADS>(a, row, r, true, (unsigned long long)r.k, sum, count, &shared);
-    keep = p.sum + (r.k - p.count) * r.weight(r.distance(p.key));
+    const Place p = descend<TY, THREADS>(a, row, r, true, (unsigned long long)r.k, m, &shared);
+    keep = p.sum + (r.k - p.count) * weight_of(r, value_of(p.key), m.table);
   }
   if (r.share < 1.0) {
     const unsigned long long t = r.share_of(keep);
-    const Place p = descend<TY, THREADS>(a, row, r, false, t, sum, count, &shared);
-    const unsigned long long w = r.weight(r.distance(p.key));
+    const Place p = descend<TY, THREADS>(a, row, r, false, t, m, &shared);
+    const unsigned long long w = weight_of(r, value_of(p.key), m.table);
     keep = min(keep, p.sum + (t - p.sum + w - 1) / w * w);
   }
   if (r.least > 0.0) {
-    if (tid == 0) kept = 0ull;
+    if (tid == 0) m.kept = 0ull;
     __syncthreads();
-    unsigned long long m = 0;
-    each_token<TY, THREADS>(a, row, 0, a.V, [&](uint32_t key, int) {
-      const double d = r.distance(key);
-      if (exp_minus(d) >= r.least) m += r.weight(d);
+    unsigned long long sum = 0;
+    Tokens<TY, THREADS>(a, row, 0, a.V).template each<true>([&](float v, int) {
+      const double d = r.distance(v);
+      if (!(d < 30.0)) return;
+      const Spot at(d, m.table);
+      if (at.ratio() >= r.least) sum += at.weight();
     });
-    if (m) atomicAdd(&kept, m);
+    if (sum) atomicAdd(&m.kept, sum);
     __syncthreads();
-    keep = min(keep, kept);
+    keep = min(keep, m.kept);
   }
   const unsigned long long t = r.draw(keep);
-  const Place p = descend<TY, THREADS>(a, row, r, false, t, sum, count, &shared);
-  const unsigned long long w = r.weight(r.distance(p.key));
+  const Place p = descend<TY, THREADS>(a, row, r, false, t, m, &shared);
+  const unsigned long long w = weight_of(r, value_of(p.key), m.table);
   // the nth of the equal ones, by ids
   const uint32_t nth = (uint32_t)((t - 1 - p.sum) / w);
   uint32_t before = 0;
   for (int i0 = 0; i0 < a.V && before <= nth; i0 += THREADS) {
     const int i = i0 + tid;
     const bool hit = i < a.V && order_bits(load1(a.z, TY, row * a.ldz + i)) == p.key;
-    const uint64_t m = __ballot(hit);
-    if (lane == 0) part[wave] = __popcll(m);
+    const uint64_t same = __ballot(hit);
+    if (lane == 0) m.part32[wave] = __popcll(same);
     __syncthreads();
     uint32_t mine = before;
     for (int j = 0; j < THREADS / 64; ++j) {
-      if (j < wave) mine += part[j];
-      before += part[j];
+      if (j < wave) mine += m.part32[j];
+      before += m.part32[j];
     }
-    if (hit && mine + __popcll(m & ((1ull << lane) - 1)) == nth)
-      give(a, row, i, exp_minus(r.distance(p.key)) * kOne / (double)keep);
+    if (hit && mine + __popcll(same & ((1ull << lane) - 1)) == nth)
+      give(a, row, i, Spot(r.distance(value_of(p.key)), m.table).ratio() * kOne / (double)keep);
     __syncthreads();
   }
 }
 
-constexpr int kResolve = 1024;
-
-template <int TY>
-__global__ __launch_bounds__(kResolve) void sample_resolve_kernel(SampleArgs a, int segments) {
-  constexpr int kMine = kBins / kResolve;
-  __shared__ unsigned long long sum[kBins], x[kCap], part64[kResolve / 64], least_before;
-  __shared__ uint32_t count[kBins], part32[kResolve / 64];
-  Space &s = ((Space *)a.ws)[blockIdx.x];
-  const long long row = blockIdx.x;
-  const int tid = threadIdx.x;
-  const unsigned long long first = top_of(s, segments);
-  const Row r(a, row, (uint32_t)(first >> 32));
-  if (!first || r.greedy) {
-    if (tid == 0) give(a, row, first ? (int)~(uint32_t)first : -1, first ? 1.0 : 0.0);
-    return;
-  }
-  uint32_t c[kMine], mine32 = 0, tokens;
-  unsigned long long w[kMine], mine64 = 0, total;
-#pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    c[j] = s.count[kMine * tid + j], w[j] = s.sum[kMine * tid + j], mine32 += c[j], mine64 += w[j];
-  uint32_t c0 = block_before<uint32_t, kResolve>(mine32, part32, tokens);
-  unsigned long long w0 = block_before<unsigned long long, kResolve>(mine64, part64, total);
-  const int n = (int)s.gathered;
-  if (n > kCap) {
-    settle_by_digits<TY, kResolve>(a, row, r, total, tokens, sum, count);
-    return;
-  }
-  const int b0 = r.least > 0.0 ? bin_of(fmin(fmax(-log(r.least) - 1e-9, 0.0), 31.9)) : 0;
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const int b = kMine * tid + j;
-    if (b == b0) least_before = w0;
-    sum[b] = w0, count[b] = c0;
-    w0 += w[j], c0 += c[j];
-  }
-  int size = 128;
-  while (size < n) size *= 2;
-  for (int i = tid; i < size; i += kResolve) x[i] = i < n ? s.near[i] : 0ull;
+// Puts the tokens of the wanted bins into m.token (those past kCap are only counted).
+template <int TY, int THREADS>
+__device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const Row &r, Lds<THREADS> &m) {
+  // the range of values of the wanted bins: most tokens are passed over by it
+  const double far = bin_start((int)m.high + 1) * r.temp, near = bin_start((int)m.low) * r.temp;
+  const double slack = 1e-6 * (fabs(r.top) + far);
+  const float low = (float)(r.top - far - slack), high = (float)(r.top - near + slack);
+  tokens.template each<true>([&](float v, int id) {
+    if (!(v >= low && v <= high)) return;
+    const double d = r.distance(v);
+    if (!(d < 30.0)) return;
+    const Spot at(d, m.table);
+    if (!(m.wanted[at.bin >> 5] >> (at.bin & 31) & 1u) || !at.weight()) return;
+    const uint32_t i = atomicAdd(&m.gathered, 1u);
+    if (i < kCap) m.token[i] = token_of(order_bits(v), id);
+  });
   __syncthreads();
-  sort_falling<kResolve>(x, size);
-  settle<kResolve, true>(a, row, r, x, n, sum, count, total, tokens, least_before);
 }
 
-// Rows of up to kCap tokens: all of them sorted.
-constexpr int kShort = 512;
+template <int TY>
+__global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
+  __shared__ Lds<kScan> m;
+  __shared__ uint32_t base;
+  Space &s = ((Space *)a.ws)[blockIdx.y];
+  int lo, hi;
+  segment(a, lo, hi);
+  const Tokens<TY, kScan> tokens(a, blockIdx.y, lo, hi);
+  Row r(a, blockIdx.y);
+  for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = s.sum[i], m.count[i] = s.count[i];
+  const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
+  fill_table<kScan>(m.table);
+  if (!top || r.greedy) return;
+  r.top = (double)value_of(top);
+  __syncthreads();
+  unsigned long long total;
+  uint32_t all;
+  decide(r, m, total, all);
+  gather(tokens, r, m);
+  const uint32_t n = m.gathered;
+  if (n == 0u) return;
+  if (threadIdx.x == 0) base = atomicAdd(&s.gathered, n);
+  __syncthreads();
+  if (base + n > kCap) return;
+  for (uint32_t i = threadIdx.x; i < n; i += kScan) s.near[base + i] = m.token[i];
+}
 
 template <int TY>
-__global__ __launch_bounds__(kShort) void sample_short_kernel(SampleArgs a, int size) {
-  __shared__ unsigned long long x[kCap], part64[kShort / 64];
-  __shared__ uint32_t part32[kShort / 64];
+__global__ __launch_bounds__(kScan) void sample_finish_kernel(SampleArgs a, int segments) {
+  __shared__ Lds<kScan> m;
+  const Space &s = ((const Space *)a.ws)[blockIdx.x];
   const long long row = blockIdx.x;
-  const int tid = threadIdx.x;
-  for (int i = tid; i < size; i += kShort) {
-    const uint32_t key = i < a.V ? order_bits(load1(a.z, TY, row * a.ldz + i)) : 0u;
-    x[i] = key ? token_of(key, i) : 0ull;
-  }
-  __syncthreads();
-  sort_falling<kShort>(x, size);
-  const unsigned long long first = x[0];
-  const Row r(a, row, (uint32_t)(first >> 32));
+  Row r(a, row);
+  const int n = (int)s.gathered;
+  for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = s.sum[i], m.count[i] = s.count[i];
+  for (int i = threadIdx.x; i < min(n, kCap); i += kScan) m.token[i] = s.near[i];
+  const unsigned long long first = top_of(s, segments);
+  fill_table<kScan>(m.table);
   if (!first || r.greedy) {
-    if (tid == 0) give(a, row, first ? (int)~(uint32_t)first : -1, first ? 1.0 : 0.0);
+    if (threadIdx.x == 0) give(a, row, first ? (int)~(uint32_t)first : -1, first ? 1.0 : 0.0);
     return;
   }
-  uint32_t mine32 = 0, tokens;
-  unsigned long long mine64 = 0, total;
-  for (int i = tid; i < a.V; i += kShort) {
-    const unsigned long long w = r.weight(r.distance((uint32_t)(x[i] >> 32)));
-    mine32 += w != 0, mine64 += w;
-  }
-  (void)block_before<uint32_t, kShort>(mine32, part32, tokens);
-  (void)block_before<unsigned long long, kShort>(mine64, part64, total);
+  r.top = (double)value_of((uint32_t)(first >> 32));
   __syncthreads();
-  settle<kShort, false>(a, row, r, x, a.V, nullptr, nullptr, total, tokens, 0ull);
+  unsigned long long total;
+  uint32_t tokens;
+  decide(r, m, total, tokens);
+  if (n > kCap)
+    settle_by_digits<TY, kScan>(a, row, r, m, total, tokens);
+  else
+    settle(a, row, r, m, n, total, tokens);
+}
+
+template <int TY>
+__global__ __launch_bounds__(kScan) void sample_row_kernel(SampleArgs a) {
+  __shared__ Lds<kScan> m;
+  const long long row = blockIdx.x;
+  const Tokens<TY, kScan> tokens(a, row, 0, a.V);
+  Row r(a, row);
+  for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = 0ull, m.count[i] = 0u;
+  fill_table<kScan>(m.table);
+  First mine;
+  tokens.template each<false>([&](float v, int id) { mine.see(v, id); });
+  const unsigned long long first = block_max<kScan>(mine.token(), m.part);
+  if (!first || r.greedy) {
+    if (threadIdx.x == 0) give(a, row, first ? (int)~(uint32_t)first : -1, first ? 1.0 : 0.0);
+    return;
+  }
+  r.top = (double)value_of((uint32_t)(first >> 32));
+  add_bins<true>(tokens, r, m.sum, m.count, m.table);
+  __syncthreads();
+  unsigned long long total;
+  uint32_t all;
+  decide(r, m, total, all);
+  gather(tokens, r, m);
+  const int n = (int)m.gathered;
+  if (n > kCap)
+    settle_by_digits<TY, kScan>(a, row, r, m, total, all);
+  else
+    settle(a, row, r, m, n, total, all);
 }
 
 int segments_of(int T, int V) {
@@ -603,22 +744,18 @@ int segments_of(int T, int V) {
 
 template <int TY>
 hipError_t launch_type(const SampleArgs &a, hipStream_t s) {
-  if (a.V <= kCap) {
-    int size = 128;
-    while (size < a.V) size *= 2;
-    return launch(sample_short_kernel<TY>, dim3(a.T), dim3(kShort), s, a, size);
-  }
+  if (a.V <= kShortRow) return launch(sample_row_kernel<TY>, dim3(a.T), dim3(kScan), s, a);
   const int n = segments_of(a.T, a.V);
   hipError_t e = launch(sample_tops_kernel<TY>, dim3(n, a.T), dim3(kScan), s, a);
   if (e == hipSuccess) e = launch(sample_bins_kernel<TY>, dim3(n, a.T), dim3(kScan), s, a);
   if (e == hipSuccess) e = launch(sample_gather_kernel<TY>, dim3(n, a.T), dim3(kScan), s, a);
-  if (e == hipSuccess) e = launch(sample_resolve_kernel<TY>, dim3(a.T), dim3(kResolve), s, a, n);
+  if (e == hipSuccess) e = launch(sample_finish_kernel<TY>, dim3(a.T), dim3(kScan), s, a, n);
   return e;
 }
 
 }  // namespace
 
-size_t sample_ws_bytes(int T, int V) { return V <= kCap ? 0 : (size_t)T * sizeof(Space); }
+size_t sample_ws_bytes(int T, int V) { return V <= kShortRow ? 0 : (size_t)T * sizeof(Space); }
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
   return a.type == kF32 ? launch_type<kF32>(a, s) : a.type == kBf16 ? launch_type<kBf16>(a, s) : launch_type<kF16>(a, s);
