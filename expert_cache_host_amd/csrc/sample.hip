@@ -73,15 +73,22 @@ __device__ __forceinline__ void fill_table(double *table) {
   for (int i = threadIdx.x; i < kTable; i += THREADS) table[i] = exp_minus(i * 0.015625) * kOne;
 }
 
-// A distance below 30: its bin, and the two factors of its weight.  Bins are 1/128 of a
-// temperature wide up to 12, then 5/128.
+// Bins are 1/128 of a temperature wide up to a distance of 12, then 5/128: the bin of
+// the t-th 128th.
+__device__ __forceinline__ int bin_of(int t) {
+  return t < 1536 ? t : 1536 + (int)(__umul24(t - 1536, 52429) >> 18);  // (t - 1536) / 5
+}
+// The first distance of a bin.
+__device__ __forceinline__ double bin_start(int b) { return b < 1536 ? b * 0.0078125 : 12.0 + (b - 1536) * 0.0390625; }
+
+// A distance below 30: its bin, and the two factors of its weight.
 struct Spot {
   int bin;
   double whole, part;
   __device__ __forceinline__ Spot(double d, const double *table) {
 #pragma clang fp contract(off)
     const int t = (int)(d * 128.0);
-    bin = t < 1536 ? t : 1536 + (int)(__umul24(t - 1536, 52429) >> 18);  // (t - 1536) / 5
+    bin = bin_of(t);
     const double f = fma((double)(t >> 1), -0.015625, d);
     double p = 1.0 / 720.0;
     p = fma(p, f, -1.0 / 120.0);
@@ -98,9 +105,6 @@ struct Spot {
   }
   __device__ __forceinline__ double ratio() const { return whole * part * (1.0 / kOne); }
 };
-
-// The first distance of a bin.
-__device__ __forceinline__ double bin_start(int b) { return b < 1536 ? b * 0.0078125 : 12.0 + (b - 1536) * 0.0390625; }
 
 // A row's settings and its largest logit.
 struct Row {
@@ -226,9 +230,9 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long v, un
   return v;
 }
 
-// Sum of v over the threads before this one; `total` gets that of all.
+// Sum of v over the threads before this one.
 template <class T, int THREADS>
-__device__ __forceinline__ T block_before(T v, T *part, T &total) {
+__device__ __forceinline__ T block_before(T v, T *part) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   T run = v;
 #pragma unroll
@@ -238,14 +242,8 @@ __device__ __forceinline__ T block_before(T v, T *part, T &total) {
   }
   if (lane == 63) part[wave] = run;
   __syncthreads();
-  T before = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 64; ++i) {
-    if (i < wave) before += part[i];
-    total += part[i];
-  }
-  return before + run - v;
+  for (int i = 0; i < wave; ++i) run += part[i];
+  return run - v;
 }
 
 __device__ __forceinline__ void segment(const SampleArgs &a, int &lo, int &hi) {
@@ -261,14 +259,23 @@ __device__ __forceinline__ void give(const SampleArgs &a, long long row, int tok
 // The workgroup's memory.
 template <int THREADS>
 struct Lds {
-  unsigned long long sum[kBins];   // of a bin, then of the bins before it
+  unsigned long long sum[kBins + 1];   // of a bin; then of the bins before it
   unsigned long long token[kCap], sorted[kCap];
   double table[kTable];
-  uint32_t count[kBins];           // likewise
-  uint32_t wanted[kBins / 32], low, high, gathered;
-  unsigned long long part[THREADS / 64], ends[3], kept;
+  uint32_t count[kBins + 1];           // likewise
+  uint32_t gathered;
+  unsigned long long part[THREADS / 64];
   uint32_t part32[THREADS / 64];
 };
+
+// The last i in [0, n) with below(i), which holds up to some place from 0 on; n <= 2048.
+// Every lane of the wave takes part and gets it.
+template <class F>
+__device__ __forceinline__ int last_below(int n, F below) {
+  const int lane = threadIdx.x & 63;
+  const int base = 32 * max(__popcll(__ballot(32 * lane < n && below(min(32 * lane, n - 1)))) - 1, 0);
+  return base + max(__popcll(__ballot(lane < 32 && base + lane < n && below(min(base + lane, n - 1)))) - 1, 0);
+}
 
 // Adds the tokens to the bins.
 template <bool kSmall, int TY, int THREADS>
@@ -346,71 +353,78 @@ __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
   }
 }
 
+// Which bins are wanted: up to four runs of them.
+struct Wanted {
+  int first[4], last[4];
+  int low = kBins - 1, high = 0;
+  unsigned long long before_least = 0;  // sum before the first bin in which min-p's border can lie
+  __device__ __forceinline__ void add(int i, int from, int to) {
+    first[i] = from, last[i] = to;
+    low = min(low, from), high = max(high, to);
+  }
+  __device__ __forceinline__ bool has(int b) const {
+    bool in = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in |= b >= first[i] && b <= last[i];
+    return in;
+  }
+};
+
 // From the bins' counts and sums (in m; they become those of the bins before each):
-// which bins are wanted, and the range of keys that holds them.
+// which bins are wanted.  Every wave finds them for itself.
 template <int THREADS>
-__device__ void decide(const Row &r, Lds<THREADS> &m, unsigned long long &total, uint32_t &tokens) {
+__device__ Wanted decide(const Row &r, Lds<THREADS> &m) {
   constexpr int kMine = kBins / THREADS;
-  const int tid = threadIdx.x, b0 = kMine * tid;
-  // running counts and sums at the ends of this thread's bins
-  uint32_t c[kMine + 1];
-  unsigned long long w[kMine + 1];
-  c[0] = 0u, w[0] = 0ull;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b0 = kMine * threadIdx.x;
+  uint32_t c[kMine], run32 = 0;
+  unsigned long long w[kMine], run = 0;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) c[j + 1] = c[j] + m.count[b0 + j], w[j + 1] = w[j] + m.sum[b0 + j];
-  if (tid < kBins / 32) m.wanted[tid] = 0u;
-  if (tid == 0) m.low = kBins, m.high = 0u, m.gathered = 0u;
-  const uint32_t before32 = block_before<uint32_t, THREADS>(c[kMine], m.part32, tokens);
-  const unsigned long long before = block_before<unsigned long long, THREADS>(w[kMine], m.part, total);
+  for (int j = 0; j < kMine; ++j) c[j] = run32, w[j] = run, run32 += m.count[b0 + j], run += m.sum[b0 + j];
+  uint32_t up32 = run32;
+  unsigned long long up = run;
 #pragma unroll
-  for (int j = 0; j <= kMine; ++j) c[j] += before32, w[j] += before;
+  for (int off = 1; off < 64; off <<= 1) {
+    const uint32_t o32 = __shfl_up(up32, off, 64);
+    const unsigned long long o = __shfl_up(up, off, 64);
+    if (lane >= off) up32 += o32, up += o;
+  }
+  if (lane == 63) m.part32[wave] = up32, m.part[wave] = up;
+  if (threadIdx.x == 0) m.gathered = 0u;
+  __syncthreads();
+  up32 -= run32, up -= run;
+  for (int i = 0; i < wave; ++i) up32 += m.part32[i], up += m.part[i];
 #pragma unroll
-  for (int j = 0; j < kMine; ++j) m.count[b0 + j] = c[j], m.sum[b0 + j] = w[j];
-  const auto want = [&](int b) {
-    atomicOr(&m.wanted[b >> 5], 1u << (b & 31));
-    atomicMin(&m.low, (uint32_t)b);
-    atomicMax(&m.high, (uint32_t)b);
-  };
+  for (int j = 0; j < kMine; ++j) m.count[b0 + j] = up32 + c[j], m.sum[b0 + j] = up + w[j];
+  if (threadIdx.x == THREADS - 1) m.count[kBins] = up32 + run32, m.sum[kBins] = up + run;
+  __syncthreads();
+  Wanted wanted;
+  // the bin of a position in the running sums
+  const auto bin_at = [&](unsigned long long to) { return last_below(kBins, [&](int b) { return m.sum[b] < to; }); };
   // what is kept lies in [lo, hi]
-  unsigned long long lo = total, hi = total;
-  if (r.k > 0 && (uint32_t)r.k < tokens) {
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (c[j] < (uint32_t)r.k && (uint32_t)r.k <= c[j + 1]) want(b0 + j), m.ends[0] = w[j], m.ends[1] = w[j + 1];
-    __syncthreads();
-    lo = max(m.ends[0], 1ull), hi = m.ends[1];
+  unsigned long long lo = m.sum[kBins], hi = lo;
+  wanted.first[0] = wanted.first[1] = wanted.first[2] = kBins;
+  wanted.last[0] = wanted.last[1] = wanted.last[2] = -1;
+  if (r.k > 0 && (uint32_t)r.k < m.count[kBins]) {
+    const int b = last_below(kBins, [&](int b) { return m.count[b] < (uint32_t)r.k; });
+    wanted.add(0, b, b);
+    lo = max(m.sum[b], 1ull), hi = m.sum[b + 1];
   }
   if (r.share < 1.0) {
     const unsigned long long from = r.share_of(lo), to = r.share_of(hi);
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      if (w[j] < to && w[j + 1] >= from) want(b0 + j);
-      if (w[j] < to && w[j + 1] >= to) m.ends[2] = w[j + 1];
-    }
-    __syncthreads();
-    lo = min(lo, from), hi = min(hi, m.ends[2]);
+    const int b = bin_at(from), e = bin_at(to);
+    wanted.add(1, b, e);
+    lo = min(lo, from), hi = min(hi, m.sum[e + 1]);
   }
   if (r.least > 0.0) {
-    // the border's distance, and the bins on either side of what rounding may make of it
-    const double d = -log(r.least);
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const double first = bin_start(b0 + j), last = bin_start(b0 + j + 1);
-      if (d > last + 1e-9 || d < first - 1e-9) continue;
-      want(b0 + j);
-      if (d >= first + 1e-9 || b0 + j == 0) m.ends[0] = w[j];
-      if (d < last - 1e-9) m.ends[1] = w[j + 1];
-    }
-    if (tid == 0 && d > 29.99) m.ends[0] = m.ends[1] = total;  // past every token
-    __syncthreads();
-    lo = min(lo, max(m.ends[0], 1ull)), hi = min(hi, m.ends[1]);
+    // the border lies between two entries of the table, or within rounding of them
+    const int i = last_below(kTable, [&](int i) { return m.table[i] >= r.least * kOne; });
+    const int b = bin_of(max(2 * i - 1, 0)), e = bin_of(2 * i + 2);
+    wanted.add(2, b, e);
+    wanted.before_least = m.sum[b];
+    lo = min(lo, max(m.sum[b], 1ull)), hi = min(hi, m.sum[e + 1]);
   }
-  const unsigned long long from = r.draw(lo), to = r.draw(hi);
-#pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    if (w[j] < to && w[j + 1] >= from) want(b0 + j);
-  __syncthreads();
+  wanted.add(3, bin_at(r.draw(lo)), bin_at(r.draw(hi)));
+  return wanted;
 }
 
 // Sorts n (a power of two, at least 128) numbers in LDS, the largest first.  A pair's
@@ -458,76 +472,59 @@ __device__ const unsigned long long *sorted(Lds<THREADS> &m, int n) {
   return m.token;
 }
 
-// The row's token from its n gathered tokens.  total and tokens are the row's.
+// The row's token from its n gathered tokens.
 template <int THREADS>
 __device__ void settle(const SampleArgs &a, long long row, const Row &r, Lds<THREADS> &m, int n,
-                       unsigned long long total, uint32_t tokens) {
+                       unsigned long long before_least) {
   constexpr int kMine = kCap / THREADS;
-  const int tid = threadIdx.x, i0 = kMine * tid;
+  const int lane = threadIdx.x & 63, i0 = kMine * threadIdx.x;
   const unsigned long long *x = sorted(m, n);
+  // running sums up to each token, in the array that x is not
+  unsigned long long *to = x == m.token ? m.sorted : m.token;
+  const auto spot = [&](int i) { return Spot(r.distance(value_of((uint32_t)(x[i] >> 32))), m.table); };
   int bin[kMine];
-  double ratio[kMine];
-  unsigned long long w[kMine], to[kMine], sum = 0, all;
+  unsigned long long w[kMine], sum = 0;
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    bin[j] = -1, ratio[j] = 0.0, w[j] = 0ull;
+    bin[j] = -1, w[j] = 0ull;
     if (i0 + j < n) {
-      const Spot at(r.distance(value_of((uint32_t)(x[i0 + j] >> 32))), m.table);
-      bin[j] = at.bin, ratio[j] = at.ratio(), w[j] = at.weight();
+      const Spot at = spot(i0 + j);
+      bin[j] = at.bin, w[j] = at.weight();
     }
     sum += w[j];
   }
-  unsigned long long before = block_before<unsigned long long, THREADS>(sum, m.part, all);
+  const int last_bin = i0 > 0 && i0 < n ? spot(i0 - 1).bin : -1;
+  unsigned long long run = block_before<unsigned long long, THREADS>(sum, m.part);
   // a bin's first gathered token: what its tokens' sums and places are off by
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    if (bin[j] >= 0) {
-      const int last = i0 + j == 0 ? -1
-                       : j > 0     ? bin[j - 1]
-                                   : Spot(r.distance(value_of((uint32_t)(x[i0 - 1] >> 32))), m.table).bin;
-      if (last != bin[j]) m.sum[bin[j]] -= before, m.count[bin[j]] -= (uint32_t)(i0 + j);
-    }
-    before += w[j], to[j] = before;
+    if (bin[j] >= 0 && bin[j] != (j > 0 ? bin[j - 1] : last_bin))
+      m.sum[bin[j]] -= run, m.count[bin[j]] -= (uint32_t)(i0 + j);
+    run += w[j];
   }
-  if (tid == 0) m.kept = total;
   __syncthreads();
+  run -= sum;
 #pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    if (bin[j] >= 0) to[j] += m.sum[bin[j]];
-  unsigned long long keep = total;
-  if (r.k > 0 && (uint32_t)r.k < tokens) {
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (bin[j] >= 0 && (uint32_t)(i0 + j) + m.count[bin[j]] == (uint32_t)r.k - 1) m.kept = to[j];
-    __syncthreads();
-    keep = m.kept;
-    __syncthreads();
+  for (int j = 0; j < kMine; ++j) {
+    run += w[j];
+    if (i0 + j < n) to[i0 + j] = run + m.sum[bin[j]];
   }
-  if (r.share < 1.0) {
-    const unsigned long long p = r.share_of(keep);
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (to[j] >= p && to[j] - w[j] < p) m.kept = to[j];
-    __syncthreads();
-    keep = min(keep, m.kept);
-    __syncthreads();
-  }
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  // the first token whose running sum reaches a position
+  const auto token_at = [&](unsigned long long p) {
+    return n - 1 - last_below(n, [&](int i) { return to[n - 1 - i] >= p; });
+  };
+  unsigned long long keep = m.sum[kBins];
+  if (r.k > 0 && (uint32_t)r.k < m.count[kBins])
+    keep = to[last_below(n, [&](int i) { return (uint32_t)i + m.count[spot(i).bin] < (uint32_t)r.k; })];
+  if (r.share < 1.0) keep = min(keep, to[token_at(r.share_of(keep))]);
   if (r.least > 0.0) {
-    if (tid == 0) m.kept = m.ends[0];  // before the first bin that may hold the border
-    __syncthreads();
-    unsigned long long last = 0;
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-      if (bin[j] >= 0 && ratio[j] >= r.least) last = max(last, to[j]);
-    if (last) atomicMax(&m.kept, last);
-    __syncthreads();
-    keep = min(keep, m.kept);
+    const int i = last_below(n, [&](int i) { return spot(i).ratio() >= r.least; });
+    keep = min(keep, spot(i).ratio() >= r.least ? max(before_least, to[i]) : before_least);
   }
-  const unsigned long long p = r.draw(keep);
-#pragma unroll
-  for (int j = 0; j < kMine; ++j)
-    if (to[j] >= p && to[j] - w[j] < p)
-      give(a, row, (int)~(uint32_t)x[i0 + j], ratio[j] * kOne / (double)keep);
+  const int i = token_at(r.draw(keep));
+  if (lane == 0) give(a, row, (int)~(uint32_t)x[i], spot(i).ratio() * kOne / (double)keep);
 }
 
 // ---- rows whose gathered tokens are too many
@@ -582,11 +579,13 @@ __device__ Place descend(const SampleArgs &a, long long row, const Row &r, bool 
 }
 
 template <int TY, int THREADS>
-__device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &r, Lds<THREADS> &m,
-                                 unsigned long long total, uint32_t tokens) {
+__device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &r, Lds<THREADS> &m) {
   __shared__ Place shared;
+  __shared__ unsigned long long kept;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  unsigned long long keep = total;
+  unsigned long long keep = m.sum[kBins];
+  const uint32_t tokens = m.count[kBins];
+  __syncthreads();
   if (r.k > 0 && (uint32_t)r.k < tokens) {
     const Place p = descend<TY, THREADS>(a, row, r, true, (unsigned long long)r.k, m, &shared);
     keep = p.sum + (r.k - p.count) * weight_of(r, value_of(p.key), m.table);
@@ -598,7 +597,7 @@ __device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &
     keep = min(keep, p.sum + (t - p.sum + w - 1) / w * w);
   }
   if (r.least > 0.0) {
-    if (tid == 0) m.kept = 0ull;
+    if (tid == 0) kept = 0ull;
     __syncthreads();
     unsigned long long sum = 0;
     Tokens<TY, THREADS>(a, row, 0, a.V).template each<true>([&](float v, int) {
@@ -607,9 +606,9 @@ __device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &
       const Spot at(d, m.table);
       if (at.ratio() >= r.least) sum += at.weight();
     });
-    if (sum) atomicAdd(&m.kept, sum);
+    if (sum) atomicAdd(&kept, sum);
     __syncthreads();
-    keep = min(keep, m.kept);
+    keep = min(keep, kept);
   }
   const unsigned long long t = r.draw(keep);
   const Place p = descend<TY, THREADS>(a, row, r, false, t, m, &shared);
@@ -636,9 +635,10 @@ __device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &
 
 // Puts the tokens of the wanted bins into m.token (those past kCap are only counted).
 template <int TY, int THREADS>
-__device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const Row &r, Lds<THREADS> &m) {
+__device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const Row &r, const Wanted &wanted,
+                                       Lds<THREADS> &m) {
   // the range of values of the wanted bins: most tokens are passed over by it
-  const double far = bin_start((int)m.high + 1) * r.temp, near = bin_start((int)m.low) * r.temp;
+  const double far = bin_start(wanted.high + 1) * r.temp, near = bin_start(wanted.low) * r.temp;
   const double slack = 1e-6 * (fabs(r.top) + far);
   const float low = (float)(r.top - far - slack), high = (float)(r.top - near + slack);
   tokens.template each<true>([&](float v, int id) {
@@ -646,7 +646,7 @@ __device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const 
     const double d = r.distance(v);
     if (!(d < 30.0)) return;
     const Spot at(d, m.table);
-    if (!(m.wanted[at.bin >> 5] >> (at.bin & 31) & 1u) || !at.weight()) return;
+    if (!wanted.has(at.bin) || !at.weight()) return;
     const uint32_t i = atomicAdd(&m.gathered, 1u);
     if (i < kCap) m.token[i] = token_of(order_bits(v), id);
   });
@@ -668,10 +668,7 @@ __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
   if (!top || r.greedy) return;
   r.top = (double)value_of(top);
   __syncthreads();
-  unsigned long long total;
-  uint32_t all;
-  decide(r, m, total, all);
-  gather(tokens, r, m);
+  gather(tokens, r, decide(r, m), m);
   const uint32_t n = m.gathered;
   if (n == 0u) return;
   if (threadIdx.x == 0) base = atomicAdd(&s.gathered, n);
@@ -697,13 +694,11 @@ __global__ __launch_bounds__(kScan) void sample_finish_kernel(SampleArgs a, int 
   }
   r.top = (double)value_of((uint32_t)(first >> 32));
   __syncthreads();
-  unsigned long long total;
-  uint32_t tokens;
-  decide(r, m, total, tokens);
+  const Wanted wanted = decide(r, m);
   if (n > kCap)
-    settle_by_digits<TY, kScan>(a, row, r, m, total, tokens);
+    settle_by_digits<TY, kScan>(a, row, r, m);
   else
-    settle(a, row, r, m, n, total, tokens);
+    settle(a, row, r, m, n, wanted.before_least);
 }
 
 template <int TY>
@@ -724,15 +719,13 @@ __global__ __launch_bounds__(kScan) void sample_row_kernel(SampleArgs a) {
   r.top = (double)value_of((uint32_t)(first >> 32));
   add_bins<true>(tokens, r, m.sum, m.count, m.table);
   __syncthreads();
-  unsigned long long total;
-  uint32_t all;
-  decide(r, m, total, all);
-  gather(tokens, r, m);
+  const Wanted wanted = decide(r, m);
+  gather(tokens, r, wanted, m);
   const int n = (int)m.gathered;
   if (n > kCap)
-    settle_by_digits<TY, kScan>(a, row, r, m, total, all);
+    settle_by_digits<TY, kScan>(a, row, r, m);
   else
-    settle(a, row, r, m, n, total, all);
+    settle(a, row, r, m, n, wanted.before_least);
 }
 
 int segments_of(int T, int V) {
