@@ -62,9 +62,13 @@ __device__ __forceinline__ double exp_minus(double d) {
   return __builtin_bit_cast(double, __builtin_bit_cast(int64_t, p) - ((int64_t)(int)n << 52));
 }
 
+// Distances from the largest logit count in 128ths of a temperature; weights are 0 from
+// kFar on (30 temperatures).
+constexpr double kFar = 3840.0;
+
 // 2^42 exp(-i / 64), made by every workgroup: with it a weight takes a polynomial of
 // degree 6 (the terms left out are below 2^-54).
-constexpr int kTable = 1920;     // distances up to 30
+constexpr int kTable = 1920;
 constexpr double kOne = 4398046511104.0;  // 2^42: the largest token's weight
 
 template <int THREADS>
@@ -73,29 +77,27 @@ __device__ __forceinline__ void fill_table(double *table) {
   for (int i = threadIdx.x; i < kTable; i += THREADS) table[i] = exp_minus(i * 0.015625) * kOne;
 }
 
-// Bins are 1/128 of a temperature wide up to a distance of 12, then 5/128: the bin of
-// the t-th 128th.
-__device__ __forceinline__ int bin_of(int t) {
-  return t < 1536 ? t : 1536 + (int)(__umul24(t - 1536, 52429) >> 18);  // (t - 1536) / 5
-}
+// The bin of the t-th 128th: bins are 1/128 of a temperature wide up to 10, then 1/32.
+__device__ __forceinline__ int bin_of(int t) { return min(t, 960 + (t >> 2)); }
 // The first distance of a bin.
-__device__ __forceinline__ double bin_start(int b) { return b < 1536 ? b * 0.0078125 : 12.0 + (b - 1536) * 0.0390625; }
+__device__ __forceinline__ double bin_start(int b) { return b < 1280 ? b : 4 * (b - 960); }
 
-// A distance below 30: its bin, and the two factors of its weight.
+// A distance below kFar: its bin, and the two factors of its weight.
 struct Spot {
   int bin;
   double whole, part;
   __device__ __forceinline__ Spot(double d, const double *table) {
 #pragma clang fp contract(off)
-    const int t = (int)(d * 128.0);
+    const int t = (int)d;
     bin = bin_of(t);
-    const double f = fma((double)(t >> 1), -0.015625, d);
-    double p = 1.0 / 720.0;
-    p = fma(p, f, -1.0 / 120.0);
-    p = fma(p, f, 1.0 / 24.0);
-    p = fma(p, f, -1.0 / 6.0);
-    p = fma(p, f, 0.5);
-    p = fma(p, f, -1.0);
+    const double f = d - (double)(t & ~1);
+    // exp(-f / 128)
+    double p = 1.0 / (720.0 * 4398046511104.0);
+    p = fma(p, f, -1.0 / (120.0 * 34359738368.0));
+    p = fma(p, f, 1.0 / (24.0 * 268435456.0));
+    p = fma(p, f, -1.0 / (6.0 * 2097152.0));
+    p = fma(p, f, 0.5 / 16384.0);
+    p = fma(p, f, -1.0 / 128.0);
     part = fma(p, f, 1.0);
     whole = table[t >> 1];
   }
@@ -108,12 +110,12 @@ struct Spot {
 
 // A row's settings and its largest logit.
 struct Row {
-  double top, temp, inv;     // largest logit, temperature and its inverse
+  double top, temp, inv;     // largest logit, a 128th of the temperature and its inverse
   double share, least, u;    // top-p (1: all), min-p (0: all), the random number
   int k;                     // top-k (0: all)
   bool greedy;
   __device__ __forceinline__ Row(const SampleArgs &a, long long row) {
-    temp = a.temperatures ? (double)a.temperatures[row] : a.temperature;
+    temp = (a.temperatures ? (double)a.temperatures[row] : a.temperature) * 0.0078125;
     greedy = !(temp > 0.0);
     inv = greedy ? 1.0 : 1.0 / temp;
     const double p = a.top_ps ? (double)a.top_ps[row] : a.top_p;
@@ -124,8 +126,7 @@ struct Row {
     const double v = (double)a.u[row];
     u = v >= 0.0 ? fmin(v, 1.0) : 0.0;
   }
-  // how far below the largest, in temperatures; weights are 0 from 30 on
-  // (minus infinity and NaN: not below 30)
+  // how far below the largest (minus infinity and NaN: not below kFar)
   __device__ __forceinline__ double distance(float v) const {
 #pragma clang fp contract(off)
     return (top - (double)v) * inv;
@@ -182,10 +183,11 @@ struct Tokens {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) first[j] = load(lo + 4 * ((int)threadIdx.x + THREADS * j));
   }
-  // Calls f(value, id) for each; plus infinity comes as the largest float, places past
-  // the end as minus infinity.
+  // Calls f(value, id) for each (kSmall: each in [low, high]); plus infinity comes as the
+  // largest float, places past the end as minus infinity.
   template <bool kSmall, class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void each(F f, float low = -3.40282347e38f, float high = __builtin_inff()) const {
+    const auto inside = [&](float v) { return v >= low && v <= high; };
     float4 v0 = first[0], v1 = first[1];
     const auto one = [&](float v, int i) { f(v > 3.40282347e38f ? 3.40282347e38f : v, i); };
 #pragma unroll 1
@@ -193,10 +195,11 @@ struct Tokens {
       const float4 v = v0;
       v0 = v1, v1 = load(i + 4 * THREADS * kAhead);
       if constexpr (kSmall) {
+        if (!(inside(v.x) || inside(v.y) || inside(v.z) || inside(v.w))) continue;
         float x = v.x, y = v.y, z = v.z;
 #pragma unroll 1
         for (int e = 0; e < 4; ++e) {
-          one(x, i + e);
+          if (inside(x)) one(x, i + e);
           x = y, y = z, z = v.w;
         }
       } else {
@@ -284,12 +287,11 @@ __device__ __forceinline__ void add_bins(const Tokens<TY, THREADS> &tokens, cons
   const bool counts = r.k > 0;  // (looked at for top-k alone)
   tokens.template each<kSmall>([&](float v, int) {
     const double d = r.distance(v);
-    if (!(d < 30.0)) return;
+    if (!(d < kFar)) return;
     const Spot at(d, table);
     const unsigned long long w = at.weight();
-    if (!w) return;
     atomicAdd(&sum[at.bin], w);
-    if (counts) atomicAdd(&count[at.bin], 1u);
+    if (counts && w) atomicAdd(&count[at.bin], 1u);
   });
 }
 
@@ -539,7 +541,7 @@ struct Place {
 // The weight of a value, or 0.
 __device__ __forceinline__ unsigned long long weight_of(const Row &r, float v, const double *table) {
   const double d = r.distance(v);
-  return d < 30.0 ? Spot(d, table).weight() : 0ull;
+  return d < kFar ? Spot(d, table).weight() : 0ull;
 }
 
 template <int TY, int THREADS>
@@ -602,7 +604,7 @@ __device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &
     unsigned long long sum = 0;
     Tokens<TY, THREADS>(a, row, 0, a.V).template each<true>([&](float v, int) {
       const double d = r.distance(v);
-      if (!(d < 30.0)) return;
+      if (!(d < kFar)) return;
       const Spot at(d, m.table);
       if (at.ratio() >= r.least) sum += at.weight();
     });
@@ -640,16 +642,16 @@ __device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const 
   // the range of values of the wanted bins: most tokens are passed over by it
   const double far = bin_start(wanted.high + 1) * r.temp, near = bin_start(wanted.low) * r.temp;
   const double slack = 1e-6 * (fabs(r.top) + far);
-  const float low = (float)(r.top - far - slack), high = (float)(r.top - near + slack);
+  const float low = fmaxf((float)(r.top - far - slack), -3.40282347e38f);
+  const float high = r.top - near + slack < 3.4e38 ? (float)(r.top - near + slack) : __builtin_inff();
   tokens.template each<true>([&](float v, int id) {
-    if (!(v >= low && v <= high)) return;
     const double d = r.distance(v);
-    if (!(d < 30.0)) return;
+    if (!(d < kFar)) return;
     const Spot at(d, m.table);
     if (!wanted.has(at.bin) || !at.weight()) return;
     const uint32_t i = atomicAdd(&m.gathered, 1u);
     if (i < kCap) m.token[i] = token_of(order_bits(v), id);
-  });
+  }, low, high);
   __syncthreads();
 }
 
