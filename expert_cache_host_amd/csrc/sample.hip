@@ -166,6 +166,10 @@ struct Tokens {
   const SampleArgs &a;
   long long at;
   int lo, hi;
+  template <bool kSmall, class F>
+  __device__ __forceinline__ void each(F f) const {
+    each<kSmall>(f, [](float v) { return v >= -3.40282347e38f; });
+  }
   __device__ __forceinline__ float4 load(int i) const {
     if (i + 3 < hi) return load4(a.z, TY, at + i);
     const float none = -__builtin_inff();
@@ -183,11 +187,10 @@ struct Tokens {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) first[j] = load(lo + 4 * ((int)threadIdx.x + THREADS * j));
   }
-  // Calls f(value, id) for each (kSmall: each in [low, high]); plus infinity comes as the
-  // largest float, places past the end as minus infinity.
-  template <bool kSmall, class F>
-  __device__ __forceinline__ void each(F f, float low = -3.40282347e38f, float high = __builtin_inff()) const {
-    const auto inside = [&](float v) { return v >= low && v <= high; };
+  // Calls f(value, id) for each (kSmall: each that is `inside`); plus infinity comes as
+  // the largest float, places past the end as minus infinity.
+  template <bool kSmall, class F, class I>
+  __device__ __forceinline__ void each(F f, I inside) const {
     float4 v0 = first[0], v1 = first[1];
     const auto one = [&](float v, int i) { f(v > 3.40282347e38f ? 3.40282347e38f : v, i); };
 #pragma unroll 1
@@ -358,11 +361,9 @@ __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
 // Which bins are wanted: up to four runs of them.
 struct Wanted {
   int first[4], last[4];
-  int low = kBins - 1, high = 0;
   unsigned long long before_least = 0;  // sum before the first bin in which min-p's border can lie
   __device__ __forceinline__ void add(int i, int from, int to) {
     first[i] = from, last[i] = to;
-    low = min(low, from), high = max(high, to);
   }
   __device__ __forceinline__ bool has(int b) const {
     bool in = false;
@@ -635,24 +636,56 @@ __device__ void settle_by_digits(const SampleArgs &a, long long row, const Row &
   }
 }
 
+// A run of bins as a range of values, a little wider.
+struct Range {
+  bool on;
+  float low, high;
+  __device__ __forceinline__ Range(const Row &r, int first, int last) {
+    const double far = bin_start(last + 1) * r.temp, near = bin_start(first) * r.temp;
+    const double slack = 1e-6 * (fabs(r.top) + far);
+    const float h = r.top - near + slack < 3.4e38 ? (float)(r.top - near + slack) : __builtin_inff();
+    on = __builtin_amdgcn_readfirstlane(first <= last);
+    low = __int_as_float(__builtin_amdgcn_readfirstlane(
+        __float_as_int(fmaxf((float)(r.top - far - slack), -3.40282347e38f))));
+    high = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(h)));
+  }
+  __device__ __forceinline__ bool has(float v) const { return v >= low && v <= high; }
+};
+
 // Puts the tokens of the wanted bins into m.token (those past kCap are only counted).
 template <int TY, int THREADS>
 __device__ __forceinline__ void gather(const Tokens<TY, THREADS> &tokens, const Row &r, const Wanted &wanted,
                                        Lds<THREADS> &m) {
-  // the range of values of the wanted bins: most tokens are passed over by it
-  const double far = bin_start(wanted.high + 1) * r.temp, near = bin_start(wanted.low) * r.temp;
-  const double slack = 1e-6 * (fabs(r.top) + far);
-  const float low = fmaxf((float)(r.top - far - slack), -3.40282347e38f);
-  const float high = r.top - near + slack < 3.4e38 ? (float)(r.top - near + slack) : __builtin_inff();
-  tokens.template each<true>([&](float v, int id) {
-    const double d = r.distance(v);
-    if (!(d < kFar)) return;
-    const Spot at(d, m.table);
-    if (!wanted.has(at.bin) || !at.weight()) return;
-    const uint32_t i = atomicAdd(&m.gathered, 1u);
-    if (i < kCap) m.token[i] = token_of(order_bits(v), id);
-  }, low, high);
+  // most tokens are passed over by their values
+  const Range a0(r, wanted.first[0], wanted.last[0]), a1(r, wanted.first[1], wanted.last[1]),
+      a2(r, wanted.first[2], wanted.last[2]), a3(r, wanted.first[3], wanted.last[3]);
+  tokens.template each<true>(
+      [&](float v, int id) {
+        const double d = r.distance(v);
+        if (!(d < kFar)) return;
+        const Spot at(d, m.table);
+        if (!wanted.has(at.bin) || !at.weight()) return;
+        const uint32_t i = atomicAdd(&m.gathered, 1u);
+        if (i < kCap) m.token[i] = token_of(order_bits(v), id);
+      },
+      [&](float v) {
+        bool in = a3.has(v);
+        if (a0.on) in |= a0.has(v);
+        if (a1.on) in |= a1.has(v);
+        if (a2.on) in |= a2.has(v);
+        return in;
+      });
   __syncthreads();
+}
+
+// The row's token once m holds the bins before each bin and n gathered tokens.
+template <int TY>
+__device__ __forceinline__ void finish(const SampleArgs &a, long long row, const Row &r, const Wanted &wanted,
+                                       Lds<kScan> &m, uint32_t n) {
+  if (n > kCap)
+    settle_by_digits<TY, kScan>(a, row, r, m);
+  else
+    settle(a, row, r, m, (int)n, wanted.before_least);
 }
 
 template <int TY>
@@ -679,15 +712,17 @@ __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
   for (uint32_t i = threadIdx.x; i < n; i += kScan) s.near[base + i] = m.token[i];
 }
 
+// (Done by the gathering's last workgroup instead, a launch less, the fences that make
+// its tokens visible across the dies took far more: 89 for 42 us at 32 x 131072.)
 template <int TY>
 __global__ __launch_bounds__(kScan) void sample_finish_kernel(SampleArgs a, int segments) {
   __shared__ Lds<kScan> m;
   const Space &s = ((const Space *)a.ws)[blockIdx.x];
   const long long row = blockIdx.x;
   Row r(a, row);
-  const int n = (int)s.gathered;
+  const uint32_t n = s.gathered;
   for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = s.sum[i], m.count[i] = s.count[i];
-  for (int i = threadIdx.x; i < min(n, kCap); i += kScan) m.token[i] = s.near[i];
+  for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kCap); i += kScan) m.token[i] = s.near[i];
   const unsigned long long first = top_of(s, segments);
   fill_table<kScan>(m.table);
   if (!first || r.greedy) {
@@ -697,10 +732,7 @@ __global__ __launch_bounds__(kScan) void sample_finish_kernel(SampleArgs a, int 
   r.top = (double)value_of((uint32_t)(first >> 32));
   __syncthreads();
   const Wanted wanted = decide(r, m);
-  if (n > kCap)
-    settle_by_digits<TY, kScan>(a, row, r, m);
-  else
-    settle(a, row, r, m, n, wanted.before_least);
+  finish<TY>(a, row, r, wanted, m, n);
 }
 
 template <int TY>
@@ -723,11 +755,7 @@ __global__ __launch_bounds__(kScan) void sample_row_kernel(SampleArgs a) {
   __syncthreads();
   const Wanted wanted = decide(r, m);
   gather(tokens, r, wanted, m);
-  const int n = (int)m.gathered;
-  if (n > kCap)
-    settle_by_digits<TY, kScan>(a, row, r, m);
-  else
-    settle(a, row, r, m, n, wanted.before_least);
+  finish<TY>(a, row, r, wanted, m, m.gathered);
 }
 
 int segments_of(int T, int V) {
