@@ -21,6 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kCap = 2048;        // tokens sorted in LDS
+constexpr int kFew = 256;         // of which so many by counting
 constexpr int kBins = 2048;
 constexpr int kMaxSegments = 128;
 constexpr int kScan = 512;        // threads of a workgroup
@@ -66,40 +67,51 @@ __device__ __forceinline__ double exp_minus(double d) {
 // kFar on (30 temperatures).
 constexpr double kFar = 3840.0;
 
-// 2^42 exp(-i / 64), made by every workgroup: with it a weight takes a polynomial of
-// degree 6 (the terms left out are below 2^-54).
-constexpr int kTable = 1920;
+// 2^42 exp(-i / 4) and exp(-i / 128), made by every workgroup: with them a weight takes
+// a polynomial of degree 5 (the terms left out are below 2^-57).
+constexpr int kPlaces = 3841;             // 128ths up to kFar
 constexpr double kOne = 4398046511104.0;  // 2^42: the largest token's weight
+struct Table {
+  double quarter[kPlaces / 32 + 1], part[32];
+  __device__ __forceinline__ double at(int t) const {
+#pragma clang fp contract(off)
+    return quarter[t >> 5] * part[t & 31];
+  }
+  // (the workgroup meets before it is used)
+  __device__ __forceinline__ void fill() {
+    const int i = threadIdx.x;
+    if (i < 32)
+      part[i] = exp_minus(i * 0.0078125);
+    else if (i - 32 <= kPlaces / 32)
+      quarter[i - 32] = exp_minus((i - 32) * 0.25) * kOne;
+  }
+};
 
-template <int THREADS>
-__device__ __forceinline__ void fill_table(double *table) {
-#pragma unroll 1
-  for (int i = threadIdx.x; i < kTable; i += THREADS) table[i] = exp_minus(i * 0.015625) * kOne;
-}
-
-// The bin of the t-th 128th: bins are 1/128 of a temperature wide up to 10, then 1/32.
+// The bin of the tokens nearest to distance t: bins are 1/128 of a temperature wide up to
+// 10, then 1/32.
 __device__ __forceinline__ int bin_of(int t) { return min(t, 960 + (t >> 2)); }
-// The first distance of a bin.
-__device__ __forceinline__ double bin_start(int b) { return b < 1280 ? b : 4 * (b - 960); }
+// Where a bin starts.
+__device__ __forceinline__ double bin_start(int b) { return (b < 1280 ? b : 4 * (b - 960)) - 0.5; }
 
 // A distance below kFar: its bin, and the two factors of its weight.
 struct Spot {
   int bin;
   double whole, part;
-  __device__ __forceinline__ Spot(double d, const double *table) {
+  __device__ __forceinline__ Spot(double d, const Table &table) {
 #pragma clang fp contract(off)
-    const int t = (int)d;
+    // the sum with 1.5 * 2^52 rounds to a whole number, which its low bits are
+    const double u = d + 6755399441055744.0;
+    const int t = (int)(uint32_t)__builtin_bit_cast(uint64_t, u);
     bin = bin_of(t);
-    const double f = d - (double)(t & ~1);
+    const double f = d - (u - 6755399441055744.0);
     // exp(-f / 128)
-    double p = 1.0 / (720.0 * 4398046511104.0);
-    p = fma(p, f, -1.0 / (120.0 * 34359738368.0));
+    double p = -1.0 / (120.0 * 34359738368.0);
     p = fma(p, f, 1.0 / (24.0 * 268435456.0));
     p = fma(p, f, -1.0 / (6.0 * 2097152.0));
     p = fma(p, f, 0.5 / 16384.0);
     p = fma(p, f, -1.0 / 128.0);
     part = fma(p, f, 1.0);
-    whole = table[t >> 1];
+    whole = table.at(t);
   }
   // rounded to a whole number by the sum with 2^52
   __device__ __forceinline__ unsigned long long weight() const {
@@ -266,8 +278,8 @@ __device__ __forceinline__ void give(const SampleArgs &a, long long row, int tok
 template <int THREADS>
 struct Lds {
   unsigned long long sum[kBins + 1];   // of a bin; then of the bins before it
-  unsigned long long token[kCap], sorted[kCap];
-  double table[kTable];
+  unsigned long long token[kCap], sorted[kFew];
+  Table table;
   uint32_t count[kBins + 1];           // likewise
   uint32_t gathered;
   unsigned long long part[THREADS / 64];
@@ -286,12 +298,11 @@ __device__ __forceinline__ int last_below(int n, F below) {
 // Adds the tokens to the bins.
 template <bool kSmall, int TY, int THREADS>
 __device__ __forceinline__ void add_bins(const Tokens<TY, THREADS> &tokens, const Row &r,
-                                         unsigned long long *sum, uint32_t *count, const double *table) {
+                                         unsigned long long *sum, uint32_t *count, const Table &table) {
   const bool counts = r.k > 0;  // (looked at for top-k alone)
   tokens.template each<kSmall>([&](float v, int) {
-    const double d = r.distance(v);
-    if (!(d < kFar)) return;
-    const Spot at(d, table);
+    // (tokens of weight 0 add nothing to a bin behind all others: no branch)
+    const Spot at(fmin(r.distance(v), kFar), table);
     const unsigned long long w = at.weight();
     atomicAdd(&sum[at.bin], w);
     if (counts && w) atomicAdd(&count[at.bin], 1u);
@@ -338,7 +349,7 @@ template <int TY>
 __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
   __shared__ unsigned long long sum[kBins];
   __shared__ uint32_t count[kBins];
-  __shared__ double table[kTable];
+  __shared__ Table table;
   Space &s = ((Space *)a.ws)[blockIdx.y];
   int lo, hi;
   segment(a, lo, hi);
@@ -346,7 +357,7 @@ __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
   Row r(a, blockIdx.y);
   const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
   for (int i = threadIdx.x; i < kBins; i += kScan) sum[i] = 0ull, count[i] = 0u;
-  fill_table<kScan>(table);
+  table.fill();
   if (!top || r.greedy) return;
   r.top = (double)value_of(top);
   __syncthreads();
@@ -356,6 +367,12 @@ __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
     if (sum[i]) atomicAdd(&s.sum[i], sum[i]);
     if (count[i]) atomicAdd(&s.count[i], count[i]);
   }
+}
+
+// The last of the table's places that is not below v (the first, if all are).
+__device__ __forceinline__ int table_place(const Table &table, double v) {
+  const int i = last_below(kPlaces / 2 + 1, [&](int i) { return table.at(2 * i) >= v; });
+  return 2 * i + 1 < kPlaces && table.at(2 * i + 1) >= v ? 2 * i + 1 : 2 * i;
 }
 
 // Which bins are wanted: up to four runs of them.
@@ -420,8 +437,8 @@ __device__ Wanted decide(const Row &r, Lds<THREADS> &m) {
   }
   if (r.least > 0.0) {
     // the border lies between two entries of the table, or within rounding of them
-    const int i = last_below(kTable, [&](int i) { return m.table[i] >= r.least * kOne; });
-    const int b = bin_of(max(2 * i - 1, 0)), e = bin_of(2 * i + 2);
+    const int i = table_place(m.table, r.least * kOne);
+    const int b = bin_of(max(i - 1, 0)), e = bin_of(min(i + 2, kPlaces - 1));
     wanted.add(2, b, e);
     wanted.before_least = m.sum[b];
     lo = min(lo, max(m.sum[b], 1ull)), hi = min(hi, m.sum[e + 1]);
@@ -456,7 +473,7 @@ __device__ void sort_falling(unsigned long long *x, int n) {
 // The gathered tokens, the largest first; where they are.
 template <int THREADS>
 __device__ const unsigned long long *sorted(Lds<THREADS> &m, int n) {
-  if (n <= 256) {
+  if (n <= kFew) {
     // a token's place is the number of larger ones
     for (int i = threadIdx.x; i < n; i += THREADS) {
       const unsigned long long mine = m.token[i];
@@ -482,8 +499,6 @@ __device__ void settle(const SampleArgs &a, long long row, const Row &r, Lds<THR
   constexpr int kMine = kCap / THREADS;
   const int lane = threadIdx.x & 63, i0 = kMine * threadIdx.x;
   const unsigned long long *x = sorted(m, n);
-  // running sums up to each token, in the array that x is not
-  unsigned long long *to = x == m.token ? m.sorted : m.token;
   const auto spot = [&](int i) { return Spot(r.distance(value_of((uint32_t)(x[i] >> 32))), m.table); };
   int bin[kMine];
   unsigned long long w[kMine], sum = 0;
@@ -507,18 +522,25 @@ __device__ void settle(const SampleArgs &a, long long row, const Row &r, Lds<THR
   }
   __syncthreads();
   run -= sum;
+  const unsigned long long total = m.sum[kBins];
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
     run += w[j];
-    if (i0 + j < n) to[i0 + j] = run + m.sum[bin[j]];
+    w[j] = bin[j] >= 0 ? run + m.sum[bin[j]] : 0ull;
   }
+  __syncthreads();
+  // the running sums up to each token take the place of the bins'
+  unsigned long long *to = m.sum;
+#pragma unroll
+  for (int j = 0; j < kMine; ++j)
+    if (i0 + j < n) to[i0 + j] = w[j];
   __syncthreads();
   if (threadIdx.x >= 64) return;
   // the first token whose running sum reaches a position
   const auto token_at = [&](unsigned long long p) {
     return n - 1 - last_below(n, [&](int i) { return to[n - 1 - i] >= p; });
   };
-  unsigned long long keep = m.sum[kBins];
+  unsigned long long keep = total;
   if (r.k > 0 && (uint32_t)r.k < m.count[kBins])
     keep = to[last_below(n, [&](int i) { return (uint32_t)i + m.count[spot(i).bin] < (uint32_t)r.k; })];
   if (r.share < 1.0) keep = min(keep, to[token_at(r.share_of(keep))]);
@@ -540,7 +562,7 @@ struct Place {
 };
 
 // The weight of a value, or 0.
-__device__ __forceinline__ unsigned long long weight_of(const Row &r, float v, const double *table) {
+__device__ __forceinline__ unsigned long long weight_of(const Row &r, float v, const Table &table) {
   const double d = r.distance(v);
   return d < kFar ? Spot(d, table).weight() : 0ull;
 }
@@ -699,7 +721,7 @@ __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
   Row r(a, blockIdx.y);
   for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = s.sum[i], m.count[i] = s.count[i];
   const uint32_t top = (uint32_t)(top_of(s, gridDim.x) >> 32);
-  fill_table<kScan>(m.table);
+  m.table.fill();
   if (!top || r.greedy) return;
   r.top = (double)value_of(top);
   __syncthreads();
@@ -724,7 +746,7 @@ __global__ __launch_bounds__(kScan) void sample_finish_kernel(SampleArgs a, int 
   for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = s.sum[i], m.count[i] = s.count[i];
   for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kCap); i += kScan) m.token[i] = s.near[i];
   const unsigned long long first = top_of(s, segments);
-  fill_table<kScan>(m.table);
+  m.table.fill();
   if (!first || r.greedy) {
     if (threadIdx.x == 0) give(a, row, first ? (int)~(uint32_t)first : -1, first ? 1.0 : 0.0);
     return;
@@ -742,7 +764,7 @@ __global__ __launch_bounds__(kScan) void sample_row_kernel(SampleArgs a) {
   const Tokens<TY, kScan> tokens(a, row, 0, a.V);
   Row r(a, row);
   for (int i = threadIdx.x; i < kBins; i += kScan) m.sum[i] = 0ull, m.count[i] = 0u;
-  fill_table<kScan>(m.table);
+  m.table.fill();
   First mine;
   tokens.template each<false>([&](float v, int id) { mine.see(v, id); });
   const unsigned long long first = block_max<kScan>(mine.token(), m.part);
