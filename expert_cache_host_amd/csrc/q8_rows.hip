@@ -62,9 +62,11 @@ __global__ __launch_bounds__(kThreads) void q8_rows_kernel(Q8RowsArgs a) {
   }
 }
 
+// One wave a row where rows are short, or many enough to fill the card that way.
 template <int TY>
 hipError_t launch_type(const Q8RowsArgs &a, hipStream_t s) {
-  if (a.cols <= 64 * 8 * kHeld) return launch(q8_rows_kernel<TY, 1>, dim3((a.n + 3) / 4), dim3(kThreads), s, a);
+  if (a.cols <= 512 || (a.cols <= 64 * 8 * kHeld && a.n >= 4096))
+    return launch(q8_rows_kernel<TY, 1>, dim3((a.n + 3) / 4), dim3(kThreads), s, a);
   return launch(q8_rows_kernel<TY, 4>, dim3(a.n), dim3(kThreads), s, a);
 }
 
