@@ -1,8 +1,8 @@
 // Rows in 8-bit integers: s = max|x| / 127 (float32), code = rint(x / s).
 //
-// Bound by memory: a row is read once into registers, its maximum taken, and coded
-// from there (what a thread cannot hold is read a second time, out of the cache).  A
-// row of up to 2048 columns takes one wave, a longer one a workgroup of four.
+// Bound by memory (4096 x 6144 bfloat16: 21 us, 3.6 TB/s; 512 x 6144: 5.7, latency): a
+// row is read once into registers, its maximum taken, and coded
+// from there (what a thread cannot hold is read a second time, out of the cache).
 #include "q8_code.hpp"
 #include "step_ops.hpp"
 
@@ -62,7 +62,8 @@ __global__ __launch_bounds__(kThreads) void q8_rows_kernel(Q8RowsArgs a) {
   }
 }
 
-// One wave a row where rows are short, or many enough to fill the card that way.
+// One wave a row where rows are short, or many enough to fill the card that way (8192 x
+// 1024 float32: 11.6 us, 13.8 with four); else four (509 x 2045: 4.1 us, 6.4 with one).
 template <int TY>
 hipError_t launch_type(const Q8RowsArgs &a, hipStream_t s) {
   if (a.cols <= 512 || (a.cols <= 64 * 8 * kHeld && a.n >= 4096))

@@ -7,7 +7,9 @@
 // counts from ballots); the experts not below it by more than the estimates' error get
 // their values in binary64, a lane each, and are ranked.  Groups
 // are kept by estimates too.  Where estimates cannot decide (groups too close, more than
-// 64 candidates) the token is computed in binary64 throughout.
+// 64 candidates) the token is computed in binary64 throughout.  12288 tokens of 512
+// bfloat16 logits with a bias: 17 us, bound by instruction issue, where binary64 for all
+// took 42; 512 tokens of 256 in groups 6.9 (12).
 #include "device_types.hpp"
 #include "step_ops.hpp"
 

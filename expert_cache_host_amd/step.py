@@ -144,11 +144,13 @@ def q8_matmul(x, w: Q8Matrix, out=None, dtype: Optional[torch.dtype] = None, str
     else:
         ldx = _rows(x, "x", dev, None, w.cols)
         T, dt = x.shape[0], x.dtype
+    if T > 1 << 20:
+        raise ValueError("x holds more than 2^20 rows")
     if out is None:
         dt = dtype or dt
         if dt not in _TYPES:
             raise ValueError("dtype must be float32, bfloat16 or float16")
-        out = torch.empty((T, w.rows), dtype=dt, device=w.device)
+        out = w.scales.new_empty((T, w.rows), dtype=dt)
         ldo = w.rows
     else:
         ldo = _rows(out, "out", dev, T, w.rows, dtype)
@@ -159,10 +161,8 @@ def q8_matmul(x, w: Q8Matrix, out=None, dtype: Optional[torch.dtype] = None, str
         rc = lib.moe_q8_matmul(x.codes.data_ptr(), x.codes.shape[1], x.scales.data_ptr(), T, wp, ldw, sp, rows, cols,
                                out.data_ptr(), _TYPES[dt], ldo, _raw_stream(dev))
     else:
-        need = lib.moe_q8_linear_workspace(T, rows, cols)
-        if need < 0:
-            _check(need)
-        ws = torch.empty(need, dtype=torch.uint8, device=w.device) if need else None
+        need = T * (-(-cols // _PAD) * _PAD + 4)  # as moe_q8_linear_workspace says
+        ws = w.codes.new_empty(need) if need else None
         rc = lib.moe_q8_linear(x.data_ptr(), _TYPES[x.dtype], ldx, T, wp, ldw, sp, rows, cols, out.data_ptr(),
                                _TYPES[dt], ldo, ws.data_ptr() if need else None, need, _raw_stream(dev))
     if rc:
@@ -197,8 +197,8 @@ def route_experts(logits, rule: RoutingRule, bias=None, stream=None) -> Tuple[to
     ld = _rows(logits, "logits", dev)
     T, E = logits.shape
     bp = None if bias is None else _weight(bias, "bias", dev, E)
-    idx = torch.empty((T, rule.top_k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, rule.top_k), dtype=torch.float32, device=logits.device)
+    idx = logits.new_empty((T, rule.top_k), dtype=torch.int32)
+    w = logits.new_empty((T, rule.top_k), dtype=torch.float32)
     rc = _library().moe_route(logits.data_ptr(), _TYPES[logits.dtype], ld, bp, T, E, rule._cp, idx.data_ptr(),
                               w.data_ptr(), _raw_stream(dev))
     if rc:
@@ -237,13 +237,12 @@ def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, str
     if not 0 <= k0 <= _I32:
         raise ValueError("top_k must be in [0, 2^31)")
     opts = _SampleOpts(t0, p0, m0, k0, tp, pp, mp, kp)
-    token = torch.empty(T, dtype=torch.int32, device=logits.device)
-    prob = torch.empty(T, dtype=f32, device=logits.device)
+    token, prob = u.new_empty(T, dtype=torch.int32), u.new_empty(T)
     lib = _library()
     need = lib.moe_sample_workspace(T, V)
     if need < 0:
         _check(need)
-    ws = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
+    ws = u.new_empty(need, dtype=torch.uint8) if need else None
     rc = lib.moe_sample(logits.data_ptr(), _TYPES[logits.dtype], ld, T, V, up, opts, token.data_ptr(), prob.data_ptr(),
                         ws.data_ptr() if need else None, need, _raw_stream(dev))
     if rc:

@@ -673,7 +673,9 @@ moe_status moe_route(const void *logits, int32_t type, int64_t stride, const flo
 /* moe_layer_forward_ruled -- moe_layer_forward with the experts and gating weights that
  * `rule` selects from the router's logits (router_bias is part of the logits, select_bias,
  * device float32 [n_experts] or NULL, of the selection alone).  rule->top_k must be the
- * cache's top_k; the cache's norm_topk is not looked at.  Everything else is as there. */
+ * cache's top_k; the cache's norm_topk is not looked at.  On decode calls the host waits
+ * for the rule's kernel instead of selecting from published logits; that kernel is not
+ * among the timed ones.  Everything else is as there. */
 moe_status moe_layer_forward_ruled(moe_cache *c, int32_t layer, const float *x, int32_t n_tokens,
                                    const float *router_w, const float *router_bias, const moe_route_rule *rule,
                                    const float *select_bias, float *out, moe_stream_t stream);

@@ -173,6 +173,14 @@ def test_q8_matmul_rows_that_are_not_finite(T):
     check_product(x, w, codes, scales, dtype=torch.float16)  # past the type's largest: infinities
 
 
+@pytest.mark.parametrize("rows,cols,T", [(1, 131072, 300), (1, 5000, 1), (70, 131056, 33), (5000, 1, 700), (10240, 16, 16),
+                                         (10239, 127, 32), (4097, 300, 17), (4096, 300, 32), (3, 40000, 4)])
+def test_q8_matmul_thin(rows, cols, T):
+    g = gen(rows + T)
+    codes, scales = matrix(g, rows, cols)
+    check_product(rnd(g, T, cols), m.Q8Matrix(codes, scales), codes, scales)
+
+
 def test_q8_matmul_empty():
     g = gen(6)
     codes, scales = matrix(g, 70, 200)
@@ -281,6 +289,12 @@ def test_route_ties_and_close_values(groups, keep, score):
     z = 1 + torch.randint(0, 40, (50, E), generator=g, device="cuda") * 2.0 ** -23
     check_route(z, torch.full((E,), 100.0, device="cuda"), k=k, score=score, groups=groups, keep=keep, best=2)
     check_route(-z * 20, torch.full((E,), 1.0, device="cuda"), k=k, score=score, groups=groups, keep=keep, best=1)
+    # more equal values than a wave has lanes
+    b = torch.zeros(512, device="cuda")
+    b[7] = 1
+    check_route(torch.ones(3, 512, device="cuda"), b, k=k, score=score, groups=groups, keep=keep, best=2)
+    check_route(torch.round(rnd(g, 20, 512) / 2), b, k=63, score=score, groups=groups, keep=keep, best=2)
+    check_route(torch.round(rnd(g, 20, 512) / 2), None, k=64, score=score, groups=groups, keep=keep)
     # +0 and -0 are equal
     z = torch.zeros(2, E, device="cuda")
     z[:, ::2] = -0.0
@@ -434,6 +448,29 @@ def test_sample_sizes(V, ty):
     for kw in (dict(), dict(temperature=0.0), dict(temperature=0.7, top_k=50, top_p=0.9), dict(top_p=0.6),
                dict(min_p=0.05), dict(temperature=1.3, top_k=1000, top_p=0.97, min_p=0.01), dict(top_k=1),
                dict(temperature=2.5, top_k=V // 2 + 1)):
+        check_sample(z, u, **kw)
+
+
+@pytest.mark.parametrize("V", [16383, 16384, 16385, 20001])
+def test_sample_around_the_short_rows(V):
+    """Rows that one workgroup takes and rows that several launches take; many rows of one segment each."""
+    g = gen(V)
+    for T in (2, 600 if V > 16384 else 40):
+        z, u = rnd(g, T, V, scale=2.5), torch.rand(T, generator=g, device="cuda")
+        check_sample(z, u, temperature=0.9, top_k=77, top_p=0.9, min_p=0.01)
+
+
+@pytest.mark.parametrize("V", [9000, 40000])
+@pytest.mark.parametrize("n", [255, 256, 257, 2047, 2048, 2049, 2500])
+def test_sample_around_the_sorted_tokens(V, n):
+    """n equal tokens ahead of the others: as many as are sorted by counting, in LDS, or not at all."""
+    g = gen(n)
+    T = 9
+    z = rnd(g, T, V) - 20
+    for t in range(T):
+        z[t, torch.randperm(V, generator=g, device="cuda")[:n]] = 1.5
+    u = torch.linspace(0, 0.9999999, T, device="cuda")
+    for kw in (dict(), dict(top_k=n - 1), dict(top_k=n + 1), dict(top_p=0.5), dict(min_p=0.9, top_k=n // 2)):
         check_sample(z, u, **kw)
 
 

@@ -63,6 +63,8 @@ def test_q8_linear(kw, msg):
 def test_q8_linear_workspace():
     ws = step._library().moe_q8_linear_workspace
     assert ws(0, 40, 100) >= 0 and ws(3, 40, 129) >= 3 * (256 + 4)
+    for T, rows, cols in ((1, 1, 1), (7, 300, 128), (1 << 20, 64, 131072), (4000, 9000, 6145)):  # what the binding gives
+        assert ws(T, rows, cols) == T * (-(-cols // 128) * 128 + 4)
     refused(ws(-1, 40, 100), "n_tokens")
     refused(ws(1, 0, 100), "rows")
     refused(ws(1, 1, 0), "cols")
