@@ -1,8 +1,8 @@
 // Rows in 8-bit integers: s = max|x| / 127 (float32), code = rint(x / s).
 //
 // Bound by memory (4096 x 6144 bfloat16: 21 us, 3.6 TB/s; 512 x 6144: 5.7, latency): a
-// row is read once into registers, its maximum taken, and coded
-// from there (what a thread cannot hold is read a second time, out of the cache).
+// row is read once into registers, its maximum taken, and coded from there (what a
+// thread cannot hold is read a second time, out of the cache).
 #include "q8_code.hpp"
 #include "step_ops.hpp"
 

