@@ -8,8 +8,8 @@
 // their values in binary64, a lane each, and are ranked.  Groups
 // are kept by estimates too.  Where estimates cannot decide (groups too close, more than
 // 64 candidates) the token is computed in binary64 throughout.  12288 tokens of 512
-// bfloat16 logits with a bias: 17 us, bound by instruction issue, where binary64 for all
-// took 42; 512 tokens of 256 in groups 6.9 (12).
+// bfloat16 logits with a bias: 15 us, bound by instruction issue, where binary64 for all
+// took 42; 512 tokens of 256 in groups 6.4 (12).
 #include "device_types.hpp"
 #include "step_ops.hpp"
 
@@ -85,6 +85,9 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 }
 
 constexpr uint32_t kLeast = 0x00800000u;  // of the lowest finite float
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
+}
 
 // A logit as it counts: NaN as minus infinity, plus infinity as the largest float.
 __device__ __forceinline__ float logit_of(float v) {
@@ -294,21 +297,25 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
   double my_s = 0.0;
   if (sure) {
     // the bits of a float32 that at least k estimates reach, k + 4 at most unless more
-    // are equal: by halving, first from 2 binary orders below the largest on
-    uint32_t key[N];
+    // are equal: by halving, first from half a binary order below the largest on
     float top = kLow;
 #pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = c[i] > kLow ? order_bits(c[i]) : 0u, top = fmaxf(top, c[i]);
+    for (int i = 0; i < N; ++i) top = fmaxf(top, c[i]);
     const auto reach = [&](uint32_t to) {
+      const float v = value_of(to);
       int n = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= to));
+      for (int i = 0; i < N; ++i) n += __popcll(__ballot(c[i] >= v));
       return n;
     };
     uint32_t above = __builtin_amdgcn_readfirstlane(order_bits(wave_max(top))) + 1u;
-    uint32_t least = above > kLeast + (1u << 24) ? above - (1u << 24) : kLeast;
+    uint32_t least = above > kLeast + (1u << 22) ? above - (1u << 22) : kLeast;
     int n = reach(least);
-    if (n < a.k) above = least, least = kLeast, n = reach(least);
+    for (int wide = 24; n < a.k && least > kLeast; wide = 32) {
+      above = least;
+      least = wide == 24 && above > kLeast + (1u << 24) ? above - (1u << 24) : kLeast;
+      n = reach(least);
+    }
     while (n > a.k + 4 && above - least > 1u) {
       const uint32_t to = least + (above - least) / 2;
       const int got = reach(to);
@@ -317,14 +324,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
       else
         above = to;
     }
-    if (slack > 0.f) {
-      const float v = __uint_as_float(least >> 31 ? least & 0x7fffffffu : ~least);
-      least = max(order_bits(v - 2.f * slack - 4.8e-7f * fabsf(v)), kLeast);
-    }
+    float from = value_of(least);
+    if (slack > 0.f) from = fmaxf(from - 2.f * slack - 4.8e-7f * fabsf(from), -3.40282347e38f);
     // candidates (excluded experts are none)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool in = key[i] >= least;
+      const bool in = c[i] >= from;
       const uint64_t who = __ballot(in);
       const int place = count + __popcll(who & ((1ull << lane) - 1));
       if (in && place < 64) list[place] = expert(i);
@@ -343,17 +348,23 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
       value = a.bias ? s + (double)a.bias[e] : (double)v;
     }
     int rank = 0;
-    for (int o = 0; o < count; ++o) {
-      const double x = lane_of(value, o);
-      const int i = __builtin_amdgcn_readlane(e, o);
-      rank += x > value || (x == value && i < e);
+    for (int o = 0; o < count; ++o) rank += lane_of(value, o) > value;
+    // to the lane of its rank; equal values, which meet there, go by their ids
+    wave_sync();
+    if (lane < count) list[rank] = lane;
+    wave_sync();
+    if (__ballot(lane < count && list[rank] != lane)) {
+      rank = 0;
+      for (int o = 0; o < count; ++o) {
+        const double x = lane_of(value, o);
+        rank += x > value || (x == value && __builtin_amdgcn_readlane(e, o) < e);
+      }
+      wave_sync();
+      if (lane < count) list[rank] = lane;
+      wave_sync();
     }
-    // to the lane of its rank
-    wave_sync();
-    if (lane < count && rank < a.k) list[rank] = lane;
-    wave_sync();
-    const int from = lane < a.k ? list[lane] : 0;
-    my_e = __shfl(e, from, 64), my_s = __shfl(s, from, 64);
+    const int at = lane < a.k ? list[lane] : 0;
+    my_e = __shfl(e, at, 64), my_s = __shfl(s, at, 64);
   } else {
     wave_sync();
     const RouteArgs copy = a;  // (the address of `a` itself would move it to memory for all)
