@@ -181,10 +181,15 @@ class RoutingRule:
                  group_best: int = 1, renorm: bool = True, scale: float = 1.0):
         if score not in _SCORES:
             raise ValueError("score must be 'softmax' or 'sigmoid'")
-        self.top_k = top_k
+        if not 1 <= top_k <= 64:
+            raise ValueError("top_k must be in [1, 64]")
         self._c = RouteRule(top_k, _SCORES[score], groups, groups if keep_groups is None else keep_groups, group_best,
                             1 if renorm else 0, scale)
         self._cp = ctypes.pointer(self._c)
+
+    @property
+    def top_k(self) -> int:
+        return self._c.top_k
 
 
 def route_experts(logits, rule: RoutingRule, bias=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -197,8 +202,8 @@ def route_experts(logits, rule: RoutingRule, bias=None, stream=None) -> Tuple[to
     ld = _rows(logits, "logits", dev)
     T, E = logits.shape
     bp = None if bias is None else _weight(bias, "bias", dev, E)
-    idx = logits.new_empty((T, rule.top_k), dtype=torch.int32)
-    w = logits.new_empty((T, rule.top_k), dtype=torch.float32)
+    k = rule._c.top_k
+    idx, w = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32)
     rc = _library().moe_route(logits.data_ptr(), _TYPES[logits.dtype], ld, bp, T, E, rule._cp, idx.data_ptr(),
                               w.data_ptr(), _raw_stream(dev))
     if rc:

@@ -405,6 +405,34 @@ def test_layer_with_a_rule(mode, T):
     c.close()
 
 
+@pytest.mark.parametrize("T", [1, 6])
+def test_layer_with_a_rule_timed_and_on_another_stream(T):
+    """Timing, partial results and logits as without a rule; calls on changing streams."""
+    wl = synth.WORKLOADS["tiny"]
+    c = m.MoECache(1, wl.n_experts, 4, wl.d_model, wl.d_ff, synth.gen_experts(wl, 0), top_k=wl.top_k, miss_mode="host",
+                   keep_debug=True)
+    c.set_timing(True)
+    g = gen(T)
+    w_r = rnd(g, wl.n_experts, wl.d_model, scale=0.1)
+    r = m.RoutingRule(wl.top_k, "sigmoid", scale=2.0)
+    streams = [torch.cuda.current_stream(), torch.cuda.Stream()]
+    x = rnd(g, T, wl.d_model)
+    torch.cuda.synchronize()
+    outs = []
+    for call in range(4):
+        with torch.cuda.stream(streams[call % 2]):
+            outs.append(c.forward(0, x, w_r, rule=r))
+        torch.cuda.synchronize()
+        gpu, host = c.partials(0)
+        np.testing.assert_array_equal(gpu + host, outs[-1].cpu().numpy())
+        z = router_logits_fp32(x.cpu().numpy(), w_r.cpu().numpy(), None)
+        idx, w = o.route(z, None, wl.top_k, "sigmoid", scale=2.0)
+        np.testing.assert_array_equal(c.routing(0)[0], idx)
+    assert c.kernel_stats()["router"][0] == 4
+    check_close(outs[3].cpu().numpy(), f64(outs[0]))
+    c.close()
+
+
 def test_layer_rule_refusals():
     wl = synth.WORKLOADS["tiny"]
     c = m.MoECache(1, wl.n_experts, 4, wl.d_model, wl.d_ff, synth.gen_experts(wl, 0), top_k=wl.top_k)

@@ -145,3 +145,8 @@ def test_tensors_must_be_on_the_gpu():
             call()
     with pytest.raises(ValueError, match="score"):
         m.RoutingRule(2, score="tanh")
+    for k in (0, -1, 65):
+        with pytest.raises(ValueError, match="top_k"):
+            m.RoutingRule(k)
+    with pytest.raises(AttributeError):
+        m.RoutingRule(2).top_k = 3
