@@ -283,10 +283,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
       rank += x > v || (x == v && o < g);
     }
     const uint64_t kept = __ballot(g < a.groups && rank < a.keep);
-    // the last kept and the first left out have to lie apart by more than both are off
+    // the last kept and the first left out have to lie apart by more than both are off (a
+    // pair's sum by as much as its larger part's rounding, though the parts may cancel)
     const float last = __shfl(v, __ffsll((unsigned long long)__ballot(g < a.groups && rank == a.keep - 1)) - 1, 64);
     const float next = __shfl(v, __ffsll((unsigned long long)__ballot(g < a.groups && rank == a.keep)) - 1, 64);
-    const float apart = (a.bias || scores ? 2.f * a.best * off + 4.8e-7f * (fabsf(last) + fabsf(next)) : 0.f);
+    const float size = a.best == 2 ? wave_max(v > kLow ? fabsf(v1) + fabsf(v2) : 0.f) : fabsf(last) + fabsf(next);
+    const float apart = a.bias || scores ? 2.f * a.best * off + 4.8e-7f * size : 0.f;
     if (apart > 0.f && !(last - next > apart)) sure = next == kLow && last == kLow;
 #pragma unroll
     for (int i = 0; i < N; ++i)

@@ -275,6 +275,18 @@ def test_route_groups(E, groups, keep, k, best):
         check_route(rnd(g, T, E, scale=1.5, dtype=TYPES[ty]), bias, k=k, score=score, groups=groups, keep=keep, best=best)
 
 
+@pytest.mark.parametrize("size", [50.0, 1e4, 1e30])
+def test_route_groups_whose_pairs_cancel(size):
+    """A group's two best of opposite signs: their sum is far smaller than what float32 rounds off either."""
+    g = gen(5)
+    E, groups = 64, 8
+    bias = torch.full((E,), -size, device="cuda")
+    bias[::E // groups] = size
+    z = 1e-5 * rnd(g, 200, E)
+    for score in ("sigmoid", "softmax"):
+        check_route(z, bias, k=4, score=score, groups=groups, keep=3, best=2)
+
+
 @pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_and_close_values(groups, keep, score):
