@@ -129,8 +129,10 @@ struct Row {
   int k;                     // top-k (0: all)
   bool greedy;
   __device__ __forceinline__ Row(const SampleArgs &a, long long row) {
-    temp = (a.temperatures ? (double)a.temperatures[row] : a.temperature) * 0.0078125;
-    greedy = !(temp > 0.0);
+    const double t = a.temperatures ? (double)a.temperatures[row] : a.temperature;
+    greedy = !(t > 0.0);
+    // (below 1e-300, whose inverse is finite, unequal float32 logits have weights 1 and 0 alike)
+    temp = fmax(t, 1e-300) * 0.0078125;
     inv = greedy ? 1.0 : 1.0 / temp;
     const double p = a.top_ps ? (double)a.top_ps[row] : a.top_p;
     share = p < 1.0 ? fmax(p, 0.0) : 1.0;  // NaN keeps all

@@ -578,6 +578,24 @@ def test_sample_flat_and_steep():
     check_sample(z + 1e6, u, temperature=1e-2, top_k=9)
 
 
+@pytest.mark.parametrize("V", [700, 20000])
+def test_sample_temperatures_at_the_ends(V):
+    """Temperatures whose inverse passes binary64, infinite ones, and those at the ends of float32."""
+    g = gen(19)
+    T = 6
+    u = torch.rand(T, generator=g, device="cuda")
+    z = rnd(g, T, V)
+    z[2, :5] = z[2].max() + 1  # equal largest tokens
+    for t in (5e-324, 1e-310, 1e-306, 1e300):
+        for kw in (dict(), dict(top_k=3), dict(top_p=0.7), dict(min_p=0.4)):
+            check_sample(z, u, temperature=t, **kw)
+    t = torch.full_like(u, float("inf"))
+    t[::3] = 1e-45
+    t[1::3] = 3.4e38
+    check_sample(z, u, temperature=t)
+    check_sample(z, u, temperature=t, top_k=50, top_p=0.6, min_p=0.2)
+
+
 def test_sample_masked():
     g = gen(12)
     inf = float("inf")
