@@ -162,6 +162,7 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   const int steps = (a.cols + 127) / 128;
 #pragma unroll
   for (int i = 0; i < S; ++i) load(i * kStep, 128 * i);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the scales, before the workgroup meets
   wait_loads<(S - 1) * (LA + LB)>();
 #pragma unroll
   for (int n = 0; n < kFrags; ++n) read1(lds, 0, f0, n);
@@ -230,6 +231,7 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   first_half(nothing);
   multiply(f2, nothing);
   multiply(f3, nothing);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // a single step's loads past the last column
   // a lane holds, of token lane % 32, four rows in eight; the wave's halves swap, so
   // that it has eight in sixteen
   const int half = lane >> 5;
