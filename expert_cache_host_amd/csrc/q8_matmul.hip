@@ -16,6 +16,7 @@
 // Few tokens: memory.  24 x 6144 x 10240 in 14.3 us (4.4 TB/s of weights), one token
 // by 2816 x 8192, its codes made on the way, in 8.1.
 #include "q8_code.hpp"
+#include "q8_tiles.hpp"
 #include "step_ops.hpp"
 
 namespace moe {
@@ -35,19 +36,19 @@ __device__ __forceinline__ float scaled(int sum, float sx, float sw) {
 
 using i32x16 = __attribute__((ext_vector_type(16))) int;
 
-// Rows of codes as a buffer that starts at row r0: what lies behind the last row reads 0.
-__device__ __forceinline__ i32x4 rows_from(const int8_t *p, long long ld, int r0, int rows, int most, int bytes) {
+// n rows of codes from row r0 on as a buffer.
+__device__ __forceinline__ i32x4 rows_from(const int8_t *p, long long ld, int r0, int n, int bytes) {
   const uint64_t base = (uint64_t)(p + (long long)r0 * ld);
   i32x4 r;
   r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
   r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xffff);
-  r[2] = __builtin_amdgcn_readfirstlane((min(rows - r0, most) - 1) * (int)ld + bytes);
+  r[2] = __builtin_amdgcn_readfirstlane(q8_buffer_bytes(n, (int)ld, bytes));
   r[3] = 0x00027000;
   return r;
 }
 
 // 16 bytes a lane from the buffer's byte lane_at + at into LDS, the wave's kilobyte
-// at place `l`.  Written as assembly (it returns nothing in registers) because the
+// at place `l`; `at` lies in the buffer, a lane's byte behind its end gives 0.  Written as assembly (it returns nothing in registers) because the
 // compiler waits for every such load before any read of LDS (nothing else here uses
 // m0); wait_loads says which
 // of them a wave waits for.
@@ -109,19 +110,20 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   __shared__ __attribute__((aligned(16))) float sws[RT], sxs[TT];
   for (int i = threadIdx.x; i < RT; i += 64 * NW) sws[i] = r0 + i < a.rows ? a.w_scales[r0 + i] : 0.f;
   for (int i = threadIdx.x; i < TT; i += 64 * NW) sxs[i] = t0 + i < a.T ? a.x_scales[t0 + i] : 0.f;
-  const auto wr = rows_from(a.w, a.ldw, r0, a.rows, RT, (a.cols + 15) & ~15);
-  const auto xr = rows_from(a.x, a.ldx, t0, a.T, TT, (a.cols + 127) & ~127);
-  // a wave's load takes 8 rows of 128 bytes; the 16-byte pieces of row r lie at place
-  // piece ^ r / 2 % 8: sixteen lanes that read the same piece of sixteen rows then
-  // touch each of the 64 banks once (with r % 8 half of the LDS time was conflicts)
+  const int n_rows = min(a.rows - r0, RT), n_tokens = min(a.T - t0, TT);
+  const auto wr = rows_from(a.w, a.ldw, r0, n_rows, (a.cols + 15) & ~15);
+  const auto xr = rows_from(a.x, a.ldx, t0, n_tokens, (a.cols + 127) & ~127);
   static_assert(NW % 2 == 0, "a wave's loads all start at rows of the same r / 8 % 2");
-  const int piece = ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4))) * 16, row = (lane >> 3) + 8 * wave;
-  const int wo = row * (int)a.ldw + piece, xo = row * (int)a.ldx + piece;
-  const int ldw8 = 8 * NW * (int)a.ldw, ldx8 = 8 * NW * (int)a.ldx;
+  const int wo = q8_lane_at(lane, wave, (int)a.ldw), xo = q8_lane_at(lane, wave, (int)a.ldx);
+  int wj[LA], xj[LB];
+#pragma unroll
+  for (int j = 0; j < LA; ++j) wj[j] = q8_load_at(j, NW, n_rows, (int)a.ldw);
+#pragma unroll
+  for (int j = 0; j < LB; ++j) xj[j] = q8_load_at(j, NW, n_tokens, (int)a.ldx);
   const uint32_t lds_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t *)lds + wave * 1024;
-  const auto load_w = [&](int j, int to, int k) { load_lds(wr, lds_at + to + j * NW * 1024, wo, j * ldw8 + k); };
+  const auto load_w = [&](int j, int to, int k) { load_lds(wr, lds_at + to + j * NW * 1024, wo, wj[j] + k); };
   const auto load_x = [&](int j, int to, int k) {
-    load_lds(xr, lds_at + to + RT * 128 + j * NW * 1024, xo, j * ldx8 + k);
+    load_lds(xr, lds_at + to + RT * 128 + j * NW * 1024, xo, xj[j] + k);
   };
   const auto load = [&](int to, int k) {
 #pragma unroll
@@ -157,11 +159,10 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   };
   Frag f0, f1, f2, f3;
   int cur = 0;
-  // S steps of 128 columns are under way; those past the last column are loaded (out
-  // of the rows behind, or as 0) and not used
-  const int steps = (a.cols + 127) / 128;
+  // S steps of 128 columns are under way
+  const int steps = q8_steps(a.cols);
 #pragma unroll
-  for (int i = 0; i < S; ++i) load(i * kStep, 128 * i);
+  for (int i = 0; i < S; ++i) load(i * kStep, q8_step_at(i, a.cols));
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the scales, before the workgroup meets
   wait_loads<(S - 1) * (LA + LB)>();
 #pragma unroll
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(64 * WR * WT) void q8_tile_kernel(Q8MatmulArgs a, i
   first_half(nothing);
   multiply(f2, nothing);
   multiply(f3, nothing);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // a single step's loads past the last column
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // a single step's repeated loads
   // a lane holds, of token lane % 32, four rows in eight; the wave's halves swap, so
   // that it has eight in sixteen
   const int half = lane >> 5;
@@ -366,41 +367,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void q8_few_kernel(Q8MatmulArgs a, 
   }
 }
 
-// Tiles (rows x tokens, waves, steps under way) and what a step of 128 columns takes
-// on a CU, in microseconds: alone, and with as many workgroups as fit; `tile` is a
-// tile's start and end.  Fitted to 48 products of 65 to 4096 tokens, 200 to 12288
-// columns and 64 to 32768 rows (matrices out of the cache), of which the estimate's
-// choice took 1.03 of the best tile's time in the mean and 1.17 at most; one tile of
-// 256 x 256 for all took 1.9 and 4.8.
-struct Tile {
-  int rows, tokens, fit;
-  float tile, alone, shared;
-};
-constexpr Tile kTiles[] = {
-    {256, 256, 1, 9.6f, 1.11f, 1.11f}, {160, 128, 2, 6.0f, 0.49f, 1.32f}, {128, 128, 2, 5.5f, 0.43f, 1.08f},
-    {96, 128, 1, 4.0f, 0.39f, 0.39f},  {64, 64, 2, 2.0f, 0.21f, 0.44f},   {32, 64, 2, 1.8f, 0.19f, 0.28f},
-    {64, 32, 3, 1.1f, 0.17f, 0.49f},
-};
-
-int best_tile(const Q8MatmulArgs &a) {
-  int best = 0;
-  double least = 1e30;
-  for (int i = 0; i < (int)(sizeof kTiles / sizeof *kTiles); ++i) {
-    const Tile &c = kTiles[i];
-    const int64_t tiles = (int64_t)((a.rows + c.rows - 1) / c.rows) * ((a.T + c.tokens - 1) / c.tokens);
-    if (tiles >= 1 << 22) continue;  // a grid holds fewer than 2^32 threads
-    const int64_t n = (tiles + 255) / 256, steps = (a.cols + 127) / 128;  // tiles a CU
-    const double t = (double)((n + c.fit - 1) / c.fit) * c.tile +
-                     (double)steps * ((double)(n / c.fit) * c.shared + (double)(n % c.fit) * c.alone);
-    if (t < least) least = t, best = i;
-  }
-  return best;
-}
-
-template <int TY, int RT, int TT, int WR, int WT, int S>
+template <int TY, int I>
 hipError_t launch_tile(const Q8MatmulArgs &a, hipStream_t s) {
-  const int r = (a.rows + RT - 1) / RT, t = (a.T + TT - 1) / TT;
-  return launch(q8_tile_kernel<TY, RT, TT, WR, WT, S>, dim3(r * t), dim3(64 * WR * WT), s, a, r, t);
+  constexpr Q8Tile c = kQ8Tiles[I];
+  const int r = (a.rows + c.rows - 1) / c.rows, t = (a.T + c.tokens - 1) / c.tokens;
+  return launch(q8_tile_kernel<TY, c.rows, c.tokens, c.row_waves, c.token_waves, c.ahead>, dim3(r * t),
+                dim3(64 * c.row_waves * c.token_waves), s, a, r, t);
 }
 
 template <int TY, int TX, int NT, int RB>
@@ -410,26 +382,21 @@ hipError_t launch_few(const Q8MatmulArgs &a, const Q8RowsArgs *q, hipStream_t s)
                     kFewWaves * NT * RB * 1024 + codes, s, a, q ? q->x : nullptr, q ? q->ldx : 0ll);
 }
 
-// Few tokens and rows: too few tiles of 64 or 32 rows to keep the CUs' loads under way,
-// so that 8 waves share a tile's columns.  One token, 2816 and 6144 columns, 4096 rows:
-// 6.8 and 8.4 us (tiles of 64 x 32 take 8.5 and 12.8); 8192 rows: 6.9 and 12.1 (8.2 and
-// 13.4); 16384 rows: 11.7 and 22.0 (10.9 and 19.8).
-bool few(const Q8MatmulArgs &a) { return a.T <= (a.rows <= 4096 ? 32 : 16) && a.rows < 10240; }
-
 template <int TY>
 hipError_t launch_type(const Q8MatmulArgs &a, hipStream_t s) {
-  if (few(a)) {
+  if (q8_few(a.T, a.rows)) {
     if (a.rows > 4096) return launch_few<TY, -1, 1, 2>(a, nullptr, s);
     return a.T <= 16 ? launch_few<TY, -1, 1, 1>(a, nullptr, s) : launch_few<TY, -1, 2, 1>(a, nullptr, s);
   }
-  switch (best_tile(a)) {
-    case 0: return launch_tile<TY, 256, 256, 2, 4, 2>(a, s);
-    case 1: return launch_tile<TY, 160, 128, 1, 4, 2>(a, s);
-    case 2: return launch_tile<TY, 128, 128, 2, 2, 2>(a, s);
-    case 3: return launch_tile<TY, 96, 128, 1, 4, 4>(a, s);
-    case 4: return launch_tile<TY, 64, 64, 2, 2, 4>(a, s);
-    case 5: return launch_tile<TY, 32, 64, 1, 2, 6>(a, s);
-    default: return launch_tile<TY, 64, 32, 2, 1, 4>(a, s);
+  static_assert(kQ8TileCount == 7, "a case each");
+  switch (q8_best_tile(a.T, a.rows, a.cols)) {
+    case 0: return launch_tile<TY, 0>(a, s);
+    case 1: return launch_tile<TY, 1>(a, s);
+    case 2: return launch_tile<TY, 2>(a, s);
+    case 3: return launch_tile<TY, 3>(a, s);
+    case 4: return launch_tile<TY, 4>(a, s);
+    case 5: return launch_tile<TY, 5>(a, s);
+    default: return launch_tile<TY, 6>(a, s);
   }
 }
 
@@ -447,7 +414,7 @@ hipError_t launch_q8_matmul(const Q8MatmulArgs &a, hipStream_t s) {
 
 hipError_t launch_q8_linear(const Q8RowsArgs &q, const Q8MatmulArgs &a, hipStream_t s) {
   // each workgroup makes all codes: worth it while they are few (and fit the LDS)
-  if (few(a) && a.T <= 4 && a.T * q8_padded(a.cols) <= 32768 && q.type == a.type)
+  if (q8_few(a.T, a.rows) && a.T <= 4 && a.T * q8_padded(a.cols) <= 32768 && q.type == a.type)
     return a.type == kF32    ? launch_few_linear<kF32>(q, a, s)
            : a.type == kBf16 ? launch_few_linear<kBf16>(q, a, s)
                              : launch_few_linear<kF16>(q, a, s);

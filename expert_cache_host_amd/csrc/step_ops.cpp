@@ -83,7 +83,8 @@ moe_status moe_q8_matmul(const void *x, int64_t x_stride, const float *x_scales,
     return einval("a pointer is not aligned to its element type");
   moe::Q8MatmulArgs a{};
   a.x = (const int8_t *)x, a.w = (const int8_t *)w, a.x_scales = x_scales, a.w_scales = w_scales, a.out = out;
-  a.ldx = x_stride, a.ldw = w_stride, a.ldo = out_stride, a.type = type;
+  a.ldx = n_tokens > 1 ? x_stride : moe::q8_padded(cols), a.ldw = rows > 1 ? w_stride : moe::q8_padded(cols);
+  a.ldo = out_stride, a.type = type;
   a.T = n_tokens, a.rows = rows, a.cols = cols;
   return done(moe::launch_q8_matmul(a, stream));
 }
@@ -117,7 +118,7 @@ moe_status moe_q8_linear(const void *x, int32_t type, int64_t x_stride, int32_t 
   q.ldx = x_stride, q.ldc = padded, q.type = type, q.n = n_tokens, q.cols = cols;
   moe::Q8MatmulArgs a{};
   a.x = q.codes, a.w = (const int8_t *)w, a.x_scales = q.scales, a.w_scales = w_scales, a.out = out;
-  a.ldx = padded, a.ldw = w_stride, a.ldo = out_stride, a.type = out_type;
+  a.ldx = padded, a.ldw = rows > 1 ? w_stride : padded, a.ldo = out_stride, a.type = out_type;
   a.T = n_tokens, a.rows = rows, a.cols = cols;
   return done(moe::launch_q8_linear(q, a, stream));
 }
