@@ -276,7 +276,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
       v2 = fmaxf(fmaxf(v2, o2), fminf(v1, o1));
       v1 = fmaxf(v1, o1);
     }
-    const float v = a.best == 2 ? (v2 > kLow ? v1 + v2 : kLow) : v1;
+    // (a pair's sum may pass float32: only a group without a pair is minus infinity)
+    const float v = a.best == 2 ? (v2 > kLow ? fmaxf(v1 + v2, -3.40282347e38f) : kLow) : v1;
     int rank = 0;
     for (int o = 0; o < a.groups; ++o) {
       const float x = lane_of(v, o * per);

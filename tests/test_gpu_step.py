@@ -287,6 +287,30 @@ def test_route_groups_whose_pairs_cancel(size):
         check_route(z, bias, k=4, score=score, groups=groups, keep=3, best=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_whose_pairs_pass_float32(score):
+    """A bias near the lowest float32, a mask that many use: pairs sum to less than float32 holds, yet their groups come
+    before one with a single expert left."""
+    inf, low = float("inf"), -3.4028234e38
+    t = lambda v: torch.tensor(v, device="cuda")  # noqa: E731
+    for b in ([0.0, 0.0, -3.4e38, -3.4e38], [0.0, 0.0, low, low], [0.0, 0.0, -1.8e38, -1.8e38]):
+        idx, _ = check_route(t([[0.0, -inf, 0.0, 0.0]]), t(b), k=1, score=score, groups=2, keep=1, best=2)
+        assert idx.tolist() == [[2]]
+    # groups of such pairs among themselves, beside ordinary and excluded ones
+    g = gen(12)
+    for k, groups, keep in ((2, 8, 3), (9, 16, 5)):
+        z = rnd(g, 60, 64)
+        z[torch.rand(60, 64, generator=g, device="cuda") < 0.3] = -inf
+        bias = rnd(g, 64, scale=0.2)
+        bias[8:40] = low
+        bias[16:24] = -1.75e38
+        bias[40:48] = -inf
+        bias[50] = inf
+        check_route(z, bias, k=k, score=score, groups=groups, keep=keep, best=2)
+        check_route(z, bias, k=k, score=score, groups=groups, keep=keep, best=1)
+        check_route(z, -bias, k=k, score=score, groups=groups, keep=keep, best=2)
+
+
 @pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_and_close_values(groups, keep, score):
