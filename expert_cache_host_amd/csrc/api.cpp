@@ -679,11 +679,15 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
   // a rule's kernel writes the routing to the device and to page-locked memory;
   // the host waits for it as for a prompt batch's
   const auto route_by_rule = [&]() {
+    KTime kt(c, MOE_K_TOPK, st);
     moe::RouteArgs a = moe::route_args(*rule);
     a.z = ws.z, a.bias = select_bias, a.idx = (int32_t *)ws.idx, a.w = (float *)ws.w;
     a.idx2 = (int32_t *)c->h_idx.p, a.w2 = (float *)c->h_w.p;
     a.ldz = E, a.type = moe::kF32, a.T = T, a.E = E;
-    HIPCHK(moe::launch_route(a, st));
+    hipEvent_t start, stop;
+    moe::take_launch_events(start, stop);
+    HIPCHK(moe::launch_route(a, st, start, stop));
+    kt.end(4.0 * ((double)T * E + 4.0 * T * k + (select_bias ? E : 0)));
   };
   const bool publish = dec && !rule;  // decode calls select on the host from published logits
   if (dec) {
@@ -705,11 +709,16 @@ moe_status forward_impl(moe_cache *c, int32_t layer, const float *x, int32_t T,
                               router_x ? (float *)c->h_x.p : nullptr,
                               publish ? (unsigned long long *)c->h_z : nullptr, c->z_seq));
     kt.end(4.0 * ((double)E * d + (double)T * d * 2 + (double)T * E + (router_bias ? E : 0)));
-    if (rule) route_by_rule();
-    KTime kt2(c, MOE_K_TOPK, st);
-    HIPCHK(rule ? moe::launch_decode_buckets(T, a, st)
-                : moe::launch_topk_decode((const float *)ws.z, T, E, a, st));
-    kt2.end(4.0 * ((double)T * E + 4.0 * T * k));
+    if (rule) {
+      route_by_rule();
+      KTime kt2(c, MOE_K_REMAP, st);
+      HIPCHK(moe::launch_decode_buckets(T, a, st));
+      kt2.end((double)(T * k + (ns > 0 ? T : 0)) * 8);
+    } else {
+      KTime kt2(c, MOE_K_TOPK, st);
+      HIPCHK(moe::launch_topk_decode((const float *)ws.z, T, E, a, st));
+      kt2.end(4.0 * ((double)T * E + 4.0 * T * k));
+    }
   } else {
     {
       KTime kt(c, MOE_K_ROUTER, st);

@@ -1,6 +1,7 @@
 // Device helpers of the decoder-layer operators: loads and stores of the three
 // element types through float32, and the packed batch's row lookup.
 #pragma once
+#include <hip/hip_ext.h>
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -16,6 +17,16 @@ template <class... P>
 hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, std::common_type_t<P>... args) {
   void *p[] = {(void *)&args...};
   const hipError_t e = hipLaunchKernel((const void *)kernel, grid, block, p, 0, s);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
+// The same with events recorded at the kernel's start and end.
+template <class... P>
+hipError_t launch_timed(void (*kernel)(P...), dim3 grid, dim3 block, hipStream_t s, hipEvent_t start, hipEvent_t stop,
+                        std::common_type_t<P>... args) {
+  void *p[] = {(void *)&args...};
+  const hipError_t e = hipExtLaunchKernel((const void *)kernel, grid, block, p, 0, s, start, stop, 0);
   if (e != hipSuccess) (void)hipGetLastError();
   return e;
 }

@@ -37,11 +37,16 @@ bool launch_events_pending() {
   return p;
 }
 
+void take_launch_events(hipEvent_t &start, hipEvent_t &stop) {
+  start = t_ev_start, stop = t_ev_stop;
+  t_ev_start = t_ev_stop = nullptr;
+}
+
 template <typename... KArgs, typename... Args>
 static void launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 blk, size_t lds, hipStream_t s,
                      Args... args) {
-  hipEvent_t a = t_ev_start, b = t_ev_stop;
-  t_ev_start = t_ev_stop = nullptr;
+  hipEvent_t a, b;
+  take_launch_events(a, b);
   hipExtLaunchKernelGGL(kernel, grid, blk, (uint32_t)lds, s, a, b, 0u, static_cast<KArgs>(args)...);
 }
 

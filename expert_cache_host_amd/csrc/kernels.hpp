@@ -14,6 +14,8 @@ void set_launch_events(hipEvent_t start, hipEvent_t stop);
 // True when events set by set_launch_events were not taken by a launch (the
 // launch function returned without launching); clears them either way.
 bool launch_events_pending();
+// Takes them for a launch made elsewhere (null where none are set).
+void take_launch_events(hipEvent_t &start, hipEvent_t &stop);
 
 
 // Expert -> slot table of one stage, passed by value as a kernel argument so

@@ -390,12 +390,13 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(8))
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t s) {
+hipError_t launch_route(const RouteArgs &a, hipStream_t s, hipEvent_t start, hipEvent_t stop) {
   auto *k = a.E <= 64    ? route_kernel<1, 1>
             : a.E <= 128 ? route_kernel<2, 1>
             : a.E <= 256 ? route_kernel<4, 1>
                          : route_kernel<4, 2>;
-  return launch(k, dim3((a.T + kWaves - 1) / kWaves), dim3(64 * kWaves), s, a);
+  const dim3 grid((a.T + kWaves - 1) / kWaves), block(64 * kWaves);
+  return start ? launch_timed(k, grid, block, s, start, stop, a) : launch(k, grid, block, s, a);
 }
 
 }  // namespace moe

@@ -44,7 +44,8 @@ struct RouteArgs {
   int type, T, E, k, sigmoid, groups, keep, best, renorm;
   float scale;
 };
-hipError_t launch_route(const RouteArgs &a, hipStream_t s);
+// start, stop: events recorded at the kernel's start and end, or null.
+hipError_t launch_route(const RouteArgs &a, hipStream_t s, hipEvent_t start = nullptr, hipEvent_t stop = nullptr);
 
 struct SampleArgs {
   const void *z;   // [T] rows of V logits, stride ldz

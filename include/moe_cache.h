@@ -264,8 +264,8 @@ moe_status moe_cache_set_timing(moe_cache *c, int32_t on);
 
 /* Kernels timed one launch at a time when timing is on. */
 #define MOE_K_ROUTER 0  /* router logits */
-#define MOE_K_TOPK 1    /* top-k + softmax gating weights */
-#define MOE_K_REMAP 2   /* expert -> slot remap and bucketing */
+#define MOE_K_TOPK 1    /* top-k + softmax gating weights, or a routing rule's kernel */
+#define MOE_K_REMAP 2   /* expert -> slot remap and bucketing (of decode calls only where a rule routes) */
 #define MOE_K_GATEUP 3  /* Q4 gate/up projections + SwiGLU */
 #define MOE_K_DOWN 4    /* Q4 down projection */
 #define MOE_K_COMBINE 5 /* weighted combine */
@@ -674,8 +674,9 @@ moe_status moe_route(const void *logits, int32_t type, int64_t stride, const flo
  * `rule` selects from the router's logits (router_bias is part of the logits, select_bias,
  * device float32 [n_experts] or NULL, of the selection alone).  rule->top_k must be the
  * cache's top_k; the cache's norm_topk is not looked at.  On decode calls the host waits
- * for the rule's kernel instead of selecting from published logits; that kernel is not
- * among the timed ones.  Everything else is as there. */
+ * for the rule's kernel instead of selecting from published logits.  That kernel is timed
+ * as MOE_K_TOPK, the bucketing of decode calls, a launch of its own, as MOE_K_REMAP.
+ * Everything else is as there. */
 moe_status moe_layer_forward_ruled(moe_cache *c, int32_t layer, const float *x, int32_t n_tokens,
                                    const float *router_w, const float *router_bias, const moe_route_rule *rule,
                                    const float *select_bias, float *out, moe_stream_t stream);

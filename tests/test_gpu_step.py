@@ -469,6 +469,48 @@ def test_layer_with_a_rule_timed_and_on_another_stream(T):
     c.close()
 
 
+@pytest.mark.parametrize("T", [1, 3, 6])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_layer_with_a_rule_kernel_stats(T, with_bias):
+    """The rule's kernel counts as the top-k, with the bytes it moves; the buckets of decode calls as the remap."""
+    wl = synth.WORKLOADS["tiny"]
+    E, k = wl.n_experts, wl.top_k
+    c = m.MoECache(1, E, E, wl.d_model, wl.d_ff, synth.gen_experts(wl, 0), top_k=k)
+    g = gen(T)
+    x, w_r = rnd(g, T, wl.d_model), rnd(g, E, wl.d_model, scale=0.1)
+    bias = rnd(g, E, scale=0.1) if with_bias else None
+    r = m.RoutingRule(k, "sigmoid")
+    c.forward(0, x, w_r, rule=r, select_bias=bias)
+    c.sync()
+    for plain in (False, True):
+        c.set_timing(True)
+        c.reset_stats()
+        for _ in range(5):
+            if plain:
+                c.forward(0, x, w_r)
+            else:
+                c.forward(0, x, w_r, rule=r, select_bias=bias)
+        c.sync()
+        ks = c.kernel_stats()
+        n, sec, by = ks["topk"]
+        # logits, then ids and weights twice: on the device and in page-locked memory
+        assert (n, by) == (5, 5 * 4 * (T * E + 4 * T * k + (E if with_bias and not plain else 0))) and sec > 0
+        n, sec, by = ks["remap"]
+        if T <= 4:  # the plain path's top-k lists the buckets itself
+            assert (n, by) == ((0, 0) if plain else (5, 5 * 8 * T * k)) and (sec > 0) == (not plain)
+        else:
+            assert n >= 5 and by == n * 8 * T * k and sec > 0
+        c.set_timing(False)
+    # a rule alone, which times nothing, between timed calls
+    c.set_timing(True)
+    c.reset_stats()
+    m.route_experts(x @ w_r.t(), r, bias)
+    c.forward(0, x, w_r, rule=r)
+    c.sync()
+    assert c.kernel_stats()["topk"][0] == 1
+    c.close()
+
+
 def test_layer_rule_refusals():
     wl = synth.WORKLOADS["tiny"]
     c = m.MoECache(1, wl.n_experts, 4, wl.d_model, wl.d_ff, synth.gen_experts(wl, 0), top_k=wl.top_k)
