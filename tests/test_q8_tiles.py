@@ -1,10 +1,13 @@
 """The tiles of the 8-bit product without a GPU (tests/sanitize/q8_loads_driver.cpp):
-where their loads go, under the address and undefined-behaviour sanitizers."""
+where their loads go, under the address and undefined-behaviour sanitizers, and which
+product takes which."""
 import os
 import shutil
 import subprocess
 
 import pytest
+
+from q8_tile_cases import CASES
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not found")
@@ -30,3 +33,17 @@ def driver(tmp_path_factory):
 def test_loads_stay_in_their_buffers(driver):
     """The scalar offset alone lies in the buffer for every load of every tile, and each lane reads its own element."""
     assert driver()[-1] == "ok"
+
+
+def test_cases_reach_every_tile(driver):
+    """The products of test_gpu_q8_tiles.py go to the tiles they are meant for, with fewer steps than are under way, as
+    many, one more and more than twice as many: a new choice of tiles that loses one shows here."""
+    chosen = [tuple(map(int, line.split())) for line in driver(*(v for c in CASES for v in c[1:]))]
+    seen = set()
+    for (tile, T, rows, cols), (got, ahead) in zip(CASES, chosen):
+        assert got == tile, (T, rows, cols)
+        steps = -(-cols // 128)
+        seen.add((tile, "fewer" if steps < ahead else "as many" if steps == ahead else "one more" if steps == ahead + 1
+                  else "more"))
+        assert steps <= ahead + 1 or steps > 2 * ahead
+    assert seen == {(t, n) for t in range(7) for n in ("fewer", "as many", "one more", "more")}
