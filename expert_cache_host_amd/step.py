@@ -183,8 +183,11 @@ class RoutingRule:
             raise ValueError("score must be 'softmax' or 'sigmoid'")
         if not 1 <= top_k <= 64:
             raise ValueError("top_k must be in [1, 64]")
-        self._c = RouteRule(top_k, _SCORES[score], groups, groups if keep_groups is None else keep_groups, group_best,
-                            1 if renorm else 0, scale)
+        keep = groups if keep_groups is None else keep_groups
+        for name, v in (("keep_groups", keep), ("groups", groups), ("group_best", group_best)):
+            if not -_I32 <= v <= _I32:  # (their ranges are checked with the experts they are for)
+                raise ValueError(f"{name} must be a 32-bit number")
+        self._c = RouteRule(top_k, _SCORES[score], groups, keep, group_best, 1 if renorm else 0, scale)
         self._cp = ctypes.pointer(self._c)
 
     @property

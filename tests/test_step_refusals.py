@@ -150,3 +150,11 @@ def test_tensors_must_be_on_the_gpu():
             m.RoutingRule(k)
     with pytest.raises(AttributeError):
         m.RoutingRule(2).top_k = 3
+
+
+@pytest.mark.parametrize("kw", [dict(groups=2 ** 32 + 1), dict(keep_groups=2 ** 32 + 1), dict(group_best=2 ** 32 + 1),
+                                dict(groups=-2 ** 32 + 1), dict(groups=8, keep_groups=2 ** 33 + 4), dict(group_best=2 ** 33)])
+def test_rule_counts_that_pass_32_bits(kw):
+    """Not taken for their low 32 bits, which would be a rule of their own."""
+    with pytest.raises(ValueError, match=next(reversed(kw))):
+        m.RoutingRule(2, **kw)
