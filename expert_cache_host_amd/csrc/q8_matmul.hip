@@ -4,16 +4,17 @@
 // Many tokens (q8_tile_kernel): a workgroup takes a tile of rows by tokens, 128
 // columns a step, both operands loaded straight into LDS, S steps under way.  Large
 // products are bound by the card's power (the clock falls to about 1.5 GHz while the
-// matrix cores are busy): 4096 x 6144 x 16384 in 349 us, 2360 TOP/s (a library's
-// product of these sizes without scales: 395 us); 8192^3 in 440 us, 2500 TOP/s (the
-// library 440).  Small ones are bound by what a CU can load next to its reads, about
-// 50 GB/s: 512 x 6144 x 10240 in 37 us.
+// matrix cores are busy, 0.85 of the CUs' cycles): 4096 x 6144 x 16384 in 345 us, 2390
+// TOP/s (a library's product of these sizes without scales: 395 us); 8192^3 in 440 us,
+// 2500 TOP/s (the library 440).  Middle ones keep no unit busy throughout: 512 x 6144 x
+// 10240 takes 37 us, a tile of 160 x 128 and one wave a SIMD on each CU, matrix cores
+// 0.46 of its cycles, LDS reads 0.28, its loads coming in at about 50 GB/s.
 // What mattered: fragments read a step ahead of their products and loads a step and a
 // quarter ahead of their fragments (8192^3: 567 -> 472 us); pieces laid out so that
 // reads meet no bank conflict; a step's loads spread over it, since LDS takes their
 // writes between the reads (491 -> 441 us, and 84 -> 67 us for 80 tiles of 6144
 // columns, one each on 80 CUs).
-// Few tokens: memory.  24 x 6144 x 10240 in 14.3 us (4.4 TB/s of weights), one token
+// Few tokens: memory.  24 x 6144 x 10240 in 14 us (4.5 TB/s of weights), one token
 // by 2816 x 8192, its codes made on the way, in 8.1.
 #include "q8_code.hpp"
 #include "q8_tiles.hpp"

@@ -1,8 +1,9 @@
 // Rows in 8-bit integers: s = max|x| / 127 (float32), code = rint(x / s).
 //
-// Bound by memory (4096 x 6144 bfloat16: 21 us, 3.6 TB/s; 512 x 6144: 5.7, latency): a
-// row is read once into registers, its maximum taken, and coded from there (what a
-// thread cannot hold is read a second time, out of the cache).
+// A row is read once into registers, its maximum taken, and coded from there (what a
+// thread cannot hold is read a second time, out of the cache).  4096 x 6144 bfloat16:
+// 22 us, 3.4 TB/s, bound by vector instructions, 24 an element (the exact codes), which
+// take 0.76 of the CUs' cycles; 512 x 6144: 5.6, latency.
 #include "q8_code.hpp"
 #include "step_ops.hpp"
 

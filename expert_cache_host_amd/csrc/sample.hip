@@ -12,9 +12,13 @@
 //
 // A row of up to kShortRow tokens takes one workgroup and one launch.  A longer one
 // takes four: its largest logit, its bins and the gathering each over many workgroups,
-// the rest in one.  Measured: 36 rows of 645 in 11 us, one of 131072 in 24 (the launches
-// one after the other), 64 of 262144 float32 in 68 (13 + 23 + 24 + 9: the logits at 5.2
-// TB/s, the bins' binary64 arithmetic, the logits again, the sorting).
+// the rest in one.  Measured: 36 rows of 645 in 11 us; one of 131072 in 24 (3 + 5 + 10 +
+// 7: every workgroup of the gathering, and the last launch again, reads the 24 KB of
+// bins, sums them up and searches the borders, which takes longer than its tokens do);
+// 64 of 262144 float32 in 68 (13 + 23 + 24 + 9).  There the first pass reads the logits at
+// 5.2 TB/s; in the second vector instructions, 28 a token, take 0.68 of the CUs' cycles
+// and LDS 0.41, half of it bank conflicts; in the third they take 0.39 and 0.13, the rest
+// is the borders' search and its waiting.  Rows settled by digits: 0.4 to 2.5 ms.
 #include "device_types.hpp"
 #include "step_ops.hpp"
 
